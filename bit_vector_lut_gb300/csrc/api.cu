@@ -512,12 +512,12 @@ const char* vq3_version(void) {
 
 int vq3_bounds_check(unsigned* out, int n_out, int reset) {
 #ifdef VQ3_BOUNDS_CHECK
-  if (!out || n_out < 2 * VQ3_BOUNDS_FILES)
-    return report_error(VQ3_EINVAL, "bounds_check: out needs %d entries", 2 * VQ3_BOUNDS_FILES);
-  cudaError_t (*const rd[VQ3_BOUNDS_FILES])(unsigned*, bool) = {bounds_read_persistent, bounds_read_lowrank,
-                                                                 bounds_read_delta,      bounds_read_rotate,
-                                                                 bounds_read_prefill,    bounds_read_prefill_wide};
-  for (int f = 0; f < VQ3_BOUNDS_FILES; ++f) {
+  constexpr int kLeast = 12;  // the first six files, which every caller has room for
+  if (!out || n_out < kLeast) return report_error(VQ3_EINVAL, "bounds_check: out needs %d entries", kLeast);
+  cudaError_t (*const rd[VQ3_BOUNDS_FILES])(unsigned*, bool) = {
+      bounds_read_persistent,   bounds_read_lowrank, bounds_read_delta,     bounds_read_rotate, bounds_read_prefill,
+      bounds_read_prefill_wide, bounds_read_attn,    bounds_read_attn_wide, bounds_read_kvcache};
+  for (int f = 0; f < VQ3_BOUNDS_FILES && 2 * f + 1 < n_out; ++f) {
     const cudaError_t e = rd[f](out + 2 * f, reset != 0);
     if (e != cudaSuccess) return report_error(VQ3_ECUDA, "bounds_check: %s", cudaGetErrorString(e));
   }

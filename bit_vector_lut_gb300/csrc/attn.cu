@@ -1,0 +1,507 @@
+// Attention of a few query rows per request over a long cache (single tokens, short verify
+// steps), and the pass that combines the parts of a unit split between CTAs.
+//
+//   out[row] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j - max),  j < seen(row)
+//
+// in one pass over the keys with a running maximum and sum (FP32). The keys and values of a
+// request are read once for all rows of a key/value head: bound by the memory they are read
+// from. Every warp walks its own groups of 16 tokens with its own maximum, sum and output
+// and needs neither shared memory nor barriers until the end of a unit:
+//   S^T[16 tokens][8 rows] = K Q^T: the A operand of m16n8k16 is taken straight from global
+//     memory, 16 bytes a lane. Lane (g, t) of the MMA (g = lane / 4, t = lane % 4) reads
+//     d = 32 c + 8 t .. + 7 of tokens g and g + 8; the order of d inside a 32-wide chunk is
+//     permuted against the MMA's, the same way in Q.
+//   O^T[16 d][8 rows] += V^T P^T: lane (g, t) reads d = 64 c + 8 g .. + 7 of tokens 2t, 2t + 1,
+//     2t + 8, 2t + 9 (16 bytes each) and pairs neighbouring tokens with a byte permute; P^T is
+//     S^T's accumulator packed to 16 bits and transposed by movmatrix.
+// So the loads are whole 64- and 128-byte lines and the next group's keys and values load
+// while this group's products run.
+#include "attn_common.cuh"
+
+namespace vq3 {
+VQ3_BOUNDS_RECORD(attn)
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = kWarps * 16;  // tokens of a tile: one group of 16 per warp
+constexpr int kMinTiles = 2;        // fewest tiles per CTA
+
+// CTAs per SM: what registers allow (Q, O, and one group's K and V per thread).
+template <int D, int NR>
+constexpr int rows_occ() {
+  return D == 256 ? 2 : (D == 128 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 5 : 4));
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (AttnType<T>::kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// 16 bytes, read once: not kept in L1.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Query rows `row` of the request (packed) to its place in q, out and lse.
+struct RowPlace {
+  long long token;
+  int head;
+};
+__device__ __forceinline__ RowPlace row_place(const AttnArgs& a, int q0, int kv_head, int p) {
+  const int t = p / a.group;
+  return {(long long)(q0 + t), kv_head * a.group + (p - t * a.group)};
+}
+
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kRows = 8 * NR;
+  constexpr int kC = D / 32;  // K chunks of 32
+  constexpr int kV = D / 64;  // V chunks of 64
+  constexpr float kOff = AttnType<T>::kOff;
+  __shared__ long long s_sum[kWarps];
+  __shared__ AttnPos s_pos;
+  __shared__ __align__(16) float s_o[kWarps][kRows][D + 4];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+  attn_locate<kThreads>(a, kTile, kMinTiles, s_sum, &s_pos);
+  const AttnPos pos = s_pos;
+  AttnRec rec{};
+  AttnWalk w;
+  for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+    const int rows = w.q.n_new * a.group, base = w.j * kRows;
+    // Q: the B operand of S^T = K Q^T; row g of each block of 8
+    uint4 qf[NR][kC];
+    int lim[NR][2];  // keys that rows 2t and 2t + 1 of the block see
+    int low = 0x7fffffff;
+#pragma unroll
+    for (int b = 0; b < NR; ++b) {
+      const int p = base + b * 8 + g;
+      const bool live = p < rows;
+      const RowPlace rp = row_place(a, w.q.q0, w.h, live ? p : 0);
+      const T* src = static_cast<const T*>(a.q) + rp.token * a.q_token + rp.head * a.q_head + 8 * t;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        qf[b][c] = live && VQ3_IN(rp.token, a.tokens, 1) ? __ldg(reinterpret_cast<const uint4*>(src + 32 * c))
+                                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int pe = base + b * 8 + 2 * t + e;
+        // rows beyond the last are computed on zeros and not written: nothing to mask
+        lim[b][e] = pe < rows ? attn_seen(w.q, pe / a.group) : 0x7fffffff;
+      }
+    }
+    low = attn_seen(w.q, base / a.group);  // what the first row sees: no less than nothing is masked
+
+    float m[NR][2], l[NR][2];
+    float o[NR][D / 16][4];
+#pragma unroll
+    for (int b = 0; b < NR; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[b][e] = -INFINITY;
+        l[b][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[b][i][e] = 0.f;
+    }
+
+    const int first = w.t0 * kTile + warp * 16;
+    const int stop = w.t1 * kTile < w.end ? w.t1 * kTile : w.end;
+    // page of the group that starts at token x (16 tokens never straddle pages of 16 and more)
+    const auto page_of = [&](int x) -> int {
+      if (!a.table) return 0;
+      if (x >= stop) return -1;
+      const size_t at = (size_t)w.r * a.max_pages + (x >> a.page_shift);
+      return VQ3_IN(at, (size_t)a.requests * a.max_pages, 2) ? __ldg(a.table + at) : -1;
+    };
+    const T* const kh = static_cast<const T*>(a.k) + (long long)w.h * a.k_head;
+    const T* const vh = static_cast<const T*>(a.v) + (long long)w.h * a.v_head;
+    // A page number outside the cache reads as zeros; so do tokens the request does not have.
+    const auto bad = [&](int page) { return a.table && (unsigned)page >= (unsigned)a.n_pages; };
+    uint4 kf[kC][2], vf[kV][4];
+    const auto load_k = [&](int x, int page) {
+      const long long in = a.table ? (long long)(x & ((1 << a.page_shift) - 1)) : (long long)w.q.q0 + x;
+      const T* p = kh + (long long)(a.table ? page : 0) * a.k_page + 8 * t;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tok = g + 8 * e;
+        const bool ok = x + tok < stop && !bad(page);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          kf[c][e] = ok ? ldg_stream(p + (in + tok) * a.k_token + 32 * c) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    const auto load_v = [&](int x, int page) {
+      const long long in = a.table ? (long long)(x & ((1 << a.page_shift) - 1)) : (long long)w.q.q0 + x;
+      const T* p = vh + (long long)(a.table ? page : 0) * a.v_page + 8 * g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 2 * t + (e & 1) + 8 * (e >> 1);
+        const bool ok = x + tok < stop && !bad(page);
+#pragma unroll
+        for (int c = 0; c < kV; ++c)
+          vf[c][e] = ok ? ldg_stream(p + (in + tok) * a.v_token + 64 * c) : make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    int page = page_of(first), next_page = page_of(first + kTile);
+    if (first < stop) {
+      load_k(first, page);
+      load_v(first, page);
+    }
+    for (int x = first; x < stop; x += kTile) {
+      float s[NR][4];
+#pragma unroll
+      for (int b = 0; b < NR; ++b) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[b][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          mma16816<T>(s[b], kf[c][0].x, kf[c][1].x, kf[c][0].y, kf[c][1].y, qf[b][c].x, qf[b][c].y);
+          mma16816<T>(s[b], kf[c][0].z, kf[c][1].z, kf[c][0].w, kf[c][1].w, qf[b][c].z, qf[b][c].w);
+        }
+      }
+      const int xn = x + kTile;
+      page = next_page;
+      if (xn < stop) load_k(xn, page);
+      next_page = page_of(xn + kTile);
+
+      bool raise = false;
+#pragma unroll
+      for (int b = 0; b < NR; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[b][e] *= a.scale_log2;
+          if (x + 16 > low || x + 16 > stop) {
+            const int tok = x + g + 8 * (e >> 1);
+            if (tok >= lim[b][e & 1] || tok >= stop) s[b][e] = -INFINITY;
+          }
+          raise |= s[b][e] > m[b][e & 1] + kLag;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int b = 0; b < NR; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[b][e], s[b][e + 2]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            mx = fmaxf(mx, m[b][e]);
+            const float f = m[b][e] == mx ? 1.f : ex2(m[b][e] - mx);  // equal infinities: nothing to rescale
+            m[b][e] = mx;
+            l[b][e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[b][i][e] *= f;
+              o[b][i][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t pb[NR][2];
+#pragma unroll
+      for (int b = 0; b < NR; ++b) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mm = m[b][e & 1] == -INFINITY ? 0.f : m[b][e & 1];
+          p[e] = ex2(s[b][e] - mm + kOff);
+          l[b][e & 1] += p[e];
+        }
+        pb[b][0] = transpose8x8(pack2<T>(p[0], p[1]));
+        pb[b][1] = transpose8x8(pack2<T>(p[2], p[3]));
+      }
+#pragma unroll
+      for (int c = 0; c < kV; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x0 = word(vf[c][0], i), x1 = word(vf[c][1], i), x2 = word(vf[c][2], i), x3 = word(vf[c][3], i);
+          const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+          const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+          for (int b = 0; b < NR; ++b) mma16816<T>(o[b][4 * c + i], a0, a1, a2, a3, pb[b][0], pb[b][1]);
+        }
+      if (xn < stop) load_v(xn, page);
+    }
+
+    // the warps' parts of this unit, side by side in shared memory
+#pragma unroll
+    for (int b = 0; b < NR; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        const int row = b * 8 + 2 * t + e;
+        if (g == 0) {
+          s_m[warp][row] = m[b][e];
+          s_l[warp][row] = l[b][e];
+        }
+#pragma unroll
+        for (int c = 0; c < kV; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d = 64 * c + 8 * g + 2 * i;
+            *reinterpret_cast<float2*>(&s_o[warp][row][d]) = make_float2(o[b][4 * c + i][e], o[b][4 * c + i][e + 2]);
+          }
+      }
+    __syncthreads();
+    const bool whole = w.whole();
+    const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+    if (!whole) {
+      if (w.t0 > 0) {
+        rec.flags |= kRecHead | (w.t1 == w.n ? kRecEnd : 0);
+      } else {
+        rec.flags |= kRecTail;
+        rec.q0 = w.q.q0;
+        rec.rows = rows;
+        rec.base = base;
+        rec.head = w.h;
+      }
+    }
+    constexpr int kLanes = D / 4;  // threads of a row, four columns each
+    for (int row = tid / kLanes; row < kRows; row += kThreads / kLanes) {
+      const int d = (tid % kLanes) * 4;
+      if (base + row >= rows) break;
+      float mx = s_m[0][row];
+#pragma unroll
+      for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][row]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float f = s_m[v][row] == mx ? 1.f : ex2(s_m[v][row] - mx);
+        const float4 x = *reinterpret_cast<const float4*>(&s_o[v][row][d]);
+        sum += f * s_l[v][row];
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+      if (whole) {
+        const RowPlace rp = row_place(a, w.q.q0, w.h, base + row);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (VQ3_IN(rp.token, a.tokens, 3)) {
+          uint2 y;
+          y.x = pack2<T>(acc.x * inv, acc.y * inv);
+          y.y = pack2<T>(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + d) = y;
+          if (a.lse && d == 0)
+            a.lse[rp.token * a.heads + rp.head] = sum == 0.f ? -INFINITY : (mx - kOff + log2f(sum)) * 0.6931471805599453f;
+        }
+      } else {
+        const size_t at = (size_t)slot * kRows + row;
+        if (VQ3_IN(at, (size_t)2 * gridDim.x * kRows, 4)) {
+          __stcg(reinterpret_cast<float4*>(a.part + at * D + d), acc);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + 2 * at), make_float2(mx, sum));
+        }
+      }
+    }
+    __syncthreads();  // before the next unit's parts
+  }
+  if (tid == 0) a.rec[blockIdx.x] = rec;
+}
+
+// ---------------------------------------------------------------- combining pass
+//
+// Block (c, y) takes the unit that CTA c began and did not end, if there is one; its parts
+// are slot 2c + 1 and then slot 2c' of the CTAs behind, up to the one that ends it. Rows are
+// dealt out to the blocks y. With few parts a warp takes a row by itself, with many the
+// block's warps share a row's parts (each a fixed subset, summed in a fixed order).
+constexpr int kCWarps = 8;
+constexpr int kMaxGrid = 2048;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCWarps * 32) attn_combine_kernel(const __grid_constant__ AttnArgs a, int grid,
+                                                                    int slot_rows) {
+  __shared__ int s_parts[kMaxGrid];
+  __shared__ int s_n;
+  __shared__ float s_m[kCWarps], s_l[kCWarps];
+  __shared__ __align__(16) float s_o[kCWarps][D];
+  constexpr int kPer = D / 32;  // columns of a lane
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel has ended
+  if (c == 0 && blockIdx.y == 0) {
+    // the workspace's status word: whether a wait of any CTA gave up
+    int failed = 0;
+    for (int i = tid; i < grid; i += kCWarps * 32) failed |= __ldcg(&a.rec[i].flags) & kRecFailed;
+    failed = __syncthreads_or(failed);
+    if (tid == 0) *a.status = failed ? 3 : 0;
+  }
+  if (!(__ldcg(&a.rec[c].flags) & kRecTail)) return;
+  if (warp == 0) {
+    // the slots of the unit, in CTA order
+    int n = 1;
+    if (lane == 0) s_parts[0] = 2 * c + 1;
+    for (int i0 = c + 1; i0 < grid; i0 += 32) {
+      const int i = i0 + lane;
+      const int f = i < grid ? __ldcg(&a.rec[i].flags) : 0;
+      const unsigned ends = __ballot_sync(0xffffffffu, (f & (kRecHead | kRecEnd)) == (kRecHead | kRecEnd));
+      const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;
+      const unsigned has = __ballot_sync(0xffffffffu, f & kRecHead) & upto;
+      if (has >> lane & 1) s_parts[n + __popc(has & ((1u << lane) - 1u))] = 2 * i;
+      n += __popc(has);
+      if (ends) break;
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int n = s_n;
+  const AttnRec rec = a.rec[c];
+  const bool shared = n > 8;
+  const int n_warps = shared ? 1 : kCWarps;
+  for (int row = blockIdx.y * n_warps + (shared ? 0 : warp); row < slot_rows; row += gridDim.y * n_warps) {
+    const int p = attn_packed_row(row, rec.base, rec.rows, a.block_rows, a.block_used);
+    if (p < 0) continue;  // the same for all warps that share the row
+    float mx = -INFINITY, sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    const int step = shared ? kCWarps : 1;
+    for (int i = shared ? warp : 0; i < n; i += step) {
+      const size_t at = (size_t)s_parts[i] * slot_rows + row;
+      mx = fmaxf(mx, __ldcg(a.part_ml + 2 * at));
+    }
+#pragma unroll 4
+    for (int i = shared ? warp : 0; i < n; i += step) {
+      const size_t at = (size_t)s_parts[i] * slot_rows + row;
+      if (!VQ3_IN(at, (size_t)2 * grid * slot_rows, 5)) continue;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * at));
+      const float f = ml.x == mx ? 1.f : ex2(ml.x - mx);
+      sum += f * ml.y;
+      const float* src = a.part + at * D + lane * kPer;
+      if constexpr (kPer == 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        acc[0] += f * x.x;
+        acc[1] += f * x.y;
+      } else {
+#pragma unroll
+        for (int v = 0; v < kPer / 4; ++v) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 4 * v));
+          acc[4 * v] += f * x.x;
+          acc[4 * v + 1] += f * x.y;
+          acc[4 * v + 2] += f * x.z;
+          acc[4 * v + 3] += f * x.w;
+        }
+      }
+    }
+    if (shared) {
+      __syncthreads();  // the previous row's sums have been read
+      if (lane == 0) {
+        s_m[warp] = mx;
+        s_l[warp] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i];
+      __syncthreads();
+      if (warp) continue;
+      mx = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < kCWarps; ++v) mx = fmaxf(mx, s_m[v]);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int v = 0; v < kCWarps; ++v) {
+        const float f = s_m[v] == mx ? 1.f : ex2(s_m[v] - mx);
+        sum += f * s_l[v];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += f * s_o[v][lane * kPer + i];
+      }
+    }
+    const RowPlace rp = row_place(a, rec.q0, rec.head, p);
+    if (!VQ3_IN(rp.token, a.tokens, 6)) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T* dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + lane * kPer;
+    uint32_t y[kPer / 2];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) y[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if constexpr (kPer == 2)
+      *reinterpret_cast<uint32_t*>(dst) = y[0];
+    else if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (a.lse && lane == 0)
+      a.lse[rp.token * a.heads + rp.head] =
+          sum == 0.f ? -INFINITY : (mx - AttnType<T>::kOff + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+template <typename T, int D, int NR>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
+  const int grid = rows_occ<D, NR>() * device_sm_count();
+  attn_rows_kernel<T, D, NR><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_rows_t(const AttnArgs& a, int d, int nr, cudaStream_t st) {
+  if (d == 64) return nr == 1 ? launch_rows<T, 64, 1>(a, st) : launch_rows<T, 64, 2>(a, st);
+  if (d == 128) return nr == 1 ? launch_rows<T, 128, 1>(a, st) : launch_rows<T, 128, 2>(a, st);
+  return launch_rows<T, 256, 1>(a, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_combine(const AttnArgs& a, int grid, int slot_rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  const int y = slot_rows / kCWarps < 1 ? 1 : (slot_rows / kCWarps > 8 ? 8 : slot_rows / kCWarps);
+  cfg.gridDim = dim3(grid, y);
+  cfg.blockDim = dim3(kCWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the attention kernel
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, grid, slot_rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_combine_t(const AttnArgs& a, int d, int grid, int slot_rows, cudaStream_t st) {
+  if (d == 64) return launch_combine<T, 64>(a, grid, slot_rows, st);
+  if (d == 128) return launch_combine<T, 128>(a, grid, slot_rows, st);
+  return launch_combine<T, 256>(a, grid, slot_rows, st);
+}
+
+}  // namespace
+
+int attn_rows_limit(int head_dim) { return head_dim == 256 ? 8 : 16; }
+
+int attn_rows_grid(int head_dim, int rows) {
+  const bool one = rows <= 8;
+  const int occ = head_dim == 256   ? rows_occ<256, 1>()
+                  : head_dim == 128 ? (one ? rows_occ<128, 1>() : rows_occ<128, 2>())
+                                    : (one ? rows_occ<64, 1>() : rows_occ<64, 2>());
+  const int g = occ * device_sm_count();
+  return g > kMaxGrid ? kMaxGrid : g;
+}
+
+cudaError_t launch_attn_rows(const AttnArgs& a, int head_dim, bool bf16, int nr, cudaStream_t st) {
+  return bf16 ? launch_rows_t<__nv_bfloat16>(a, head_dim, nr, st) : launch_rows_t<__half>(a, head_dim, nr, st);
+}
+
+cudaError_t launch_attn_combine(const AttnArgs& a, int head_dim, bool bf16, int grid, int slot_rows,
+                                cudaStream_t st) {
+  return bf16 ? launch_combine_t<__nv_bfloat16>(a, head_dim, grid, slot_rows, st)
+              : launch_combine_t<__half>(a, head_dim, grid, slot_rows, st);
+}
+
+}  // namespace vq3

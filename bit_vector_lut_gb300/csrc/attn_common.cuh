@@ -1,0 +1,299 @@
+// What the two attention kernels and their combining pass share: arguments, the row
+// packing of grouped heads, and the division of the work between CTAs.
+//
+// A unit is one request, one key/value head and up to `unit_rows` packed query rows; the
+// rows of a key/value head are (new token, query head of its group), row p = token p / G,
+// query head p % G, so the G heads of a group share every key and value that is read. A
+// unit's keys [0, end) are walked in tiles of kv_tile; end is what its last row sees.
+// All tiles of all units, laid end to end (request, key/value head, row block, tile), are
+// cut into equal contiguous ranges, one per CTA. A CTA that holds all of a unit writes its
+// output; otherwise it leaves (max, sum, unnormalised output) in a slot of its own, at most
+// two per CTA: slot 2c for a unit that an earlier CTA began, slot 2c + 1 for one that it
+// begins and does not end. The combining pass sums a unit's slots in CTA order, so results
+// do not depend on timing.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "vq3_internal.h"
+
+namespace vq3 {
+
+// Per-CTA record of what it left in its slots.
+struct AttnRec {
+  int flags;                 // kRec*
+  int q0, rows, base, head;  // of the unit it begins in slot 2c + 1: first query row, packed rows
+                             // of the request, first packed row of the unit, key/value head
+  int pad[3];
+};
+constexpr int kRecHead = 1;     // slot 2c holds a part of a unit that an earlier CTA began
+constexpr int kRecEnd = 2;      // and the unit ends there
+constexpr int kRecTail = 4;     // slot 2c + 1 holds the first part of a unit
+constexpr int kRecFailed = 8;   // a bounded wait of this CTA gave up
+
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;  // or null
+  long long q_token, q_head, o_token, o_head;  // strides in elements
+  long long k_page, k_token, k_head, v_page, v_token, v_head;
+  const int* q_start;  // [requests + 1]
+  const int* kv_len;   // [requests] (paged) or null: as many keys as new tokens, at row q_start
+  const int* table;    // [requests][max_pages] or null
+  int tokens, requests, heads, kv_heads, group;
+  int page_shift, max_pages, n_pages;
+  int max_kv;          // no request sees more keys than this (paged: max_pages pages)
+  int unit_rows;       // packed rows of a unit
+  int block_rows, block_used;  // the unit's rows sit in blocks of block_rows, of which block_used are used
+  float scale_log2;    // scale * log2(e)
+  float* part;         // [2 * grid][slot rows][D] unnormalised outputs
+  float* part_ml;      // [2 * grid][slot rows][2] max (log2 domain), sum
+  AttnRec* rec;        // [grid]
+  int* status;         // workspace status word
+};
+
+// P is rounded to the type of V: exp2(s - max + kOff). FP16 keeps 2^-14 .. 65504 at full
+// precision; the offset moves that window to where the probabilities are (2^-21 .. 2^8
+// relative to the running maximum, which may lag by 2^kLag).
+template <typename T>
+struct AttnType;
+template <>
+struct AttnType<__half> {
+  static constexpr float kOff = 7.f;
+  static constexpr bool kBf16 = false;
+};
+template <>
+struct AttnType<__nv_bfloat16> {
+  static constexpr float kOff = 0.f;
+  static constexpr bool kBf16 = true;
+};
+// The running maximum is only raised once a score exceeds it by 2^kLag: rescaling the
+// output is then rare after the first tiles, and exp2 stays below 2^(kLag + kOff).
+constexpr float kLag = 8.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (AttnType<T>::kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---------------------------------------------------------------- units and ranges
+
+struct AttnRequest {
+  int q0, n_new, kv, units;  // first query row, new tokens, keys, units per key/value head
+};
+
+// Lengths from device memory, clamped so that no later index leaves its buffer.
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
+  AttnRequest q;
+  int s = a.q_start[r], e = a.q_start[r + 1];
+  s = s < 0 ? 0 : (s > a.tokens ? a.tokens : s);
+  e = e < s ? s : (e > a.tokens ? a.tokens : e);
+  q.q0 = s;
+  q.n_new = e - s;
+  if (a.kv_len) {
+    const int n = a.kv_len[r];
+    q.kv = n < 0 ? 0 : (n > a.max_kv ? a.max_kv : n);
+  } else {
+    q.kv = q.n_new;
+  }
+  q.units = (q.n_new * a.group + a.unit_rows - 1) / a.unit_rows;
+  return q;
+}
+
+// Keys that new token t of the request sees: 0 .. kv - n_new + t.
+__device__ __forceinline__ int attn_seen(const AttnRequest& q, int t) {
+  const int n = q.kv - q.n_new + t + 1;
+  return n < 0 ? 0 : n;
+}
+// Keys that the last row of unit j sees.
+__device__ __forceinline__ int attn_unit_end(const AttnArgs& a, const AttnRequest& q, int j) {
+  const long long last = (long long)(j + 1) * a.unit_rows - 1;
+  const int t = (int)(last / a.group);
+  return attn_seen(q, t < q.n_new - 1 ? t : q.n_new - 1);
+}
+// Tiles of unit j; a unit that sees nothing still counts as one, its rows are written too.
+__device__ __forceinline__ int attn_unit_tiles(const AttnArgs& a, const AttnRequest& q, int j, int kv_tile) {
+  const int n = (attn_unit_end(a, q, j) + kv_tile - 1) / kv_tile;
+  return n < 1 ? 1 : n;
+}
+
+struct AttnPos {
+  int r, h, j, t;    // request, key/value head, unit of the head, first tile
+  long long tiles;   // tiles of this CTA's range (0: none)
+  long long before;  // tiles before it
+};
+
+// Cost in tiles of each lane's request (0 beyond the last), found by the whole warp where a
+// request has many units.
+__device__ __forceinline__ long long attn_costs(const AttnArgs& a, int r, int kv_tile, int lane) {
+  AttnRequest q{};
+  if (r < a.requests) q = attn_request(a, r);
+  long long c = 0;
+  if (q.units <= 4)
+    for (int j = 0; j < q.units; ++j) c += attn_unit_tiles(a, q, j, kv_tile);
+  unsigned big = __ballot_sync(0xffffffffu, q.units > 4);
+  while (big) {
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    AttnRequest o;
+    o.q0 = __shfl_sync(0xffffffffu, q.q0, src);
+    o.n_new = __shfl_sync(0xffffffffu, q.n_new, src);
+    o.kv = __shfl_sync(0xffffffffu, q.kv, src);
+    o.units = __shfl_sync(0xffffffffu, q.units, src);
+    long long s = 0;
+    for (int j = lane; j < o.units; j += 32) s += attn_unit_tiles(a, o, j, kv_tile);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (lane == src) c = s;
+  }
+  return c * a.kv_heads;
+}
+
+// Finds this CTA's range. Every thread of the CTA calls it; `sm` is shared memory for
+// kThreads / 32 + 1 sums and `pos` the shared result (valid after the call's barrier).
+// Thread i looks after requests [i * per, (i + 1) * per), so the order is the requests'.
+template <int kThreads>
+__device__ __forceinline__ void attn_locate(const AttnArgs& a, int kv_tile, int min_tiles, long long* sm,
+                                            AttnPos* pos) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const int per = (a.requests + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int i = 0; i < per; ++i) mine += attn_costs(a, tid * per + i, kv_tile, lane);
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sm[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm[w];
+    total += sm[w];
+  }
+  long long live = total / min_tiles;
+  live = live < 1 ? 1 : (live > gridDim.x ? gridDim.x : live);
+  const long long c = blockIdx.x;
+  const long long s0 = c < live ? total * c / live : total, s1 = c < live ? total * (c + 1) / live : total;
+  if (tid == 0) {
+    pos->tiles = s1 - s0;
+    pos->before = s0;
+  }
+  if (s1 > s0 && before <= s0 && s0 < before + __shfl_sync(0xffffffffu, incl, 31)) {
+    // this warp's requests hold the range's first tile
+    long long lo = before + incl - mine;
+    for (int i = 0; i < per; ++i) {
+      const int r = tid * per + i;
+      const long long cost = attn_costs(a, r, kv_tile, lane);
+      const unsigned hit = __ballot_sync(0xffffffffu, lo <= s0 && s0 < lo + cost);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        const int rr = __shfl_sync(0xffffffffu, r, src);
+        const long long per_head = __shfl_sync(0xffffffffu, cost, src) / a.kv_heads;
+        const long long off = s0 - __shfl_sync(0xffffffffu, lo, src);
+        const AttnRequest q = attn_request(a, rr);
+        const int h = (int)(off / per_head);
+        long long left = off - (long long)h * per_head;
+        for (int j0 = 0; j0 < q.units; j0 += 32) {
+          const int j = j0 + lane;
+          const int n = j < q.units ? attn_unit_tiles(a, q, j, kv_tile) : 0;
+          int in = n;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, in, d);
+            if (lane >= d) in += o;
+          }
+          const bool here = left >= in - n && left < in;
+          if (here) {
+            pos->r = rr;
+            pos->h = h;
+            pos->j = j;
+            pos->t = (int)(left - (in - n));
+          }
+          if (__ballot_sync(0xffffffffu, here)) break;
+          left -= __shfl_sync(0xffffffffu, in, 31);
+        }
+        break;
+      }
+      lo += cost;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks a CTA's range unit by unit.
+struct AttnWalk {
+  AttnRequest q;
+  int r, h, j, t0, t1, n, end;  // tiles [t0, t1) of the unit's n; end: keys its last row sees
+  long long left;               // tiles of the range from this unit on
+
+  __device__ __forceinline__ void unit(const AttnArgs& a, int kv_tile) {
+    end = attn_unit_end(a, q, j);
+    n = (end + kv_tile - 1) / kv_tile;
+    if (n < 1) n = 1;
+    t1 = left < (long long)(n - t0) ? t0 + (int)left : n;
+  }
+  __device__ __forceinline__ bool start(const AttnArgs& a, const AttnPos& p, int kv_tile) {
+    left = p.tiles;
+    if (left <= 0) return false;
+    r = p.r;
+    h = p.h;
+    j = p.j;
+    t0 = p.t;
+    q = attn_request(a, r);
+    unit(a, kv_tile);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a, int kv_tile) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++j >= q.units) {
+      j = 0;
+      if (++h >= a.kv_heads) {
+        h = 0;
+        do {
+          if (++r >= a.requests) return false;
+          q = attn_request(a, r);
+        } while (q.units == 0);
+      }
+    }
+    unit(a, kv_tile);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
+};
+
+// The packed row (of the request) at row i of a unit that starts at packed row `base`, or -1.
+__device__ __forceinline__ int attn_packed_row(int i, int base, int rows, int block_rows, int block_used) {
+  const int b = i / block_rows, o = i - b * block_rows;
+  const int p = base + b * block_used + o;
+  return o < block_used && p < rows ? p : -1;
+}
+
+// The two kernels and the combining pass.
+int attn_rows_limit(int head_dim);          // most packed rows of a request that the row kernel takes
+int attn_rows_grid(int head_dim, int rows); // CTAs of the row kernel
+int attn_wide_grid();
+int attn_wide_unit_rows(int head_dim, int group);  // packed rows of a unit of the tensor-core kernel
+cudaError_t launch_attn_rows(const AttnArgs& a, int head_dim, bool bf16, int nr, cudaStream_t st);
+cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st);
+cudaError_t launch_attn_combine(const AttnArgs& a, int head_dim, bool bf16, int grid, int slot_rows, cudaStream_t st);
+
+}  // namespace vq3

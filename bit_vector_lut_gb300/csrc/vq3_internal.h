@@ -127,6 +127,9 @@ cudaError_t bounds_read_delta(unsigned* host, bool reset);
 cudaError_t bounds_read_rotate(unsigned* host, bool reset);
 cudaError_t bounds_read_prefill(unsigned* host, bool reset);
 cudaError_t bounds_read_prefill_wide(unsigned* host, bool reset);
+cudaError_t bounds_read_attn(unsigned* host, bool reset);
+cudaError_t bounds_read_attn_wide(unsigned* host, bool reset);
+cudaError_t bounds_read_kvcache(unsigned* host, bool reset);
 #else
 #define VQ3_BOUNDS_RECORD(name)
 #define VQ3_IN(idx, n, site) ((void)(n), true)  // the extent is used only by the check
@@ -286,6 +289,35 @@ size_t lowrank_part_floats(int d_in, int rows, int rank);
 // xr_mma_order: the rows of xr are stored in the GEMM's operand order (mma_order_col).
 cudaError_t launch_lowrank(const uint16_t* xr, int rows, int d_in, const uint16_t* V, const uint16_t* U, int rank,
                            int d_out, float* part, float* ylr, cudaStream_t st, int xr_mma_order = 0);
+
+// Page plan of a serving step and append of new rows to the paged cache (layouts as
+// vq3_paged_plan and vq3_kv_append; strides in elements).
+struct PlanArgs {
+  const int* cached;
+  const int* fresh;
+  const int* ring;
+  const int* ring_state;
+  int* table;
+  int* q_start;
+  int* kv_len;
+  long long* slots;
+  int* positions;
+  int* ring_state_out;
+  int* status;
+  int requests, page_shift, ring_size, max_pages, max_tokens;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st);
+struct AppendArgs {
+  const uint16_t* k_rows;
+  const uint16_t* v_rows;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  const long long* slots;
+  long long k_row, k_row_head, v_row, v_row_head;
+  long long k_page, k_token, k_head, v_page, v_token, v_head;
+  int tokens, kv_heads, chunk_shift, n_pages, page_shift;  // chunk_shift: log2(head_dim / 8)
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
 
 // vq3_mlp_forward with passes of at most `pass_cap` rows (8, 16 or 32), and its
 // workspace size; vq3_mlp_forward itself uses 32.

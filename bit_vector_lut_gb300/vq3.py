@@ -10,7 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_size_t, c_uint8, c_void_p
+from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint8, c_void_p
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -50,6 +51,27 @@ class vq3_blob_view(ctypes.Structure):
                 ("lr_v", c_void_p)]
 
 
+class vq3_kv_cache(ctypes.Structure):
+    _fields_ = [("kv_heads", c_int), ("head_dim", c_int), ("page_size", c_int), ("n_pages", c_int), ("k", c_void_p),
+                ("v", c_void_p), ("k_page", c_longlong), ("k_token", c_longlong), ("k_head", c_longlong),
+                ("v_page", c_longlong), ("v_token", c_longlong), ("v_head", c_longlong)]
+
+
+class vq3_kv_rows(ctypes.Structure):
+    _fields_ = [("kv_heads", c_int), ("head_dim", c_int), ("tokens", c_int), ("k", c_void_p), ("v", c_void_p),
+                ("k_token", c_longlong), ("k_head", c_longlong), ("v_token", c_longlong), ("v_head", c_longlong)]
+
+
+class vq3_attn(ctypes.Structure):
+    _fields_ = [("type", c_int), ("heads", c_int), ("tokens", c_int), ("requests", c_int), ("max_new", c_int),
+                ("scale", c_float), ("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("q_start", c_void_p),
+                ("q_token", c_longlong), ("q_head", c_longlong), ("out_token", c_longlong), ("out_head", c_longlong)]
+
+
+# VQ3_TYPE_* in vq3.h
+TYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
@@ -87,6 +109,13 @@ def _load() -> ctypes.CDLL:
                                          c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         "vq3_mlp_forward_noalloc": (c_int, [c_void_p, c_int, POINTER(vq3_mlp_layer), c_void_p, c_void_p]),
         "vq3_noalloc_status": (c_int, [POINTER(c_int), c_void_p]),
+        "vq3_paged_plan": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "vq3_kv_append": (c_int, [POINTER(vq3_kv_rows), c_void_p, POINTER(vq3_kv_cache), c_void_p]),
+        "vq3_attention_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
+        "vq3_paged_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_cache), c_void_p, c_int, c_void_p, c_void_p,
+                                        c_size_t, c_void_p]),
+        "vq3_prompt_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_rows), c_void_p, c_size_t, c_void_p]),
         "vq3_last_error": (ctypes.c_char_p, []),
         "vq3_version": (ctypes.c_char_p, []),
         "vq3_bounds_check": (c_int, [POINTER(ctypes.c_uint), c_int, c_int]),
@@ -122,7 +151,7 @@ def version() -> str:
     return lib.vq3_version().decode()
 
 
-BOUNDS_FILES = ("decode", "lowrank", "delta", "rotate", "prefill", "prefill_wide")
+BOUNDS_FILES = ("decode", "lowrank", "delta", "rotate", "prefill", "prefill_wide", "attn", "attn_wide", "kvcache")
 
 
 def bounds_check(reset: bool = True) -> dict[str, tuple[int, int]]:
@@ -445,3 +474,169 @@ def mlp_prenorm_step(r: torch.Tensor, layer: MLP, out: torch.Tensor, r_next: tor
     _check(lib.vq3_mlp_prenorm_step(r.data_ptr(), _ptr(ss), rows, ctypes.byref(layer.struct), eps, out.data_ptr(),
                                     r_next.data_ptr(), _ptr(ss_next), ws.data_ptr(), ws.numel(), _stream(stream)))
     return r_next
+
+
+# ---------------------------------------------------------------- attention and its paged cache
+
+class PagedPlan(NamedTuple):
+    """What paged_plan writes beside the table (device tensors); `status` is 0 or a sum of VQ3_PLAN_* bits."""
+    q_start: torch.Tensor     # int32 [requests + 1]
+    kv_len: torch.Tensor      # int32 [requests]
+    slots: torch.Tensor       # int64 [max_tokens]
+    positions: torch.Tensor   # int32 [max_tokens]
+    ring_state: torch.Tensor  # int32 {head, count} after the step
+    status: torch.Tensor      # int32 [1]
+
+
+def _want(ok: bool, msg: str) -> None:
+    if not ok:
+        raise Vq3Error(-1, msg)
+
+
+def _int_arrays(device, **arrays) -> None:
+    for name, t in arrays.items():
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+            raise Vq3Error(-1, f"{name} must be a contiguous int32 tensor on {device}")
+
+
+def _launch(device, stream, call, *args) -> None:
+    """call(*args, stream) with `device` current; the stream is the caller's or the device's current one."""
+    if device.type != "cuda":
+        raise Vq3Error(-1, f"tensors must be on a CUDA device, not {device}")
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+    if rc != VQ3_OK:
+        raise Vq3Error(rc, lib.vq3_last_error().decode())
+
+
+def _kept(stream, *tensors) -> None:
+    """Tensors made here and used on a stream of the caller's: their memory is not reused before that use."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, ring: torch.Tensor,
+               ring_state: torch.Tensor, page_size: int, max_tokens: int, out: PagedPlan | None = None,
+               stream=None) -> PagedPlan:
+    """Block tables and slot maps of a serving step (vq3_paged_plan): `cached` and `fresh` [requests] int32 lengths,
+    `table` [requests, max_pages] int32 gets the new pages in place, taken from the ring of free pages. `out`: a
+    plan of the same sizes to write into (its ring_state must not be the one passed in)."""
+    device = table.device
+    requests, max_pages = table.shape
+    _int_arrays(device, cached=cached, fresh=fresh, table=table, ring=ring, ring_state=ring_state)
+    _want(cached.numel() == requests and fresh.numel() == requests and ring_state.numel() == 2,
+          "cached and fresh need one entry per table row, ring_state two")
+    if out is None:
+        ints = torch.empty(2 * requests + max_tokens + 4, dtype=torch.int32, device=device)
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        q_start, kv_len, positions, state, status = ints.split((requests + 1, requests, max_tokens, 2, 1))
+        out = PagedPlan(q_start, kv_len, slots, positions, state, status)
+        _kept(stream, ints, slots)
+    else:
+        _int_arrays(device, q_start=out.q_start, kv_len=out.kv_len, positions=out.positions,
+                    ring_state=out.ring_state, status=out.status)
+        _want(out.q_start.numel() == requests + 1 and out.kv_len.numel() == requests and
+              out.positions.numel() == max_tokens and out.slots.numel() == max_tokens and
+              out.ring_state.numel() == 2 and out.status.numel() == 1 and out.slots.dtype == torch.int64 and
+              out.slots.is_contiguous() and out.slots.device == device, "out is a plan of other sizes")
+    _launch(device, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
+            ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
+            out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+            out.ring_state.data_ptr(), out.status.data_ptr())
+    return out
+
+
+def _kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> vq3_kv_cache:
+    _want(k_pages.dim() == 4 and k_pages.shape == v_pages.shape and k_pages.dtype == v_pages.dtype and
+          k_pages.dtype in TYPES and k_pages.device == v_pages.device,
+          "k_pages and v_pages must be [n_pages, page_size, kv_heads, head_dim], FP16 or BF16, alike")
+    n_pages, page_size, kv_heads, head_dim = k_pages.shape
+    ks, vs = k_pages.stride(), v_pages.stride()
+    _want(ks[3] == 1 and vs[3] == 1, "the head_dim axis of the cache must be contiguous")
+    return vq3_kv_cache(kv_heads, head_dim, page_size, n_pages, k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1],
+                        ks[2], vs[0], vs[1], vs[2])
+
+
+def _kv_rows(k: torch.Tensor, v: torch.Tensor) -> vq3_kv_rows:
+    _want(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in TYPES and k.device == v.device,
+          "k and v must be [tokens, kv_heads, head_dim], FP16 or BF16, alike")
+    tokens, kv_heads, head_dim = k.shape
+    ks, vs = k.stride(), v.stride()
+    _want(ks[2] == 1 and vs[2] == 1, "the head_dim axis of k and v must be contiguous")
+    return vq3_kv_rows(kv_heads, head_dim, tokens, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1])
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              stream=None) -> None:
+    """Writes rows k, v [tokens, kv_heads, head_dim] into the paged cache [n_pages, page_size, kv_heads, head_dim] (any
+    strides) at `slots` [>= tokens] int64 (vq3_kv_append); negative slots are skipped."""
+    cache, rows = _kv_cache(k_pages, v_pages), _kv_rows(k, v)
+    _want(k.dtype == k_pages.dtype and k.device == k_pages.device, "rows and cache must have one type and device")
+    _want(slots.dtype == torch.int64 and slots.is_contiguous() and slots.numel() >= rows.tokens and
+          slots.device == k.device, "slots must be a contiguous int64 tensor with an entry per row")
+    _launch(k.device, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
+
+
+def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new: int = 0) -> int:
+    """Workspace of paged_attention and prompt_attention; it needs no initialisation."""
+    return int(lib.vq3_attention_workspace_bytes(heads, kv_heads, head_dim, max_new))
+
+
+def _attention(call, q, kv, q_start, max_new, scale, out, lse, ws, stream, *more) -> torch.Tensor:
+    _want(q.dim() == 3 and q.dtype in TYPES and q.shape[2] == kv.head_dim,
+          f"q must be [tokens, heads, {kv.head_dim}], FP16 or BF16")
+    device = q.device
+    tokens, heads, head_dim = q.shape
+    made = []
+    if out is None:
+        out = torch.empty((tokens, heads, head_dim), dtype=q.dtype, device=device)
+        made.append(out)
+    else:
+        _want(out.shape == q.shape and out.dtype == q.dtype and out.device == device, "out must be like q")
+    if lse is not None:
+        _want(lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.is_contiguous() and
+              lse.device == device, "lse must be a contiguous float32 tensor [tokens, heads]")
+    qs, os_ = q.stride(), out.stride()
+    _want(qs[2] == 1 and os_[2] == 1, "the head_dim axis of q and out must be contiguous")
+    _int_arrays(device, q_start=q_start)
+    if ws is None:
+        n = int(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new))
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        made.append(ws)
+    _kept(stream, *made)
+    a = vq3_attn(TYPES[q.dtype], heads, tokens, q_start.numel() - 1, max_new,
+                 head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
+                 None if lse is None else lse.data_ptr(), q_start.data_ptr(), qs[0], qs[1], os_[0], os_[1])
+    _launch(device, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+    return out
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                    q_start: torch.Tensor, kv_len: torch.Tensor, max_new: int = 0, scale: float | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Causal attention of packed new tokens q [tokens, heads, head_dim] over the paged cache (vq3_paged_attention):
+    `table` [requests, max_pages], `q_start` [requests + 1], `kv_len` [requests] int32 on the device, kv_len with the
+    new tokens counted in. max_new: most new tokens of a request, 0 if unknown (it only picks the kernel). scale:
+    1 / sqrt(head_dim) by default. `lse` [tokens, heads] FP32 is filled if given."""
+    cache = _kv_cache(k_pages, v_pages)
+    _want(table.dim() == 2 and table.shape[0] == kv_len.numel() == q_start.numel() - 1,
+          "table must be [requests, max_pages], kv_len [requests], q_start [requests + 1]")
+    _want(q.dtype == k_pages.dtype and q.device == k_pages.device, "q and cache must have one type and device")
+    _int_arrays(q.device, table=table, kv_len=kv_len)
+    return _attention(lib.vq3_paged_attention, q, cache, q_start, max_new, scale, out, lse, ws, stream,
+                      table.data_ptr(), table.shape[1], kv_len.data_ptr())
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, max_new: int = 0,
+                     scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention over whole packed prompts (vq3_prompt_attention): q [tokens, heads, head_dim], k and v [tokens,
+    kv_heads, head_dim], request r at rows q_start[r] .. q_start[r + 1] - 1 of all three."""
+    rows = _kv_rows(k, v)
+    _want(q.dtype == k.dtype and q.device == k.device, "q, k and v must have one type and device")
+    return _attention(lib.vq3_prompt_attention, q, rows, q_start, max_new, scale, out, lse, ws, stream)

@@ -302,6 +302,144 @@ VQ3_API int vq3_delta_rule_forward(const uint16_t* q, const uint16_t* k, const u
                                    uint16_t* out, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The attention token mixer and its paged key/value cache. The pages' hybrid
+ * decoder alternates the gated delta rule above with attention layers ("Release
+ * 0.2", table row "Token mixers"); they give neither its interface nor the cache's
+ * layout, so the calls below are this library's.
+ *
+ * Query heads share key/value heads in groups: query head h reads key/value head
+ * h / (heads / kv_heads). The rows of a batch are packed: request r owns rows
+ * q_start[r] .. q_start[r + 1] - 1 of q, out and lse, q_start ascending from
+ * q_start[0]. Rows behind q_start[requests] are neither read nor written. All
+ * lengths live in device memory, so that a captured graph serves any step that
+ * fits its sizes. Strides are in elements and multiples of 8, pointers to FP16 or
+ * BF16 data 16-byte aligned; the head_dim axis is contiguous; an axis of one
+ * element may have any stride.
+ * ---------------------------------------------------------------------------
+ */
+#define VQ3_TYPE_F16 0
+#define VQ3_TYPE_BF16 1
+
+/* The cache: pages of page_size tokens. Token x of a request is row x % page_size of
+ * page table[r][x / page_size]. Any order of the page, token and head axes.
+ * kv_heads >= 1; head_dim 64, 128 or 256; page_size a power of two in [16, 256]. */
+typedef struct vq3_kv_cache {
+  int kv_heads;
+  int head_dim;
+  int page_size;
+  int n_pages;
+  void* k;
+  void* v;
+  long long k_page, k_token, k_head; /* strides */
+  long long v_page, v_token, v_head;
+} vq3_kv_cache;
+
+/* Keys and values as rows: [tokens][kv_heads][head_dim] with strides (slices of a
+ * fused projection's output, for instance). */
+typedef struct vq3_kv_rows {
+  int kv_heads;
+  int head_dim;
+  int tokens;
+  const void* k;
+  const void* v;
+  long long k_token, k_head; /* strides */
+  long long v_token, v_head;
+} vq3_kv_rows;
+
+/* The query side of an attention call. */
+typedef struct vq3_attn {
+  int type;     /* VQ3_TYPE_* of q, k, v and out */
+  int heads;    /* query heads, a multiple of the key/value heads */
+  int tokens;   /* rows of q, out and lse */
+  int requests; /* at most 8192 */
+  int max_new;  /* most new tokens of a request, 0 if unknown. Only picks the kernel: a wrong
+                   value costs time, not correctness */
+  float scale;  /* of the scores, positive (1 / sqrt(head_dim) for instance) */
+  const void* q;
+  void* out;
+  float* lse;   /* [tokens][heads] natural logarithm of the softmax's sum, or NULL */
+  const int* q_start; /* device, [requests + 1] */
+  long long q_token, q_head; /* strides */
+  long long out_token, out_head;
+} vq3_attn;
+
+/*
+ * The page plan of a serving step: block tables and slot maps from the requests'
+ * lengths, on the GPU. Request r has cached[r] tokens in the cache and gets fresh[r]
+ * new ones (either may be 0); it holds ceil(cached / page_size) pages, listed in its
+ * table row, and needs ceil((cached + fresh) / page_size). The pages in between are
+ * taken from a ring of free pages in request order: ring[(head + i) % ring_size],
+ * i = 0 .. count - 1, are free, {head, count} = ring_state. (Pages that come free are
+ * written behind them and counted up by the caller.)
+ *   table      [requests][max_pages], read for the held pages, the new pages added;
+ *              every other entry is left as it was
+ *   q_start    [requests + 1] first row of each request's new tokens
+ *   kv_len     [requests] cached + fresh
+ *   slots      [max_tokens] page * page_size + row of each new token, -1 behind the
+ *              last and where the table holds a negative page
+ *   positions  [max_tokens] cached + i of each new token, -1 behind the last
+ *   ring_state_out  {head, count} after the step (not ring_state itself)
+ *   status     one word: 0, or the sum of VQ3_PLAN_* that did not hold. Then nothing is
+ *              taken: table and ring state stay, q_start and kv_len are 0 and every slot
+ *              and position -1, so that the step's other calls do nothing.
+ * All device memory. One launch; calls with the same inputs write the same outputs.
+ * requests at most 8192. Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ */
+#define VQ3_PLAN_NO_PAGES 1        /* fewer free pages than needed */
+#define VQ3_PLAN_NARROW_TABLE 2    /* a request needs more than max_pages pages */
+#define VQ3_PLAN_TOO_MANY_TOKENS 4 /* more new tokens than max_tokens */
+#define VQ3_PLAN_BAD_LENGTH 8      /* a negative or too large length (2^30), or ring state */
+VQ3_API int vq3_paged_plan(const int* cached, const int* fresh, int requests, int page_size, const int* ring,
+                           int ring_size, const int* ring_state, int* table, int max_pages, int max_tokens,
+                           int* q_start, int* kv_len, long long* slots, int* positions, int* ring_state_out,
+                           int* status, void* stream);
+
+/*
+ * Appends rows to the cache: token t's keys and values go to slot slots[t] (device,
+ * [rows->tokens]; page * page_size + row). Slots outside [0, n_pages * page_size) are
+ * skipped; the others are distinct (of two rows with one slot either may stay). The
+ * rows must not overlap the cache.
+ * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ */
+VQ3_API int vq3_kv_append(const vq3_kv_rows* rows, const long long* slots, const vq3_kv_cache* cache, void* stream);
+
+/*
+ * Workspace of the two attention calls (bytes; 0 for unsupported sizes). It needs no
+ * initialisation. Calls that share one must not overlap on the GPU. Its first 32-bit
+ * word is 0 after a call, or 3 if a wait inside a kernel gave up (about a second), the
+ * call's outputs being invalid then: vq3_workspace_status reads it.
+ */
+VQ3_API size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_dim, int max_new);
+
+/*
+ * Causal attention of new tokens over a paged cache that holds them already: single
+ * tokens, verify steps, prefill chunks, mixed in one batch. Row i of request r (of
+ * n = q_start[r + 1] - q_start[r]) sees the keys j < kv_len[r] - n + i + 1:
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * with scores, softmax statistics and sums in FP32, the probabilities rounded once to
+ * the type of v (as the operand of the second product) and out rounded once. A row
+ * that sees no key (kv_len < n) gets zeros and lse = -infinity. Keys and values behind
+ * kv_len are never used, whatever the pages hold there; those of the request's own
+ * tokens are finite. kv_len is cut to max_pages pages; a page number outside the cache
+ * reads as zeros.
+ * table: device [requests][max_pages]; kv_len: device [requests]; max_pages *
+ * page_size at most 2^30, tokens * heads below 2^30. out does not overlap an input.
+ * Deterministic; results do not depend on where the pages lie.
+ * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ENOSPACE, VQ3_ECUDA.
+ */
+VQ3_API int vq3_paged_attention(const vq3_attn* attn, const vq3_kv_cache* cache, const int* table, int max_pages,
+                                const int* kv_len, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention over whole prompts, packed: row i of request r sees rows q_start[r]
+ * .. q_start[r] + i of k and v (which have the same rows as q). Otherwise as
+ * vq3_paged_attention.
+ */
+VQ3_API int vq3_prompt_attention(const vq3_attn* attn, const vq3_kv_rows* rows, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/*
  * Cited as vq3_residual_rmsnorm and vq3_mlp_forward (the two fused).
  * One layer of the pre-norm residual stack: r' = fp16(r_in + delta) (r_in alone when
  * delta is NULL), n = fp16(r' / sqrt(mean(r'^2) + eps)) per row, out = the MLP block
@@ -447,12 +585,13 @@ VQ3_API const char* vq3_version(void);
  * points' arguments fix); an access out of range is skipped and counted. This reads
  * the counts: out[2 f] = accesses skipped in kernel file f, out[2 f + 1] = the site
  * number of the first one (0 if none), for f = 0 decode, 1 low-rank factors,
- * 2 delta rule, 3 rotation and residual, 4 prefill up to 128 rows, 5 prefill above.
- * reset != 0 clears the counts after reading. n_out: entries of out, at least
- * VQ3_BOUNDS_FILES * 2 (else VQ3_EINVAL). Synchronous on the device (waits for all
+ * 2 delta rule, 3 rotation and residual, 4 prefill up to 128 rows, 5 prefill above,
+ * 6 attention of few rows and the combining pass, 7 attention on tensor cores, 8 page
+ * plan and append. reset != 0 clears the counts after reading. n_out: entries of out, at
+ * least 12 (else VQ3_EINVAL); files whose two entries do not fit are left out. Synchronous on the device (waits for all
  * work); call it between, not during, launches.
  */
-#define VQ3_BOUNDS_FILES 6
+#define VQ3_BOUNDS_FILES 9
 VQ3_API int vq3_bounds_check(unsigned* out, int n_out, int reset);
 
 #ifdef __cplusplus
