@@ -47,7 +47,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // 16 bytes, read once: not kept in L1.
@@ -59,16 +59,6 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// Query rows `row` of the request (packed) to its place in q, out and lse.
-struct RowPlace {
-  long long token;
-  int head;
-};
-__device__ __forceinline__ RowPlace row_place(const AttnArgs& a, int q0, int kv_head, int p) {
-  const int t = p / a.group;
-  return {(long long)(q0 + t), kv_head * a.group + (p - t * a.group)};
-}
 
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
@@ -84,6 +74,7 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
 
   attn_locate<kThreads>(a, kTile, kMinTiles, s_sum, &s_pos);
   const AttnPos pos = s_pos;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   AttnRec rec{};
   AttnWalk w;
   for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
@@ -462,8 +453,7 @@ cudaError_t launch_rows_t(const AttnArgs& a, int d, int nr, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_combine(const AttnArgs& a, int grid, int slot_rows, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  const int y = slot_rows / kCWarps < 1 ? 1 : (slot_rows / kCWarps > 8 ? 8 : slot_rows / kCWarps);
-  cfg.gridDim = dim3(grid, y);
+  cfg.gridDim = dim3(grid, 8);
   cfg.blockDim = dim3(kCWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -85,11 +85,15 @@ struct Choice {
 };
 Choice choose(int head_dim, int group, int rows) {
   Choice c{};
-  c.wide = false;
+  c.wide = group <= 128 && (rows == 0 || rows > attn_rows_limit(head_dim));
+  if (c.wide) {
+    c.grid = attn_wide_grid();
+    c.slot_rows = 128 * attn_wide_blocks(head_dim);
+    return c;
+  }
   c.nr = (rows > 0 && rows <= 8) || head_dim == 256 ? 1 : 2;
   c.grid = attn_rows_grid(head_dim, 8 * c.nr);
   c.slot_rows = 8 * c.nr;
-  (void)group;
   return c;
 }
 
@@ -129,7 +133,9 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.heads = at->heads;
   a.kv_heads = kv_heads;
   a.group = group;
-  a.unit_rows = a.block_rows = a.block_used = c.slot_rows;
+  a.block_rows = c.wide ? 128 : c.slot_rows;
+  a.block_used = c.wide ? 128 / group * group : c.slot_rows;
+  a.unit_rows = c.slot_rows / a.block_rows * a.block_used;
   a.scale_log2 = at->scale * 1.4426950408889634f;
   a.status = reinterpret_cast<int*>(ws);
   a.rec = reinterpret_cast<AttnRec*>(ws + w.rec);
@@ -137,7 +143,7 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.part = reinterpret_cast<float*>(ws + w.part);
   const bool bf16 = at->type == VQ3_TYPE_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_attn_rows(a, head_dim, bf16, c.nr, st);
+  cudaError_t e = c.wide ? launch_attn_wide(a, head_dim, bf16, st) : launch_attn_rows(a, head_dim, bf16, c.nr, st);
   if (e == cudaSuccess) e = launch_attn_combine(a, head_dim, bf16, c.grid, c.slot_rows, st);
   if (e != cudaSuccess) return report_error(VQ3_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return report_ok();

@@ -280,6 +280,16 @@ struct AttnWalk {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
 };
 
+// Place of packed row p of a request in q, out and lse.
+struct RowPlace {
+  long long token;
+  int head;
+};
+__device__ __forceinline__ RowPlace row_place(const AttnArgs& a, int q0, int kv_head, int p) {
+  const int t = p / a.group;
+  return {(long long)(q0 + t), kv_head * a.group + (p - t * a.group)};
+}
+
 // The packed row (of the request) at row i of a unit that starts at packed row `base`, or -1.
 __device__ __forceinline__ int attn_packed_row(int i, int base, int rows, int block_rows, int block_used) {
   const int b = i / block_rows, o = i - b * block_rows;
@@ -291,7 +301,7 @@ __device__ __forceinline__ int attn_packed_row(int i, int base, int rows, int bl
 int attn_rows_limit(int head_dim);          // most packed rows of a request that the row kernel takes
 int attn_rows_grid(int head_dim, int rows); // CTAs of the row kernel
 int attn_wide_grid();
-int attn_wide_unit_rows(int head_dim, int group);  // packed rows of a unit of the tensor-core kernel
+int attn_wide_blocks(int head_dim);  // row blocks of 128 of a unit of the tensor-core kernel
 cudaError_t launch_attn_rows(const AttnArgs& a, int head_dim, bool bf16, int nr, cudaStream_t st);
 cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st);
 cudaError_t launch_attn_combine(const AttnArgs& a, int head_dim, bool bf16, int grid, int slot_rows, cudaStream_t st);

@@ -1,4 +1,741 @@
+// Attention of many query rows on the 5th-generation tensor cores: prefill chunks over the
+// paged cache, whole prompts, and verify steps whose rows fill more than the row kernel takes.
+//
+// One persistent CTA per SM walks its range of (request, key/value head, row block, 128-key
+// tile). Per tile, in one pass with a running maximum and sum:
+//   S[128 rows][128 keys] = Q K^T     tcgen05.mma, Q and K in shared memory (128-byte swizzle)
+//   P = exp2(S scale - max)           read from and written back to tensor memory as 16 bits
+//   O[128 rows][D] += P V             tcgen05.mma, P from tensor memory, V from shared memory
+// The rows of a block are (token, query head of the group), so the heads of a group share
+// every tile. head_dim 64 and 128: two blocks of 128 rows (A, B) share a tile, one warpgroup
+// each, so that one block's softmax runs under the other's products. head_dim 256: O alone
+// takes half of tensor memory, so there is one block, whose softmax the two warpgroups share
+// by key columns (64 each, the row maxima exchanged through shared memory), and two S
+// buffers, so that the next tile's Q K^T runs under it.
+//   warps 0-3, 4-7  softmax, rescaling and output of block A / B (or keys 0-63 / 64-127)
+//   warp 8          TMA: the lanes each copy a page's rows (page numbers prefetched a tile
+//                   ahead) into a ring of stages, in the order in which the MMA warp uses them
+//   warp 9          issues the MMAs
+// O is rescaled only when a row's maximum rises by more than 2^8 (see kLag), by the softmax
+// warps themselves.
+// Keys behind the last that the block sees are masked in S; of V only the 16-row steps that
+// hold keys are multiplied, the rest of the last such step zeroed first, so that what lies
+// behind a request's keys is never used.
+// All waits are bounded: one that runs out ends the CTA's work and marks its record.
+#include <cuda.h>  // CUtensorMap; the encoder is fetched from the driver at run time
+
 #include "attn_common.cuh"
+
 namespace vq3 {
 VQ3_BOUNDS_RECORD(attn_wide)
+namespace {
+
+constexpr int kTile = 128;      // keys per tile
+constexpr int kMinTiles = 2;    // fewest tiles per CTA
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 10 * 32;
+constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after one second
+constexpr unsigned long long kDrainNs = 100000000ull;   // the end-of-kernel drain waits at most 0.1 s
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long globaltimer_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of parity `parity`, at most kWaitNs. `abort`: the CTA's shared flag;
+// once a wait gave up, every wait returns at once.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = globaltimer_ns();
+  for (unsigned it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity) || *abort) return;
+    if ((it & 63u) == 0u && globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kDrainNs) return;
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptors in the 128-byte swizzle layout: rows of 64 16-bit elements (128
+// bytes) in 8-row atoms of 1 KB. K-major (rows along M / N): the 64 elements lie along K, which
+// advances 32 bytes per 16 elements. MN-major (rows along K): the 64 elements lie along N, the
+// next 64 `lbo` bytes on; K advances 2 KB per 16 rows.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// kind::f16, FP32 D, A K-major, B K-major or MN-major, M = 128.
+__host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+#define VQ3_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define VQ3_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+// 32 columns of this warp's 32 lanes (rows).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : VQ3_R8(r, 0), VQ3_R8(r, 8), VQ3_R8(r, 16), VQ3_R8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::VQ3_I8(r, 0),
+      VQ3_I8(r, 8), VQ3_I8(r, 16), VQ3_I8(r, 24), "r"(addr)
+      : "memory");
+}
+// Two FP32 operations per instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D>
+struct WideCfg {
+  static constexpr int kBlocks = D == 256 ? 1 : 2;          // row blocks of a unit
+  static constexpr int kStageCols = D == 64 ? 64 : 128;     // head_dim columns of a stage
+  static constexpr int kParts = D / kStageCols;             // stages per K or V tile
+  static constexpr int kCb = kStageCols / 64;               // 64-column blocks of a stage
+  static constexpr int kCbBytes = kTile * 128;              // 16 KB: 128 rows of 128 bytes
+  static constexpr int kStageBytes = kCb * kCbBytes;
+  static constexpr int kQBytes = kBlocks * (D / 64) * kCbBytes;
+  static constexpr int kStages = D == 64 ? 10 : 5;
+  static constexpr int kMisc = 3 * 1024;  // barriers, range, exchange of row maxima
+  static constexpr int kSmem = kQBytes + kStages * kStageBytes + kMisc;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert(2 * kSmem > 228 * 1024, "one CTA per SM: it takes all of tensor memory");
+  // tensor memory columns: two S buffers of 128 (P over them), then O
+  static constexpr uint32_t kO = 256;
+};
+
+// Column of P's step of 16 keys inside its S buffer: each half of P lies over the half of S
+// that it was made from.
+__device__ __forceinline__ uint32_t p_col(int step) { return (uint32_t)(step < 4 ? 8 * step : 64 + 8 * (step - 4)); }
+
+struct WideMaps {
+  CUtensorMap q, k, v;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_constant__ AttnArgs a,
+                                                                const __grid_constant__ WideMaps maps) {
+  using C = WideCfg<D>;
+  constexpr int NB = C::kBlocks;
+  constexpr bool kBf16 = AttnType<T>::kBf16;
+  constexpr float kOff = AttnType<T>::kOff;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* const misc = smem + C::kQBytes + C::kStages * C::kStageBytes;
+  float* const s_max = reinterpret_cast<float*>(misc);                 // [2][2][128]
+  unsigned long long* const bars = reinterpret_cast<unsigned long long*>(misc + 2048);  // 40
+  AttnPos* const s_pos = reinterpret_cast<AttnPos*>(misc + 2048 + 320);
+  long long* const s_sum = reinterpret_cast<long long*>(misc + 2048 + 384);  // kThreads / 32
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(misc + 2048 + 512);
+  volatile int* const abort = reinterpret_cast<volatile int*>(misc + 2048 + 516);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
+  const auto q_at = [&](int block, int cb) { return base + (uint32_t)((block * (D / 64) + cb) * C::kCbBytes); };
+  const auto stage_at = [&](int s) { return base + (uint32_t)(C::kQBytes + s * C::kStageBytes); };
+  const auto full = [&](int s) { return bar0 + 8u * s; };                    // stage holds a tile part
+  const auto empty = [&](int s) { return bar0 + 8u * (C::kStages + s); };    // its products are done
+  constexpr int kB0 = 2 * C::kStages;
+  const uint32_t q_full = bar0 + 8u * kB0, q_empty = bar0 + 8u * (kB0 + 1);
+  const auto s_full = [&](int b) { return bar0 + 8u * (kB0 + 2 + b); };      // S buffer b holds scores
+  const auto p_full = [&](int b) { return bar0 + 8u * (kB0 + 4 + b); };      // and now probabilities
+  const auto pv_done = [&](int b) { return bar0 + 8u * (kB0 + 6 + b); };     // P V of block b's latest tile done
+  const auto o_empty = [&](int b) { return bar0 + 8u * (kB0 + 8 + b); };     // O of block b read out
+  const uint32_t drain = bar0 + 8u * (kB0 + 10);
+  static_assert(kB0 + 11 <= 40, "barriers");
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(p_full(b), NB == 2 ? 4 : 8);
+      mbar_init(pv_done(b), 1);
+      mbar_init(o_empty(b), NB == 2 ? 4 : 8);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  attn_locate<kThreads>(a, kTile, kMinTiles, s_sum, s_pos);  // its barriers order the set-up above, too
+  tc_after();
+  const uint32_t tmem = *s_tmem;
+  const AttnPos pos = *s_pos;
+  // Whether a wait gave up, the same answer for the whole warp. The copy and MMA warps then issue
+  // nothing more; the softmax warps, which meet at barriers, walk on over what is there.
+  const auto stopped = [&] { return __shfl_sync(0xffffffffu, *abort, 0) != 0; };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ copies
+    const int box = a.table ? (1 << a.page_shift < kTile ? 1 << a.page_shift : kTile) : kTile;  // rows per copy
+    const int boxes = kTile / box;
+    const int my_box = lane & (boxes - 1), my_cb = lane / boxes;  // this lane's copy of a stage
+    const int tt = a.block_used / a.group;                        // tokens of a row block
+    int it = 0, units = 0;
+    AttnWalk w;
+    for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+      if (w.end == 0) continue;
+      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
+      if (units) mbar_wait(q_empty, (uint32_t)((units - 1) & 1), abort);
+      if (stopped()) break;
+      const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
+      if (lane == 0) {
+        mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.block_used * 128));
+        for (int b = 0; b < blocks; ++b)
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_3d(q_at(b, cb), &maps.q, cb * 64, w.h * a.group, w.q.q0 + (w.j * NB + b) * tt, q_full);
+      }
+      __syncwarp();
+      ++units;
+      // the page of this lane's rows of tile t
+      const auto page_of = [&](int t) -> int {
+        const int x = t * kTile + my_box * box;
+        if (!a.table || t >= w.t1 || x >= w.end) return 0;
+        const size_t at = (size_t)w.r * a.max_pages + (x >> a.page_shift);
+        return VQ3_IN(at, (size_t)a.requests * a.max_pages, 1) ? __ldg(a.table + at) : -1;
+      };
+      const auto copy = [&](const CUtensorMap* map, int t, int page) {
+        const int left = w.end - t * kTile;  // keys of the tile that count
+        const int n = a.table ? ((left < kTile ? left : kTile) + box - 1) / box : 1;
+        const int x = t * kTile + my_box * box;
+        const int row = a.table ? x & ((1 << a.page_shift) - 1) : w.q.q0 + x;
+#pragma unroll
+        for (int part = 0; part < C::kParts; ++part, ++it) {
+          const int s = it % C::kStages;
+          if (it >= C::kStages) mbar_wait(empty(s), (uint32_t)((it / C::kStages - 1) & 1), abort);
+          if (stopped()) return;
+          if (lane == 0) mbar_expect_tx(full(s), (uint32_t)(n * C::kCb * box * 128));
+          __syncwarp();
+          if (my_box < n && my_cb < C::kCb)
+            tma_4d(stage_at(s) + (uint32_t)(my_cb * C::kCbBytes + my_box * box * 128), map,
+                   part * C::kStageCols + my_cb * 64, row, w.h, a.table ? page : 0, full(s));
+        }
+      };
+      int page = page_of(w.t0);
+      if constexpr (NB == 2) {
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int next = page_of(t + 1);
+          copy(&maps.k, t, page);
+          copy(&maps.v, t, page);
+          page = next;
+        }
+      } else {
+        int ahead = page_of(w.t0 + 1);
+        copy(&maps.k, w.t0, page);
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int next = page_of(t + 2);
+          if (t + 1 < w.t1) copy(&maps.k, t + 1, ahead);
+          copy(&maps.v, t, page);
+          page = ahead;
+          ahead = next;
+        }
+      }
+    }
+    // no copy is in flight when the CTA ends (they have all been used unless a wait gave up)
+    if (units) mbar_drain(q_full, (uint32_t)((units - 1) & 1));
+    for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+      mbar_drain(full(j % C::kStages), (uint32_t)((j / C::kStages) & 1));
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t id_qk = idesc(kTile, kBf16, false), id_pv = idesc(C::kStageCols, kBf16, true);
+    int it = 0, units = 0;     // stages used, units
+    int tiles[2] = {0, 0};     // tiles of block b (NB == 2), all tiles (NB == 1, [0])
+    int outs[2] = {0, 0};      // units of block b
+    AttnWalk w;
+    const auto release = [&](int s) {
+      if (lane == 0) mma_commit(empty(s));
+    };
+    const auto q_done = [&] {  // the unit's last Q K^T is issued
+      if (lane == 0) mma_commit(q_empty);
+    };
+    // S buffer `buf` = Q of block b times stages it .. it + kParts - 1
+    const auto qk = [&](int b, int buf, int at) {
+      if (stopped()) return;
+      tc_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint32_t kb = stage_at((at + c / C::kCb) % C::kStages) + (uint32_t)((c % C::kCb) * C::kCbBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, c) + 32u * k, 16), desc_sw128(kb + 32u * k, 16),
+                   id_qk, c + k > 0);
+        }
+        mma_commit(s_full(buf));
+      }
+      __syncwarp();
+    };
+    const auto pv = [&](int b, int buf, int at, int steps, bool first) {
+      if (stopped()) return;
+      tc_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int part = 0; part < C::kParts; ++part) {
+          const uint32_t vb = stage_at((at + part) % C::kStages);
+          const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
+          for (int k = 0; k < steps; ++k)
+            mma_ts(o, tmem + (uint32_t)(buf * kTile) + p_col(k), desc_sw128(vb + 2048u * k, C::kCbBytes), id_pv,
+                   !first || k > 0);
+        }
+        mma_commit(pv_done(b));
+      }
+      __syncwarp();
+    };
+    const auto wait_stages = [&](int at) {
+#pragma unroll
+      for (int p = 0; p < C::kParts; ++p)
+        mbar_wait(full((at + p) % C::kStages), (uint32_t)(((at + p) / C::kStages) & 1), abort);
+    };
+    // V rows of the last step that lie behind the keys: zero (the probabilities there are zero,
+    // but what the memory holds need not be finite)
+    const auto clear_tail = [&](int at, int keys) {
+      if (keys % 16 == 0 || stopped()) return;
+      const int r0 = keys, r1 = (keys + 15) & ~15;
+      for (int i = lane; i < (r1 - r0) * C::kCb * C::kParts * 8; i += 32) {
+        const int chunk = i & 7, cb = (i >> 3) % (C::kCb * C::kParts), r = r0 + (i >> 3) / (C::kCb * C::kParts);
+        const uint32_t p = stage_at((at + cb / C::kCb) % C::kStages) +
+                           (uint32_t)((cb % C::kCb) * C::kCbBytes + r * 128 + chunk * 16);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+      if (w.end == 0) continue;
+      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
+      const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
+      mbar_wait(q_full, (uint32_t)(units & 1), abort);
+      ++units;
+      if constexpr (NB == 2) {
+        wait_stages(it);
+        for (int b = 0; b < blocks; ++b) qk(b, b, it);
+        release(it % C::kStages);
+        ++it;
+        if (w.t1 - w.t0 == 1) q_done();
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
+          const int vs = it, ks = it + 1;
+          const bool more = t + 1 < w.t1;
+          wait_stages(vs);
+          clear_tail(vs, keys);
+          for (int b = 0; b < blocks; ++b) {
+            mbar_wait(p_full(b), (uint32_t)(tiles[b] & 1), abort);
+            if (t == w.t0 && outs[b]) mbar_wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1), abort);
+            pv(b, b, vs, (keys + 15) / 16, t == w.t0);
+            if (more) {
+              if (b == 0) wait_stages(ks);
+              qk(b, b, ks);
+            }
+            ++tiles[b];
+          }
+          release(vs % C::kStages);
+          if (more) release(ks % C::kStages);
+          if (t + 2 == w.t1) q_done();
+          it += more ? 2 : 1;
+        }
+        for (int b = 0; b < blocks; ++b) ++outs[b];
+      } else {
+        wait_stages(it);
+        qk(0, tiles[0] & 1, it);
+        for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
+        it += C::kParts;
+        if (w.t1 - w.t0 == 1) q_done();
+        for (int t = w.t0; t < w.t1; ++t) {
+          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
+          if (t + 1 < w.t1) {
+            wait_stages(it);
+            qk(0, (tiles[0] + 1) & 1, it);
+            for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
+            it += C::kParts;
+            if (t + 2 == w.t1) q_done();
+          }
+          wait_stages(it);
+          clear_tail(it, keys);
+          mbar_wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1), abort);
+          if (t == w.t0 && outs[0]) mbar_wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1), abort);
+          pv(0, tiles[0] & 1, it, (keys + 15) / 16, t == w.t0);
+          for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
+          it += C::kParts;
+          ++tiles[0];
+        }
+        ++outs[0];
+      }
+    }
+    // every product has completed before tensor memory is freed
+    if (lane == 0) {
+      mma_commit(drain);
+      mbar_drain(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    constexpr int kCols = NB == 2 ? 128 : 64;  // key columns of a thread
+    constexpr int kOut = NB == 2 ? D : 128;    // output columns of a thread
+    const int wg = warp >> 2, sub = warp & 3, row = sub * 32 + lane;
+    const int block = NB == 2 ? wg : 0, c0 = NB == 2 ? 0 : wg * 64;
+    const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+    const uint32_t o_at = tmem + lanes + C::kO + (uint32_t)(NB == 2 ? block * D : wg * 128);
+    int tiles = 0;  // tiles of this block
+    int flags = 0;
+    AttnRec rec{};
+    AttnWalk w;
+    const auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + sub) : "memory"); };
+    for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
+      const bool whole = w.whole();
+      if (!whole) {
+        if (w.t0 > 0) {
+          flags |= kRecHead | (w.t1 == w.n ? kRecEnd : 0);
+        } else {
+          flags |= kRecTail;
+          rec.q0 = w.q.q0;
+          rec.rows = rows;
+          rec.base = first;
+          rec.head = w.h;
+        }
+      }
+      if (NB == 2 && block == 1 && first + a.block_used >= rows) continue;  // no rows in block B
+      const int p = row < a.block_used && first + block * a.block_used + row < rows
+                        ? first + block * a.block_used + row
+                        : -1;
+      const bool live = __any_sync(0xffffffffu, p >= 0);  // dead warps only keep the barriers
+      const int lim = p >= 0 ? attn_seen(w.q, p / a.group) : 0;
+      float m = -INFINITY, l = 0.f;
+      if (w.end > 0) {
+        for (int t = w.t0; t < w.t1; ++t, ++tiles) {
+          const int buf = NB == 2 ? block : tiles & 1;
+          const uint32_t s_at = tmem + lanes + (uint32_t)(buf * kTile + c0);
+          mbar_wait(s_full(buf), (uint32_t)((NB == 2 ? tiles : tiles >> 1) & 1), abort);
+          tc_after();
+          if (live) {
+            uint32_t s[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) tmem_ld32(s_at + c, s + c);
+            tc_wait_ld();
+            const int seen = lim - t * kTile - c0;  // of this thread's columns
+            if (seen < kCols) {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c)
+                if (c >= seen) s[c] = 0xff800000u;  // -infinity
+            }
+            float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8) {
+              x0 = fmaxf(x0, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+              x1 = fmaxf(x1, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
+              x2 = fmaxf(x2, fmaxf(__uint_as_float(s[c + 4]), __uint_as_float(s[c + 5])));
+              x3 = fmaxf(x3, fmaxf(__uint_as_float(s[c + 6]), __uint_as_float(s[c + 7])));
+            }
+            float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
+            if constexpr (NB == 1) {
+              // the other half's maximum of the row (buffers alternate: one barrier per tile)
+              float* const ex = s_max + (tiles & 1) * 256;
+              ex[wg * 128 + row] = mx;
+              pair_sync();
+              mx = fmaxf(mx, ex[(wg ^ 1) * 128 + row]);
+            }
+            if (__any_sync(0xffffffffu, mx > m + kLag)) {
+              const float up = fmaxf(m, mx);
+              const float f = m == up ? 1.f : ex2(m - up);  // equal infinities: nothing to rescale
+              m = up;
+              l *= f;
+              if (t > w.t0) {
+                // O = P V up to the last tile; with two S buffers that product may still run
+                if (NB == 1) {
+                  mbar_wait(pv_done(0), (uint32_t)((tiles - 1) & 1), abort);
+                  tc_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < kOut; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(o_at + c, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(o_at + c, o);
+                }
+              }
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const uint64_t sc = f2(a.scale_log2, a.scale_log2), off = f2(kOff - mm, kOff - mm);
+            uint64_t l0 = 0, l1 = 0;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 64) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float e0, e1;
+                un2(fma2(f2(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), sc, off), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                if (i & 1)
+                  l1 = add2(l1, f2(e0, e1));
+                else
+                  l0 = add2(l0, f2(e0, e1));
+                pk[i] = pack2<T>(e0, e1);
+              }
+              tmem_st32(s_at + c, pk);
+            }
+            float y0, y1;
+            un2(add2(l0, l1), y0, y1);
+            l += y0 + y1;
+            tc_wait_st();
+          }
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(buf));
+        }
+      }
+      // the unit's output, or its part of it
+      float inv = 0.f;
+      if (w.end > 0) {
+        // with two S buffers the product before the last may still run, too: its phase first
+        if (NB == 1 && w.t1 - w.t0 > 1) mbar_wait(pv_done(block), (uint32_t)(tiles & 1), abort);
+        mbar_wait(pv_done(block), (uint32_t)((tiles - 1) & 1), abort);
+        tc_after();
+      }
+      if (live) {
+        if constexpr (NB == 1) {
+          // the halves' sums
+          float* const ex = s_max + (tiles & 1) * 256;
+          ex[wg * 128 + row] = l;
+          pair_sync();
+          l += ex[(wg ^ 1) * 128 + row];
+          pair_sync();
+        }
+        inv = l == 0.f ? 0.f : 1.f / l;
+        const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        const size_t at = (size_t)slot * (NB * 128) + block * 128 + row;
+        const RowPlace rp = row_place(a, w.q.q0, w.h, p < 0 ? 0 : p);
+        T* const dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + (NB == 2 ? 0 : wg * 128);
+        float* const part = a.part + at * D + (NB == 2 ? 0 : wg * 128);
+        const bool ok = p >= 0 && VQ3_IN(rp.token, a.tokens, 2) && VQ3_IN(at, (size_t)2 * gridDim.x * NB * 128, 3);
+#pragma unroll 1
+        for (int c = 0; c < kOut; c += 32) {
+          uint32_t o[32];
+          if (w.end > 0) {
+            tmem_ld32(o_at + c, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (ok && whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 y;
+              y.x = pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              y.y = pack2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+              y.z = pack2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+              y.w = pack2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+              *reinterpret_cast<uint4*>(dst + c + i) = y;
+            }
+          } else if (ok) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              __stcg(reinterpret_cast<float4*>(part + c + i),
+                     make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                 __uint_as_float(o[i + 3])));
+          }
+        }
+        if (ok && (NB == 2 || wg == 0)) {
+          if (!whole)
+            __stcg(reinterpret_cast<float2*>(a.part_ml + 2 * at), make_float2(m, l));
+          else if (a.lse)
+            a.lse[rp.token * a.heads + rp.head] =
+                l == 0.f ? -INFINITY : (m - kOff + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      if (w.end > 0) {
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty(block));
+      }
+    }
+    if (tid == 0) {
+      rec.flags = flags;
+      a.rec[blockIdx.x] = rec;
+    }
+  }
+
+  tc_before();
+  __syncthreads();
+  if (tid == 0 && *abort) a.rec[blockIdx.x].flags = kRecFailed;
+  if (warp == kMmaWarp) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- launch
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// 64 columns x box[1] x box[2] x box[3] of a 16-bit tensor, 128-byte swizzle; outside reads as zeros.
+bool tensor_map(CUtensorMap* m, bool bf16, const void* p, int rank, const cuuint64_t* dims, const long long* strides,
+                const cuuint32_t* box) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  cuuint64_t bytes[3];
+  for (int i = 0; i + 1 < rank; ++i) bytes[i] = (cuuint64_t)strides[i] * 2;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+             const_cast<void*>(p), dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_wide(const AttnArgs& a, cudaStream_t st) {
+  constexpr bool bf16 = AttnType<T>::kBf16;
+  constexpr int smem = WideCfg<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_wide_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  alignas(64) WideMaps maps;
+  const int page = 1 << a.page_shift;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.heads, (cuuint64_t)a.tokens};
+    const long long strides[2] = {a.q_head, a.q_token};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(a.block_used / a.group)};
+    if (!tensor_map(&maps.q, bf16, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(a.table ? page : a.tokens), (cuuint64_t)a.kv_heads,
+                              (cuuint64_t)(a.table ? a.n_pages : 1)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(a.table && page < kTile ? page : kTile), 1, 1};
+  const long long ks[3] = {a.k_token, a.k_head, a.table ? a.k_page : D};
+  const long long vs[3] = {a.v_token, a.v_head, a.table ? a.v_page : D};
+  if (!tensor_map(&maps.k, bf16, a.k, 4, dims, ks, box) || !tensor_map(&maps.v, bf16, a.v, 4, dims, vs, box))
+    return cudaErrorInvalidValue;
+  attn_wide_kernel<T, D><<<attn_wide_grid(), kThreads, smem, st>>>(a, maps);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_wide_t(const AttnArgs& a, int d, cudaStream_t st) {
+  if (d == 64) return launch_wide<T, 64>(a, st);
+  if (d == 128) return launch_wide<T, 128>(a, st);
+  return launch_wide<T, 256>(a, st);
+}
+
+}  // namespace
+
+int attn_wide_grid() { return device_sm_count(); }
+int attn_wide_blocks(int head_dim) { return head_dim == 256 ? 1 : 2; }
+
+cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st) {
+  return bf16 ? launch_wide_t<__nv_bfloat16>(a, head_dim, st) : launch_wide_t<__half>(a, head_dim, st);
+}
+
 }  // namespace vq3
