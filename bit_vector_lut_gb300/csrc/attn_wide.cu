@@ -33,7 +33,10 @@ namespace {
 constexpr int kTile = 128;      // keys per tile
 constexpr int kMinTiles = 2;    // fewest tiles per CTA
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kThreads = 12 * 32;  // warps 10 and 11 fill up the third warpgroup
+// Registers per thread: at launch 168; the softmax warpgroups take what the third gives up.
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares come from the launch's registers");
 constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after one second
 constexpr unsigned long long kDrainNs = 100000000ull;   // the end-of-kernel drain waits at most 0.1 s
 
@@ -63,16 +66,23 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for the phase of parity `parity`, at most kWaitNs. `abort`: the CTA's shared flag;
-// once a wait gave up, every wait returns at once.
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return;
-  const unsigned long long t0 = globaltimer_ns();
+// Waits for the phase of parity `parity`, at most kWaitNs (the clock is read only every 256
+// polls: a read stalls the warp for longer than a tile's wait). `abort`: the CTA's shared
+// flag; once a wait gave up, every wait returns at once. False: it gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = 0;
   for (unsigned it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity) || *abort) return;
-    if ((it & 63u) == 0u && globaltimer_ns() - t0 > kWaitNs) {
-      *abort = 1;
-      return;
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0u && *abort) return false;
+    if ((it & 255u) == 0u) {
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitNs) {
+        *abort = 1;
+        return false;
+      }
     }
   }
 }
@@ -118,20 +128,52 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// Products and commits are issued by the whole converged warp through elect.sync, four K = 16
+// steps to an asm block: issued lane by lane from a divergent branch, each one stalled the
+// tensor pipe for hundreds of cycles.
+// D (+)= A B over 64 columns of K, A and B from shared memory (32 bytes a step).
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "{\n .reg .pred p, q, e;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.u64 a1, %1, 2;\n add.u64 a2, %1, 4;\n add.u64 a3, %1, 6;\n"
+      " add.u64 b1, %2, 2;\n add.u64 b2, %2, 4;\n add.u64 b3, %2, 6;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// D (+)= A B over 64 rows of K, A from tensor memory (8 columns a step), B MN-major (2 KB a step).
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "{\n .reg .pred p, q, e;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+      " add.u64 b1, %2, 128;\n add.u64 b2, %2, 256;\n add.u64 b3, %2, 384;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// One step of the same.
+__device__ __forceinline__ void mma_ts1(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
 }
 #define VQ3_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
 #define VQ3_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
@@ -195,6 +237,19 @@ struct WideCfg {
 // that it was made from.
 __device__ __forceinline__ uint32_t p_col(int step) { return (uint32_t)(step < 4 ? 8 * step : 64 + 8 * (step - 4)); }
 
+// Place in a ring of N stages: the stage and the parity of its current use.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Ring plus(int n) const {
+    Ring r;
+    r.s = s + n < N ? s + n : s + n - N;
+    r.phase = s + n < N ? phase : phase ^ 1u;
+    return r;
+  }
+};
+
 struct WideMaps {
   CUtensorMap q, k, v;
 };
@@ -257,24 +312,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   tc_after();
   const uint32_t tmem = *s_tmem;
   const AttnPos pos = *s_pos;
-  // Whether a wait gave up, the same answer for the whole warp. The copy and MMA warps then issue
-  // nothing more; the softmax warps, which meet at barriers, walk on over what is there.
-  const auto stopped = [&] { return __shfl_sync(0xffffffffu, *abort, 0) != 0; };
+  // Once a wait gave up (`dead`, the same for the whole warp), the copy and MMA warps issue nothing
+  // more; the softmax warps, which meet at barriers, walk on over what is there.
+  bool dead = false;
+  const auto wait = [&](uint32_t bar, uint32_t parity) {
+    dead = __any_sync(0xffffffffu, !mbar_wait(bar, parity, abort)) || dead;
+  };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ copies
     const int box = a.table ? (1 << a.page_shift < kTile ? 1 << a.page_shift : kTile) : kTile;  // rows per copy
     const int boxes = kTile / box;
     const int my_box = lane & (boxes - 1), my_cb = lane / boxes;  // this lane's copy of a stage
     const int tt = a.block_used / a.group;                        // tokens of a row block
+    Ring<C::kStages> at;
     int it = 0, units = 0;
     AttnWalk w;
     for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
       if (w.end == 0) continue;
       const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
-      if (units) mbar_wait(q_empty, (uint32_t)((units - 1) & 1), abort);
-      if (stopped()) break;
+      if (units) wait(q_empty, (uint32_t)((units - 1) & 1));
+      if (dead) break;
       const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
       if (lane == 0) {
         mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.block_used * 128));
@@ -297,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
         const int x = t * kTile + my_box * box;
         const int row = a.table ? x & ((1 << a.page_shift) - 1) : w.q.q0 + x;
 #pragma unroll
-        for (int part = 0; part < C::kParts; ++part, ++it) {
-          const int s = it % C::kStages;
-          if (it >= C::kStages) mbar_wait(empty(s), (uint32_t)((it / C::kStages - 1) & 1), abort);
-          if (stopped()) return;
+        for (int part = 0; part < C::kParts; ++part, ++it, at = at.plus(1)) {
+          const int s = at.s;
+          if (it >= C::kStages) wait(empty(s), at.phase ^ 1u);
+          if (dead) return;
           if (lane == 0) mbar_expect_tx(full(s), (uint32_t)(n * C::kCb * box * 128));
           __syncwarp();
           if (my_box < n && my_cb < C::kCb)
@@ -335,63 +396,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
+    using Place = Ring<C::kStages>;
+    Place it;  // the next stage to use
     constexpr uint32_t id_qk = idesc(kTile, kBf16, false), id_pv = idesc(C::kStageCols, kBf16, true);
-    int it = 0, units = 0;     // stages used, units
+    int units = 0;
     int tiles[2] = {0, 0};     // tiles of block b (NB == 2), all tiles (NB == 1, [0])
     int outs[2] = {0, 0};      // units of block b
     AttnWalk w;
-    const auto release = [&](int s) {
-      if (lane == 0) mma_commit(empty(s));
+    const auto release = [&](Place at) {
+#pragma unroll
+      for (int p = 0; p < C::kParts; ++p) mma_commit(empty(at.plus(p).s));
     };
     const auto q_done = [&] {  // the unit's last Q K^T is issued
-      if (lane == 0) mma_commit(q_empty);
+      mma_commit(q_empty);
     };
     // S buffer `buf` = Q of block b times stages it .. it + kParts - 1
-    const auto qk = [&](int b, int buf, int at) {
-      if (stopped()) return;
+    const auto qk = [&](int b, int buf, Place at) {
+      if (dead) return;
       tc_after();
-      if (lane == 0) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint32_t kb = stage_at((at + c / C::kCb) % C::kStages) + (uint32_t)((c % C::kCb) * C::kCbBytes);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, c) + 32u * k, 16), desc_sw128(kb + 32u * k, 16),
-                   id_qk, c + k > 0);
-        }
-        mma_commit(s_full(buf));
-      }
-      __syncwarp();
+      for (int c = 0; c < D / 64; ++c)
+        mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, c), 16),
+                desc_sw128(stage_at(at.plus(c / C::kCb).s) + (uint32_t)((c % C::kCb) * C::kCbBytes), 16), id_qk, c > 0);
+      mma_commit(s_full(buf));
     };
-    const auto pv = [&](int b, int buf, int at, int steps, bool first) {
-      if (stopped()) return;
+    const auto pv = [&](int b, int buf, Place at, int steps, bool first) {
+      if (dead) return;
       tc_after();
-      if (lane == 0) {
+      const uint32_t p = tmem + (uint32_t)(buf * kTile);
 #pragma unroll
-        for (int part = 0; part < C::kParts; ++part) {
-          const uint32_t vb = stage_at((at + part) % C::kStages);
-          const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
-          for (int k = 0; k < steps; ++k)
-            mma_ts(o, tmem + (uint32_t)(buf * kTile) + p_col(k), desc_sw128(vb + 2048u * k, C::kCbBytes), id_pv,
-                   !first || k > 0);
+      for (int part = 0; part < C::kParts; ++part) {
+        const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
+        const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
+        if (steps == 8) {
+          mma_ts4(o, p, v, id_pv, !first);
+          mma_ts4(o, p + 64, v + 512, id_pv, 1);
+        } else {
+          for (int k = 0; k < steps; ++k) mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
         }
-        mma_commit(pv_done(b));
       }
-      __syncwarp();
+      mma_commit(pv_done(b));
     };
-    const auto wait_stages = [&](int at) {
+    const auto wait_stages = [&](Place at) {
 #pragma unroll
-      for (int p = 0; p < C::kParts; ++p)
-        mbar_wait(full((at + p) % C::kStages), (uint32_t)(((at + p) / C::kStages) & 1), abort);
+      for (int p = 0; p < C::kParts; ++p) wait(full(at.plus(p).s), at.plus(p).phase);
     };
     // V rows of the last step that lie behind the keys: zero (the probabilities there are zero,
     // but what the memory holds need not be finite)
-    const auto clear_tail = [&](int at, int keys) {
-      if (keys % 16 == 0 || stopped()) return;
+    const auto clear_tail = [&](Place at, int keys) {
+      if (keys % 16 == 0 || dead) return;
       const int r0 = keys, r1 = (keys + 15) & ~15;
       for (int i = lane; i < (r1 - r0) * C::kCb * C::kParts * 8; i += 32) {
         const int chunk = i & 7, cb = (i >> 3) % (C::kCb * C::kParts), r = r0 + (i >> 3) / (C::kCb * C::kParts);
-        const uint32_t p = stage_at((at + cb / C::kCb) % C::kStages) +
+        const uint32_t p = stage_at(at.plus(cb / C::kCb).s) +
                            (uint32_t)((cb % C::kCb) * C::kCbBytes + r * 128 + chunk * 16);
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
       }
@@ -402,23 +459,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       if (w.end == 0) continue;
       const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
       const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
-      mbar_wait(q_full, (uint32_t)(units & 1), abort);
+      wait(q_full, (uint32_t)(units & 1));
       ++units;
       if constexpr (NB == 2) {
         wait_stages(it);
-        for (int b = 0; b < blocks; ++b) qk(b, b, it);
-        release(it % C::kStages);
-        ++it;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (b < blocks) qk(b, b, it);
+        release(it);
+        it = it.plus(1);
         if (w.t1 - w.t0 == 1) q_done();
         for (int t = w.t0; t < w.t1; ++t) {
           const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
-          const int vs = it, ks = it + 1;
+          const Place vs = it, ks = it.plus(1);
           const bool more = t + 1 < w.t1;
           wait_stages(vs);
           clear_tail(vs, keys);
-          for (int b = 0; b < blocks; ++b) {
-            mbar_wait(p_full(b), (uint32_t)(tiles[b] & 1), abort);
-            if (t == w.t0 && outs[b]) mbar_wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1), abort);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (b >= blocks) continue;
+            wait(p_full(b), (uint32_t)(tiles[b] & 1));
+            if (t == w.t0 && outs[b]) wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1));
             pv(b, b, vs, (keys + 15) / 16, t == w.t0);
             if (more) {
               if (b == 0) wait_stages(ks);
@@ -426,47 +487,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
             }
             ++tiles[b];
           }
-          release(vs % C::kStages);
-          if (more) release(ks % C::kStages);
+          release(vs);
+          if (more) release(ks);
           if (t + 2 == w.t1) q_done();
-          it += more ? 2 : 1;
+          it = it.plus(more ? 2 : 1);
         }
-        for (int b = 0; b < blocks; ++b) ++outs[b];
+        ++outs[0];
+        if (blocks == 2) ++outs[1];
       } else {
         wait_stages(it);
         qk(0, tiles[0] & 1, it);
-        for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
-        it += C::kParts;
+        release(it);
+        it = it.plus(C::kParts);
         if (w.t1 - w.t0 == 1) q_done();
         for (int t = w.t0; t < w.t1; ++t) {
           const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
           if (t + 1 < w.t1) {
             wait_stages(it);
             qk(0, (tiles[0] + 1) & 1, it);
-            for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
-            it += C::kParts;
+            release(it);
+            it = it.plus(C::kParts);
             if (t + 2 == w.t1) q_done();
           }
           wait_stages(it);
           clear_tail(it, keys);
-          mbar_wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1), abort);
-          if (t == w.t0 && outs[0]) mbar_wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1), abort);
+          wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1));
+          if (t == w.t0 && outs[0]) wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1));
           pv(0, tiles[0] & 1, it, (keys + 15) / 16, t == w.t0);
-          for (int p = 0; p < C::kParts; ++p) release((it + p) % C::kStages);
-          it += C::kParts;
+          release(it);
+          it = it.plus(C::kParts);
           ++tiles[0];
         }
         ++outs[0];
       }
     }
     // every product has completed before tensor memory is freed
-    if (lane == 0) {
-      mma_commit(drain);
-      mbar_drain(drain, 0);
-    }
+    mma_commit(drain);
+    mbar_drain(drain, 0);
     __syncwarp();
+  }
   } else {
     // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     constexpr int kCols = NB == 2 ? 128 : 64;  // key columns of a thread
     constexpr int kOut = NB == 2 ? D : 128;    // output columns of a thread
     const int wg = warp >> 2, sub = warp & 3, row = sub * 32 + lane;
