@@ -30,7 +30,7 @@ constexpr int kMinTiles = 2;        // fewest tiles per CTA
 // CTAs per SM: what registers allow (Q, O, and one group's K and V per thread).
 template <int D, int NR>
 constexpr int rows_occ() {
-  return D == 256 ? 2 : (D == 128 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 5 : 4));
+  return D == 256 ? 2 : (D == 128 ? (NR == 1 ? 3 : 2) : 4);
 }
 
 template <typename T>
@@ -269,10 +269,11 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
         rec.head = w.h;
       }
     }
-    constexpr int kLanes = D / 4;  // threads of a row, four columns each
-    for (int row = tid / kLanes; row < kRows; row += kThreads / kLanes) {
-      const int d = (tid % kLanes) * 4;
-      if (base + row >= rows) break;
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+      // four columns of a row: neighbouring threads take a row's columns of the output, or the
+      // rows of a part ([slot][D / 4][rows] of four columns)
+      const int row = whole ? i / (D / 4) : i % kRows, d = (whole ? i % (D / 4) : i / kRows) * 4;
+      if (base + row >= rows) continue;
       float mx = s_m[0][row];
 #pragma unroll
       for (int v = 1; v < kWarps; ++v) mx = fmaxf(mx, s_m[v][row]);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
       } else {
         const size_t at = (size_t)slot * kRows + row;
         if (VQ3_IN(at, (size_t)2 * gridDim.x * kRows, 4)) {
-          __stcg(reinterpret_cast<float4*>(a.part + at * D + d), acc);
+          __stcg(reinterpret_cast<float4*>(a.part) + ((size_t)slot * (D / 4) + d / 4) * kRows + row, acc);
           if (d == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + 2 * at), make_float2(mx, sum));
         }
       }
@@ -314,42 +315,72 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
 
 // ---------------------------------------------------------------- combining pass
 //
-// Block (c, y) takes the unit that CTA c began and did not end, if there is one; its parts
-// are slot 2c + 1 and then slot 2c' of the CTAs behind, up to the one that ends it. Rows are
-// dealt out to the blocks y. With few parts a warp takes a row by itself, with many the
-// block's warps share a row's parts (each a fixed subset, summed in a fixed order).
-constexpr int kCWarps = 8;
-constexpr int kMaxGrid = 2048;
+// The parts of a split unit are slot 2c + 1 of the CTA c that began it and then slot 2c' of the
+// CTAs behind, up to the one that ends it. Block (c, y) takes rows and columns y of the unit
+// that CTA c began, if it did. A thread sums four columns of a row over the parts with a
+// running maximum, in CTA order; the row kernel's units, of few rows and often very many
+// parts, get 32 columns a block and four groups of threads, each a fixed quarter of the
+// parts. Bound by latency: the records, then the parts, three dependent reads in all.
+constexpr int kCThreads = 256;
+constexpr int kMaxGrid = 608;  // CTAs of an attention kernel
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kCWarps * 32) attn_combine_kernel(const __grid_constant__ AttnArgs a, int grid,
-                                                                    int slot_rows) {
-  __shared__ int s_parts[kMaxGrid];
+struct Merge {  // running maximum (log2 domain), sum and four columns
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float pm, float pl, float4 po) {
+    const float up = fmaxf(m, pm);
+    const float f = m == up ? 1.f : ex2(m - up), g = pm == up ? 1.f : ex2(pm - up);
+    m = up;
+    l = l * f + pl * g;
+    o.x = o.x * f + po.x * g;
+    o.y = o.y * f + po.y * g;
+    o.z = o.z * f + po.z * g;
+    o.w = o.w * f + po.w * g;
+  }
+};
+
+template <bool kWide, int D>
+struct CombineCfg {
+  static constexpr int kRows = kWide ? 16 : 8;     // rows of a block
+  static constexpr int kQuads = kWide ? D / 4 : 8;  // its columns, in fours
+  static constexpr int kGroups = kWide ? 1 : 4;     // groups of threads that share the parts
+  static constexpr int kStep = kCThreads / kRows / kGroups;  // fours per pass over the columns
+  static constexpr int kPasses = kQuads / kStep;
+};
+
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int grid,
+                                                                 int slot_rows) {
+  using C = CombineCfg<kWide, D>;
+  __shared__ short s_parts[kMaxGrid];
   __shared__ int s_n;
-  __shared__ float s_m[kCWarps], s_l[kCWarps];
-  __shared__ __align__(16) float s_o[kCWarps][D];
-  constexpr int kPer = D / 32;  // columns of a lane
+  __shared__ Merge s_merge[C::kGroups > 1 ? C::kGroups - 1 : 1][64];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  constexpr int kAcross = D / 4 / C::kQuads;  // blocks over the columns
+  const int row0 = (int)blockIdx.y / kAcross * C::kRows, q0 = (int)blockIdx.y % kAcross * C::kQuads;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel has ended
+  // from L2 throughout: this block may have started before the records were written
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + c));  // flags, q0, rows, base
+  const int head = __ldcg(&a.rec[c].head);
   if (c == 0 && blockIdx.y == 0) {
     // the workspace's status word: whether a wait of any CTA gave up
     int failed = 0;
-    for (int i = tid; i < grid; i += kCWarps * 32) failed |= __ldcg(&a.rec[i].flags) & kRecFailed;
+    for (int i = tid; i < grid; i += kCThreads) failed |= __ldcg(&a.rec[i].flags) & kRecFailed;
     failed = __syncthreads_or(failed);
     if (tid == 0) *a.status = failed ? 3 : 0;
   }
-  if (!(__ldcg(&a.rec[c].flags) & kRecTail)) return;
+  if (!(rec.x & kRecTail) || attn_packed_row(row0, rec.w, rec.z, a.block_rows, a.block_used) < 0) return;
   if (warp == 0) {
-    // the slots of the unit, in CTA order
+    // the unit's slots, in CTA order
     int n = 1;
-    if (lane == 0) s_parts[0] = 2 * c + 1;
+    if (lane == 0) s_parts[0] = (short)(2 * c + 1);
     for (int i0 = c + 1; i0 < grid; i0 += 32) {
       const int i = i0 + lane;
       const int f = i < grid ? __ldcg(&a.rec[i].flags) : 0;
       const unsigned ends = __ballot_sync(0xffffffffu, (f & (kRecHead | kRecEnd)) == (kRecHead | kRecEnd));
       const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;
       const unsigned has = __ballot_sync(0xffffffffu, f & kRecHead) & upto;
-      if (has >> lane & 1) s_parts[n + __popc(has & ((1u << lane) - 1u))] = 2 * i;
+      if (has >> lane & 1) s_parts[n + __popc(has & ((1u << lane) - 1u))] = (short)(2 * i);
       n += __popc(has);
       if (ends) break;
     }
@@ -357,90 +388,55 @@ __global__ void __launch_bounds__(kCWarps * 32) attn_combine_kernel(const __grid
   }
   __syncthreads();
   const int n = s_n;
-  const AttnRec rec = a.rec[c];
-  const bool shared = n > 8;
-  const int n_warps = shared ? 1 : kCWarps;
-  for (int row = blockIdx.y * n_warps + (shared ? 0 : warp); row < slot_rows; row += gridDim.y * n_warps) {
-    const int p = attn_packed_row(row, rec.base, rec.rows, a.block_rows, a.block_used);
-    if (p < 0) continue;  // the same for all warps that share the row
-    float mx = -INFINITY, sum = 0.f, acc[kPer];
+  const int row = row0 + tid % C::kRows, group = C::kGroups > 1 ? tid / 64 : 0;
+  const int quad = q0 + tid / C::kRows % C::kStep;
+  const int p = attn_packed_row(row, rec.w, rec.z, a.block_rows, a.block_used);
+  const float4* const src = reinterpret_cast<const float4*>(a.part) + (size_t)quad * slot_rows + row;
+  const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + row;
+  Merge acc[C::kPasses];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    const int step = shared ? kCWarps : 1;
-    for (int i = shared ? warp : 0; i < n; i += step) {
-      const size_t at = (size_t)s_parts[i] * slot_rows + row;
-      mx = fmaxf(mx, __ldcg(a.part_ml + 2 * at));
-    }
+  for (int k = 0; k < C::kPasses; ++k) acc[k] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (p >= 0) {
 #pragma unroll 4
-    for (int i = shared ? warp : 0; i < n; i += step) {
-      const size_t at = (size_t)s_parts[i] * slot_rows + row;
-      if (!VQ3_IN(at, (size_t)2 * grid * slot_rows, 5)) continue;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + 2 * at));
-      const float f = ml.x == mx ? 1.f : ex2(ml.x - mx);
-      sum += f * ml.y;
-      const float* src = a.part + at * D + lane * kPer;
-      if constexpr (kPer == 2) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        acc[0] += f * x.x;
-        acc[1] += f * x.y;
-      } else {
+    for (int i = group; i < n; i += C::kGroups) {
+      const size_t slot = s_parts[i];
+      if (!VQ3_IN(slot, 2 * grid, 5)) continue;
+      const float2 x = __ldcg(ml + slot * slot_rows);
 #pragma unroll
-        for (int v = 0; v < kPer / 4; ++v) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 4 * v));
-          acc[4 * v] += f * x.x;
-          acc[4 * v + 1] += f * x.y;
-          acc[4 * v + 2] += f * x.z;
-          acc[4 * v + 3] += f * x.w;
-        }
-      }
+      for (int k = 0; k < C::kPasses; ++k)
+        acc[k].add(x.x, x.y, __ldcg(src + (slot * (D / 4) + k * C::kStep) * slot_rows));
     }
-    if (shared) {
-      __syncthreads();  // the previous row's sums have been read
-      if (lane == 0) {
-        s_m[warp] = mx;
-        s_l[warp] = sum;
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i];
-      __syncthreads();
-      if (warp) continue;
-      mx = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < kCWarps; ++v) mx = fmaxf(mx, s_m[v]);
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int v = 0; v < kCWarps; ++v) {
-        const float f = s_m[v] == mx ? 1.f : ex2(s_m[v] - mx);
-        sum += f * s_l[v];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += f * s_o[v][lane * kPer + i];
-      }
-    }
-    const RowPlace rp = row_place(a, rec.q0, rec.head, p);
-    if (!VQ3_IN(rp.token, a.tokens, 6)) continue;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T* dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + lane * kPer;
-    uint32_t y[kPer / 2];
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) y[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if constexpr (kPer == 2)
-      *reinterpret_cast<uint32_t*>(dst) = y[0];
-    else if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-    else
-      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (a.lse && lane == 0)
-      a.lse[rp.token * a.heads + rp.head] =
-          sum == 0.f ? -INFINITY : (mx - AttnType<T>::kOff + log2f(sum)) * 0.6931471805599453f;
   }
+  if constexpr (C::kGroups > 1) {
+    if (group) s_merge[group - 1][tid & 63] = acc[0];
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int v = 0; v < C::kGroups - 1; ++v) {
+      const Merge x = s_merge[v][tid];
+      acc[0].add(x.m, x.l, x.o);
+    }
+  }
+  if (p < 0) return;
+  const RowPlace rp = row_place(a, rec.y, head, p);
+  if (!VQ3_IN(rp.token, a.tokens, 6)) return;
+  T* const dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head;
+  const float sum = acc[0].l, inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < C::kPasses; ++k) {
+    uint2 y;
+    y.x = pack2<T>(acc[k].o.x * inv, acc[k].o.y * inv);
+    y.y = pack2<T>(acc[k].o.z * inv, acc[k].o.w * inv);
+    *reinterpret_cast<uint2*>(dst + 4 * (quad + k * C::kStep)) = y;
+  }
+  if (a.lse && quad == 0)
+    a.lse[rp.token * a.heads + rp.head] =
+        sum == 0.f ? -INFINITY : (acc[0].m - AttnType<T>::kOff + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D, int NR>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
-  const int grid = rows_occ<D, NR>() * device_sm_count();
-  attn_rows_kernel<T, D, NR><<<grid, kThreads, 0, st>>>(a);
+  attn_rows_kernel<T, D, NR><<<attn_rows_grid(D, 8 * NR), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -450,25 +446,26 @@ cudaError_t launch_rows_t(const AttnArgs& a, int d, int nr, cudaStream_t st) {
   return launch_rows<T, 256, 1>(a, st);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWide>
 cudaError_t launch_combine(const AttnArgs& a, int grid, int slot_rows, cudaStream_t st) {
+  using C = CombineCfg<kWide, D>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 8);
-  cfg.blockDim = dim3(kCWarps * 32);
+  cfg.gridDim = dim3(grid, slot_rows / C::kRows * (D / 4 / C::kQuads));
+  cfg.blockDim = dim3(kCThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the attention kernel
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, grid, slot_rows);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D, kWide>, a, grid, slot_rows);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-template <typename T>
+template <typename T, bool kWide>
 cudaError_t launch_combine_t(const AttnArgs& a, int d, int grid, int slot_rows, cudaStream_t st) {
-  if (d == 64) return launch_combine<T, 64>(a, grid, slot_rows, st);
-  if (d == 128) return launch_combine<T, 128>(a, grid, slot_rows, st);
-  return launch_combine<T, 256>(a, grid, slot_rows, st);
+  if (d == 64) return launch_combine<T, 64, kWide>(a, grid, slot_rows, st);
+  if (d == 128) return launch_combine<T, 128, kWide>(a, grid, slot_rows, st);
+  return launch_combine<T, 256, kWide>(a, grid, slot_rows, st);
 }
 
 }  // namespace
@@ -490,8 +487,11 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int head_dim, bool bf16, int nr,
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int head_dim, bool bf16, int grid, int slot_rows,
                                 cudaStream_t st) {
-  return bf16 ? launch_combine_t<__nv_bfloat16>(a, head_dim, grid, slot_rows, st)
-              : launch_combine_t<__half>(a, head_dim, grid, slot_rows, st);
+  if (slot_rows > 16)
+    return bf16 ? launch_combine_t<__nv_bfloat16, true>(a, head_dim, grid, slot_rows, st)
+                : launch_combine_t<__half, true>(a, head_dim, grid, slot_rows, st);
+  return bf16 ? launch_combine_t<__nv_bfloat16, false>(a, head_dim, grid, slot_rows, st)
+              : launch_combine_t<__half, false>(a, head_dim, grid, slot_rows, st);
 }
 
 }  // namespace vq3

@@ -120,8 +120,7 @@ __device__ __forceinline__ int attn_seen(const AttnRequest& q, int t) {
 }
 // Keys that the last row of unit j sees.
 __device__ __forceinline__ int attn_unit_end(const AttnArgs& a, const AttnRequest& q, int j) {
-  const long long last = (long long)(j + 1) * a.unit_rows - 1;
-  const int t = (int)(last / a.group);
+  const int t = ((j + 1) * a.unit_rows - 1) / a.group;  // tokens * heads < 2^30
   return attn_seen(q, t < q.n_new - 1 ? t : q.n_new - 1);
 }
 // Tiles of unit j; a unit that sees nothing still counts as one, its rows are written too.
@@ -250,8 +249,14 @@ __device__ __forceinline__ void attn_locate(const AttnArgs& a, int kv_tile, int 
   } else {
     long long live = total / min_tiles;
     live = live < 1 ? 1 : (live > gridDim.x ? gridDim.x : live);
-    s0 = c < live ? total * c / live : total;
-    s1 = c < live ? total * (c + 1) / live : total;
+    if (total < (1 << 20)) {  // 32 bits are enough, and a 64-bit division is slow
+      const unsigned n = (unsigned)total, l = (unsigned)live, i = (unsigned)c;
+      s0 = i < l ? n * i / l : n;
+      s1 = i < l ? n * (i + 1) / l : n;
+    } else {
+      s0 = c < live ? total * c / live : total;
+      s1 = c < live ? total * (c + 1) / live : total;
+    }
   }
   if (tid == 0) pos->tiles = cut.units ? 0 : s1 - s0;
   __syncthreads();

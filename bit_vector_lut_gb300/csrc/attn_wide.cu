@@ -15,7 +15,9 @@
 //   warps 0-3, 4-7  softmax, rescaling and output of block A / B (or keys 0-63 / 64-127)
 //   warp 8          TMA: the lanes each copy a page's rows (page numbers prefetched a tile
 //                   ahead) into a ring of stages, in the order in which the MMA warp uses them
-//   warp 9          issues the MMAs
+//   warp 9          issues the MMAs, the blocks' in turn: that keeps one block's softmax under
+//                   the other's products (two issuing warps let both softmaxes fall together,
+//                   8% slower)
 // O is rescaled only when a row's maximum rises by more than 2^8 (see kLag), by the softmax
 // warps themselves.
 // Keys behind the last that the block sees are masked in S; of V only the 16-row steps that
@@ -193,6 +195,20 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       VQ3_I8(r, 8), VQ3_I8(r, 16), VQ3_I8(r, 24), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 32 bytes, a whole sector where the address allows it (rows are 16-byte aligned at least).
+__device__ __forceinline__ void store32(void* p, const uint32_t* y) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), VQ3_I8(y, 0) : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(y[0], y[1], y[2], y[3]);
+    *(reinterpret_cast<uint4*>(p) + 1) = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+}
 // Two FP32 operations per instruction.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -280,10 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   const uint32_t q_full = bar0 + 8u * kB0, q_empty = bar0 + 8u * (kB0 + 1);
   const auto s_full = [&](int b) { return bar0 + 8u * (kB0 + 2 + b); };      // S buffer b holds scores
   const auto p_full = [&](int b) { return bar0 + 8u * (kB0 + 4 + b); };      // and now probabilities
-  const auto pv_done = [&](int b) { return bar0 + 8u * (kB0 + 6 + b); };     // P V of block b's latest tile done
+  const auto pv_done = [&](int b) { return bar0 + 8u * (kB0 + 6 + b); };     // P V done: of block b's unit, or of buffer b's tile
   const auto o_empty = [&](int b) { return bar0 + 8u * (kB0 + 8 + b); };     // O of block b read out
-  const uint32_t drain = bar0 + 8u * (kB0 + 10);
-  static_assert(kB0 + 11 <= 40, "barriers");
+  const auto p_half = [&](int b) { return bar0 + 8u * (kB0 + 10 + b); };     // two blocks: the first 64 keys' probabilities
+  const uint32_t drain = bar0 + 8u * (kB0 + 12);                             // all products
+  static_assert(kB0 + 13 <= 40, "barriers");
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -297,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       mbar_init(p_full(b), NB == 2 ? 4 : 8);
       mbar_init(pv_done(b), 1);
       mbar_init(o_empty(b), NB == 2 ? 4 : 8);
+      mbar_init(p_half(b), 4);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -396,31 +414,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    using Place = Ring<C::kStages>;
-    Place it;  // the next stage to use
     constexpr uint32_t id_qk = idesc(kTile, kBf16, false), id_pv = idesc(C::kStageCols, kBf16, true);
+    using Place = Ring<C::kStages>;
+    Place it;                   // the next stage of the ring
     int units = 0;
-    int tiles[2] = {0, 0};     // tiles of block b (NB == 2), all tiles (NB == 1, [0])
-    int outs[2] = {0, 0};      // units of block b
+    int tiles[2] = {0, 0};      // tiles of block b (one block: all, [0])
+    int outs[2] = {0, 0};       // units of block b
     AttnWalk w;
-    const auto release = [&](Place at) {
-#pragma unroll
-      for (int p = 0; p < C::kParts; ++p) mma_commit(empty(at.plus(p).s));
-    };
-    const auto q_done = [&] {  // the unit's last Q K^T is issued
-      mma_commit(q_empty);
-    };
-    // S buffer `buf` = Q of block b times stages it .. it + kParts - 1
-    const auto qk = [&](int b, int buf, Place at) {
+    // S buffer `buf` = Q of block b times the stages at `at`; the last block's products release them
+    const auto qk = [&](int b, int buf, Place at, bool last) {
       if (dead) return;
       tc_after();
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, c), 16),
-                desc_sw128(stage_at(at.plus(c / C::kCb).s) + (uint32_t)((c % C::kCb) * C::kCbBytes), 16), id_qk, c > 0);
-      mma_commit(s_full(buf));
+      for (int part = 0; part < C::kParts; ++part) {
+#pragma unroll
+        for (int c = 0; c < C::kCb; ++c)
+          mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, part * C::kCb + c), 16),
+                  desc_sw128(stage_at(at.plus(part).s) + (uint32_t)(c * C::kCbBytes), 16), id_qk, part + c > 0);
+        if (part == C::kParts - 1) mma_commit(s_full(buf));
+        if (last) mma_commit(empty(at.plus(part).s));
+      }
     };
-    const auto pv = [&](int b, int buf, Place at, int steps, bool first) {
+    // O of block b (+)= P in S buffer `buf`, steps [k0, k1) of 16 keys, times the stages at `at`
+    const auto pv = [&](int b, int buf, Place at, int k0, int k1, bool first, bool last) {
       if (dead) return;
       tc_after();
       const uint32_t p = tmem + (uint32_t)(buf * kTile);
@@ -428,14 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       for (int part = 0; part < C::kParts; ++part) {
         const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
         const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
-        if (steps == 8) {
-          mma_ts4(o, p, v, id_pv, !first);
-          mma_ts4(o, p + 64, v + 512, id_pv, 1);
-        } else {
-          for (int k = 0; k < steps; ++k) mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (k0 <= 4 * h && k1 >= 4 * h + 4) {
+            mma_ts4(o, p + 64u * h, v + 512u * h, id_pv, !first || h > 0);
+          } else {
+            for (int k = k0 > 4 * h ? k0 : 4 * h; k < k1 && k < 4 * h + 4; ++k)
+              mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
+          }
         }
+        if (last) mma_commit(empty(at.plus(part).s));
       }
-      mma_commit(pv_done(b));
     };
     const auto wait_stages = [&](Place at) {
 #pragma unroll
@@ -461,60 +480,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
       wait(q_full, (uint32_t)(units & 1));
       ++units;
+      wait_stages(it);
       if constexpr (NB == 2) {
-        wait_stages(it);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          if (b < blocks) qk(b, b, it);
-        release(it);
+          if (b < blocks) qk(b, b, it, b + 1 == blocks);
         it = it.plus(1);
-        if (w.t1 - w.t0 == 1) q_done();
+        if (w.t1 - w.t0 == 1) mma_commit(q_empty);
         for (int t = w.t0; t < w.t1; ++t) {
-          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
+          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
           const Place vs = it, ks = it.plus(1);
           const bool more = t + 1 < w.t1;
           wait_stages(vs);
           clear_tail(vs, keys);
+          if (more) wait_stages(ks);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b >= blocks) continue;
-            wait(p_full(b), (uint32_t)(tiles[b] & 1));
             if (t == w.t0 && outs[b]) wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1));
-            pv(b, b, vs, (keys + 15) / 16, t == w.t0);
-            if (more) {
-              if (b == 0) wait_stages(ks);
-              qk(b, b, ks);
-            }
+            wait(p_half(b), (uint32_t)(tiles[b] & 1));
+            pv(b, b, vs, 0, steps < 4 ? steps : 4, t == w.t0, false);
+            wait(p_full(b), (uint32_t)(tiles[b] & 1));
+            pv(b, b, vs, 4, steps, false, b + 1 == blocks);
             ++tiles[b];
+            if (more)
+              qk(b, b, ks, b + 1 == blocks);
+            else
+              mma_commit(pv_done(b));
           }
-          release(vs);
-          if (more) release(ks);
-          if (t + 2 == w.t1) q_done();
+          if (t + 2 == w.t1) mma_commit(q_empty);
           it = it.plus(more ? 2 : 1);
         }
         ++outs[0];
         if (blocks == 2) ++outs[1];
       } else {
-        wait_stages(it);
-        qk(0, tiles[0] & 1, it);
-        release(it);
+        qk(0, tiles[0] & 1, it, true);
         it = it.plus(C::kParts);
-        if (w.t1 - w.t0 == 1) q_done();
+        if (w.t1 - w.t0 == 1) mma_commit(q_empty);
         for (int t = w.t0; t < w.t1; ++t) {
           const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
           if (t + 1 < w.t1) {
             wait_stages(it);
-            qk(0, (tiles[0] + 1) & 1, it);
-            release(it);
+            qk(0, (tiles[0] + 1) & 1, it, true);
             it = it.plus(C::kParts);
-            if (t + 2 == w.t1) q_done();
+            if (t + 2 == w.t1) mma_commit(q_empty);
           }
           wait_stages(it);
           clear_tail(it, keys);
-          wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1));
           if (t == w.t0 && outs[0]) wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1));
-          pv(0, tiles[0] & 1, it, (keys + 15) / 16, t == w.t0);
-          release(it);
+          wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1));
+          pv(0, tiles[0] & 1, it, 0, (keys + 15) / 16, t == w.t0, true);
+          mma_commit(pv_done(tiles[0] & 1));
           it = it.plus(C::kParts);
           ++tiles[0];
         }
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     const int block = NB == 2 ? wg : 0, c0 = NB == 2 ? 0 : wg * 64;
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
     const uint32_t o_at = tmem + lanes + C::kO + (uint32_t)(NB == 2 ? block * D : wg * 128);
-    int tiles = 0;  // tiles of this block
+    int tiles = 0, outs = 0;  // tiles and units of this block
     int flags = 0;
     AttnRec rec{};
     AttnWalk w;
@@ -581,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
             float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
 #pragma unroll
             for (int c = 0; c < kCols; c += 8) {
-              x0 = fmaxf(x0, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
-              x1 = fmaxf(x1, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
-              x2 = fmaxf(x2, fmaxf(__uint_as_float(s[c + 4]), __uint_as_float(s[c + 5])));
-              x3 = fmaxf(x3, fmaxf(__uint_as_float(s[c + 6]), __uint_as_float(s[c + 7])));
+              x0 = max3(x0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              x1 = max3(x1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+              x2 = max3(x2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+              x3 = max3(x3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
             }
             float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
             if constexpr (NB == 1) {
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
               if (t > w.t0) {
                 // O = P V up to the last tile; with two S buffers that product may still run
                 if (NB == 1) {
-                  mbar_wait(pv_done(0), (uint32_t)((tiles - 1) & 1), abort);
+                  mbar_wait(pv_done((tiles - 1) & 1), (uint32_t)(((tiles - 1) >> 1) & 1), abort);
                   tc_after();
                 }
 #pragma unroll 1
@@ -618,7 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
             }
             const float mm = m == -INFINITY ? 0.f : m;
             const uint64_t sc = f2(a.scale_log2, a.scale_log2), off = f2(kOff - mm, kOff - mm);
-            uint64_t l0 = 0, l1 = 0;
 #pragma unroll
             for (int c = 0; c < kCols; c += 64) {
               uint32_t pk[32];
@@ -628,30 +643,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
                 un2(fma2(f2(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), sc, off), e0, e1);
                 e0 = ex2(e0);
                 e1 = ex2(e1);
-                if (i & 1)
-                  l1 = add2(l1, f2(e0, e1));
-                else
-                  l0 = add2(l0, f2(e0, e1));
+                s[c + 2 * i] = __float_as_uint(e0);
+                s[c + 2 * i + 1] = __float_as_uint(e1);
                 pk[i] = pack2<T>(e0, e1);
               }
               tmem_st32(s_at + c, pk);
+              tc_wait_st();
+              tc_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(c + 64 < kCols ? p_half(buf) : p_full(buf));
+            }
+            // the row's sum, under the product
+            uint64_t l0 = 0, l1 = 0, l2 = 0, l3 = 0;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8) {
+              l0 = add2(l0, f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+              l1 = add2(l1, f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
+              l2 = add2(l2, f2(__uint_as_float(s[c + 4]), __uint_as_float(s[c + 5])));
+              l3 = add2(l3, f2(__uint_as_float(s[c + 6]), __uint_as_float(s[c + 7])));
             }
             float y0, y1;
-            un2(add2(l0, l1), y0, y1);
+            un2(add2(add2(l0, l1), add2(l2, l3)), y0, y1);
             l += y0 + y1;
-            tc_wait_st();
+          } else {
+            tc_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (NB == 2) mbar_arrive(p_half(buf));
+              mbar_arrive(p_full(buf));
+            }
           }
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(buf));
         }
       }
       // the unit's output, or its part of it
       float inv = 0.f;
       if (w.end > 0) {
-        // with two S buffers the product before the last may still run, too: its phase first
-        if (NB == 1 && w.t1 - w.t0 > 1) mbar_wait(pv_done(block), (uint32_t)(tiles & 1), abort);
-        mbar_wait(pv_done(block), (uint32_t)((tiles - 1) & 1), abort);
+        if (NB == 2)
+          mbar_wait(pv_done(block), (uint32_t)(outs & 1), abort);
+        else
+          mbar_wait(pv_done((tiles - 1) & 1), (uint32_t)(((tiles - 1) >> 1) & 1), abort);
+        ++outs;
         tc_after();
       }
       if (live) {
@@ -668,7 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
         const size_t at = (size_t)slot * (NB * 128) + block * 128 + row;
         const RowPlace rp = row_place(a, w.q.q0, w.h, p < 0 ? 0 : p);
         T* const dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + (NB == 2 ? 0 : wg * 128);
-        float* const part = a.part + at * D + (NB == 2 ? 0 : wg * 128);
+        // parts: [slot][D / 4][rows] of four columns, so that a warp's rows are written side by side
+        float4* const part = reinterpret_cast<float4*>(a.part) +
+                             ((size_t)slot * (D / 4) + (NB == 2 ? 0 : wg * 32)) * (NB * 128) + block * 128 + row;
         const bool ok = p >= 0 && VQ3_IN(rp.token, a.tokens, 2) && VQ3_IN(at, (size_t)2 * gridDim.x * NB * 128, 3);
 #pragma unroll 1
         for (int c = 0; c < kOut; c += 32) {
@@ -682,18 +715,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
           }
           if (ok && whole) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 y;
-              y.x = pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-              y.y = pack2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-              y.z = pack2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-              y.w = pack2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-              *reinterpret_cast<uint4*>(dst + c + i) = y;
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = pack2<T>(__uint_as_float(o[i + 2 * e]) * inv, __uint_as_float(o[i + 2 * e + 1]) * inv);
+              store32(dst + c + i, y);
             }
           } else if (ok) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              __stcg(reinterpret_cast<float4*>(part + c + i),
+              __stcg(part + (size_t)((c + i) / 4) * (NB * 128),
                      make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
                                  __uint_as_float(o[i + 3])));
           }
@@ -793,7 +825,7 @@ cudaError_t launch_wide_t(const AttnArgs& a, int d, cudaStream_t st) {
 
 }  // namespace
 
-int attn_wide_grid() { return device_sm_count(); }
+int attn_wide_grid() { return device_sm_count() < 608 ? device_sm_count() : 608; }
 int attn_wide_blocks(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
 cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st) {

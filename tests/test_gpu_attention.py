@@ -187,6 +187,18 @@ def test_long_request_split_over_the_gpu(vq3, heads):
         Batch(8, [(20011, new)], *heads, 64, "f16").check(vq3)
 
 
+@pytest.mark.parametrize("heads", [(16, 2, 128), (12, 2, 256)])
+def test_batch_that_memory_cannot_keep_up_with(vq3, heads):
+    # more keys and values than L2 holds, read as fast as they arrive: the copies, not the products, set the pace
+    reqs = [(9000 + 731 * i, 8) for i in range(14)]
+    b = Batch(21, reqs, *heads, 64, "f16")
+    out, lse = b.check(vq3)
+    for _ in range(20):
+        again, lse2 = b.run(vq3)
+    n = b.starts[-1]
+    assert torch.equal(out[:n], again[:n]) and torch.equal(lse[:n], lse2[:n])
+
+
 def test_wrong_max_new_is_only_slower(vq3):
     b = Batch(9, [(300, 70), (20, 1)], 8, 2, 128, 16, "f16")
     for hint in (0, 1, 3, 1000):
