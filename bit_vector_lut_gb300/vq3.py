@@ -493,30 +493,32 @@ def _want(ok: bool, msg: str) -> None:
         raise Vq3Error(-1, msg)
 
 
-def _int_arrays(device, **arrays) -> None:
-    for name, t in arrays.items():
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
-            raise Vq3Error(-1, f"{name} must be a contiguous int32 tensor on {device}")
+# The calls below take a few microseconds on the GPU in a decode step: what Python does per call is kept short.
+_INT, _LONG, _FLOAT = torch.int32, torch.int64, torch.float32
+_empty = torch.empty
 
 
-def _launch(device, stream, call, *args) -> None:
-    """call(*args, stream) with `device` current; the stream is the caller's or the device's current one."""
-    if device.type != "cuda":
-        raise Vq3Error(-1, f"tensors must be on a CUDA device, not {device}")
-    if device.index is None or device.index == torch.cuda.current_device():
-        rc = call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+def _ints_ok(index: int, t: torch.Tensor) -> bool:
+    return t.dtype is _INT and t.is_contiguous() and t.get_device() == index
+
+
+def _launch(index: int, stream, call, *args) -> None:
+    """call(*args, stream) with CUDA device `index` current; the stream is the caller's or the device's current one."""
+    if index < 0:
+        raise Vq3Error(-1, "tensors must be on a CUDA device")
+    if index == torch._C._cuda_getDevice():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+        with torch.cuda.device(index):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc != VQ3_OK:
         raise Vq3Error(rc, lib.vq3_last_error().decode())
 
 
 def _kept(stream, *tensors) -> None:
     """Tensors made here and used on a stream of the caller's: their memory is not reused before that use."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+    for t in tensors:
+        t.record_stream(stream)
 
 
 def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, ring: torch.Tensor,
@@ -525,25 +527,29 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, r
     """Block tables and slot maps of a serving step (vq3_paged_plan): `cached` and `fresh` [requests] int32 lengths,
     `table` [requests, max_pages] int32 gets the new pages in place, taken from the ring of free pages. `out`: a
     plan of the same sizes to write into (its ring_state must not be the one passed in)."""
-    device = table.device
+    index = table.get_device()
+    _want(table.dim() == 2, "table must be [requests, max_pages]")
     requests, max_pages = table.shape
-    _int_arrays(device, cached=cached, fresh=fresh, table=table, ring=ring, ring_state=ring_state)
-    _want(cached.numel() == requests and fresh.numel() == requests and ring_state.numel() == 2,
-          "cached and fresh need one entry per table row, ring_state two")
+    if not (_ints_ok(index, table) and _ints_ok(index, cached) and _ints_ok(index, fresh) and _ints_ok(index, ring)
+            and _ints_ok(index, ring_state) and cached.numel() == requests and fresh.numel() == requests
+            and ring_state.numel() == 2):
+        raise Vq3Error(-1, "table, cached, fresh, ring and ring_state must be contiguous int32 tensors on one device, "
+                           "cached and fresh with one entry per table row, ring_state with two")
     if out is None:
-        ints = torch.empty(2 * requests + max_tokens + 4, dtype=torch.int32, device=device)
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
-        q_start, kv_len, positions, state, status = ints.split((requests + 1, requests, max_tokens, 2, 1))
-        out = PagedPlan(q_start, kv_len, slots, positions, state, status)
-        _kept(stream, ints, slots)
+        device, size = table.device, max(int(max_tokens), 0)
+        out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device), _empty(requests, dtype=_INT, device=device),
+                        _empty(size, dtype=_LONG, device=device), _empty(size, dtype=_INT, device=device),
+                        _empty(2, dtype=_INT, device=device), _empty(1, dtype=_INT, device=device))
+        if stream is not None:
+            _kept(stream, *out)
     else:
-        _int_arrays(device, q_start=out.q_start, kv_len=out.kv_len, positions=out.positions,
-                    ring_state=out.ring_state, status=out.status)
-        _want(out.q_start.numel() == requests + 1 and out.kv_len.numel() == requests and
+        _want(_ints_ok(index, out.q_start) and _ints_ok(index, out.kv_len) and _ints_ok(index, out.positions) and
+              _ints_ok(index, out.ring_state) and _ints_ok(index, out.status) and out.slots.dtype is _LONG and
+              out.slots.is_contiguous() and out.slots.get_device() == index and
+              out.q_start.numel() == requests + 1 and out.kv_len.numel() == requests and
               out.positions.numel() == max_tokens and out.slots.numel() == max_tokens and
-              out.ring_state.numel() == 2 and out.status.numel() == 1 and out.slots.dtype == torch.int64 and
-              out.slots.is_contiguous() and out.slots.device == device, "out is a plan of other sizes")
-    _launch(device, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
+              out.ring_state.numel() == 2 and out.status.numel() == 1, "out is a plan of other sizes")
+    _launch(index, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
             ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
             out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
             out.ring_state.data_ptr(), out.status.data_ptr())
@@ -551,23 +557,28 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, r
 
 
 def _kv_cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> vq3_kv_cache:
-    _want(k_pages.dim() == 4 and k_pages.shape == v_pages.shape and k_pages.dtype == v_pages.dtype and
-          k_pages.dtype in TYPES and k_pages.device == v_pages.device,
-          "k_pages and v_pages must be [n_pages, page_size, kv_heads, head_dim], FP16 or BF16, alike")
-    n_pages, page_size, kv_heads, head_dim = k_pages.shape
-    ks, vs = k_pages.stride(), v_pages.stride()
-    _want(ks[3] == 1 and vs[3] == 1, "the head_dim axis of the cache must be contiguous")
-    return vq3_kv_cache(kv_heads, head_dim, page_size, n_pages, k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1],
-                        ks[2], vs[0], vs[1], vs[2])
+    shape, (kp, kt, kh, kd), (vp, vt, vh, vd) = _pair(k_pages, v_pages, 4)
+    if kd != 1 or vd != 1:
+        raise Vq3Error(-1, "the head_dim axis of the cache must be contiguous")
+    return vq3_kv_cache(shape[2], shape[3], shape[1], shape[0], k_pages.data_ptr(), v_pages.data_ptr(), kp, kt, kh, vp,
+                        vt, vh)
 
 
 def _kv_rows(k: torch.Tensor, v: torch.Tensor) -> vq3_kv_rows:
-    _want(k.dim() == 3 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in TYPES and k.device == v.device,
-          "k and v must be [tokens, kv_heads, head_dim], FP16 or BF16, alike")
-    tokens, kv_heads, head_dim = k.shape
-    ks, vs = k.stride(), v.stride()
-    _want(ks[2] == 1 and vs[2] == 1, "the head_dim axis of k and v must be contiguous")
-    return vq3_kv_rows(kv_heads, head_dim, tokens, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1])
+    shape, (kt, kh, kd), (vt, vh, vd) = _pair(k, v, 3)
+    if kd != 1 or vd != 1:
+        raise Vq3Error(-1, "the head_dim axis of k and v must be contiguous")
+    return vq3_kv_rows(shape[1], shape[2], shape[0], k.data_ptr(), v.data_ptr(), kt, kh, vt, vh)
+
+
+def _pair(k: torch.Tensor, v: torch.Tensor, dim: int):
+    """Shape and strides of keys and values, which are alike."""
+    shape = k.shape
+    if len(shape) != dim or v.shape != shape or k.dtype is not v.dtype or k.dtype not in TYPES or \
+            k.get_device() != v.get_device():
+        raise Vq3Error(-1, "keys and values must be FP16 or BF16 tensors alike: rows [tokens, kv_heads, head_dim], "
+                           "pages [n_pages, page_size, kv_heads, head_dim]")
+    return shape, k.stride(), v.stride()
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -575,10 +586,13 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: to
     """Writes rows k, v [tokens, kv_heads, head_dim] into the paged cache [n_pages, page_size, kv_heads, head_dim] (any
     strides) at `slots` [>= tokens] int64 (vq3_kv_append); negative slots are skipped."""
     cache, rows = _kv_cache(k_pages, v_pages), _kv_rows(k, v)
-    _want(k.dtype == k_pages.dtype and k.device == k_pages.device, "rows and cache must have one type and device")
-    _want(slots.dtype == torch.int64 and slots.is_contiguous() and slots.numel() >= rows.tokens and
-          slots.device == k.device, "slots must be a contiguous int64 tensor with an entry per row")
-    _launch(k.device, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
+    index = k.get_device()
+    if k.dtype is not k_pages.dtype or k_pages.get_device() != index:
+        raise Vq3Error(-1, "rows and cache must have one type and device")
+    if slots.dtype is not _LONG or not slots.is_contiguous() or slots.numel() < rows.tokens or \
+            slots.get_device() != index:
+        raise Vq3Error(-1, "slots must be a contiguous int64 tensor with an entry per row")
+    _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
 
 
 def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new: int = 0) -> int:
@@ -586,32 +600,37 @@ def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new:
     return int(lib.vq3_attention_workspace_bytes(heads, kv_heads, head_dim, max_new))
 
 
-def _attention(call, q, kv, q_start, max_new, scale, out, lse, ws, stream, *more) -> torch.Tensor:
-    _want(q.dim() == 3 and q.dtype in TYPES and q.shape[2] == kv.head_dim,
-          f"q must be [tokens, heads, {kv.head_dim}], FP16 or BF16")
-    device = q.device
-    tokens, heads, head_dim = q.shape
+def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws, stream, *more) -> torch.Tensor:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not dtype or shape[2] != kv.head_dim or q.get_device() != index:
+        raise Vq3Error(-1, f"q must be [tokens, heads, {kv.head_dim}] of the keys' type and device")
+    tokens, heads, head_dim = shape
+    if not _ints_ok(index, q_start) or q_start.numel() < 1:
+        raise Vq3Error(-1, "q_start must be a contiguous int32 tensor [requests + 1] on q's device")
     made = []
     if out is None:
-        out = torch.empty((tokens, heads, head_dim), dtype=q.dtype, device=device)
+        out = _empty(shape, dtype=dtype, device=q.device)
         made.append(out)
-    else:
-        _want(out.shape == q.shape and out.dtype == q.dtype and out.device == device, "out must be like q")
-    if lse is not None:
-        _want(lse.shape == q.shape[:2] and lse.dtype == torch.float32 and lse.is_contiguous() and
-              lse.device == device, "lse must be a contiguous float32 tensor [tokens, heads]")
-    qs, os_ = q.stride(), out.stride()
-    _want(qs[2] == 1 and os_[2] == 1, "the head_dim axis of q and out must be contiguous")
-    _int_arrays(device, q_start=q_start)
+    elif out.shape != shape or out.dtype is not dtype or out.get_device() != index:
+        raise Vq3Error(-1, "out must be like q")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype is not _FLOAT or not lse.is_contiguous()
+                            or lse.get_device() != index):
+        raise Vq3Error(-1, "lse must be a contiguous float32 tensor [tokens, heads]")
+    qt, qh, qd = q.stride()
+    ot, oh, od = out.stride()
+    if qd != 1 or od != 1:
+        raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
     if ws is None:
-        n = int(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        # 256 bytes at least, for the status word
+        ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
+                    dtype=torch.uint8, device=q.device)
         made.append(ws)
-    _kept(stream, *made)
-    a = vq3_attn(TYPES[q.dtype], heads, tokens, q_start.numel() - 1, max_new,
+    if stream is not None:
+        _kept(stream, *made)
+    a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
                  head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
-                 None if lse is None else lse.data_ptr(), q_start.data_ptr(), qs[0], qs[1], os_[0], os_[1])
-    _launch(device, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+                 None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
+    _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -624,12 +643,13 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     new tokens counted in. max_new: most new tokens of a request, 0 if unknown (it only picks the kernel). scale:
     1 / sqrt(head_dim) by default. `lse` [tokens, heads] FP32 is filled if given."""
     cache = _kv_cache(k_pages, v_pages)
-    _want(table.dim() == 2 and table.shape[0] == kv_len.numel() == q_start.numel() - 1,
-          "table must be [requests, max_pages], kv_len [requests], q_start [requests + 1]")
-    _want(q.dtype == k_pages.dtype and q.device == k_pages.device, "q and cache must have one type and device")
-    _int_arrays(q.device, table=table, kv_len=kv_len)
-    return _attention(lib.vq3_paged_attention, q, cache, q_start, max_new, scale, out, lse, ws, stream,
-                      table.data_ptr(), table.shape[1], kv_len.data_ptr())
+    index = k_pages.get_device()
+    if not (_ints_ok(index, table) and _ints_ok(index, kv_len) and table.dim() == 2
+            and table.shape[0] == kv_len.numel() == q_start.numel() - 1):
+        raise Vq3Error(-1, "table [requests, max_pages] and kv_len [requests] must be contiguous int32 tensors on the "
+                           "cache's device, q_start [requests + 1]")
+    return _attention(lib.vq3_paged_attention, q, cache, k_pages.dtype, index, q_start, max_new, scale, out, lse, ws,
+                      stream, table.data_ptr(), table.shape[1], kv_len.data_ptr())
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, max_new: int = 0,
@@ -637,6 +657,5 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
                      ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention over whole packed prompts (vq3_prompt_attention): q [tokens, heads, head_dim], k and v [tokens,
     kv_heads, head_dim], request r at rows q_start[r] .. q_start[r + 1] - 1 of all three."""
-    rows = _kv_rows(k, v)
-    _want(q.dtype == k.dtype and q.device == k.device, "q, k and v must have one type and device")
-    return _attention(lib.vq3_prompt_attention, q, rows, q_start, max_new, scale, out, lse, ws, stream)
+    return _attention(lib.vq3_prompt_attention, q, _kv_rows(k, v), k.dtype, k.get_device(), q_start, max_new, scale, out,
+                      lse, ws, stream)
