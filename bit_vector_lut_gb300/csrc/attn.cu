@@ -66,14 +66,14 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
   constexpr int kC = D / 32;  // K chunks of 32
   constexpr int kV = D / 64;  // V chunks of 64
   constexpr float kOff = AttnType<T>::kOff;
-  __shared__ long long s_sum[kWarps];
+  __shared__ unsigned s_sum[3 * kWarps];
   __shared__ AttnPos s_pos;
   __shared__ __align__(16) float s_o[kWarps][kRows][D + 4];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
-  attn_locate<kThreads>(a, kTile, kMinTiles, s_sum, &s_pos);
-  const AttnPos pos = s_pos;
+  const AttnPos pos = a.requests <= kWarpRequests ? attn_locate_warp(a, kTile, kMinTiles)
+                                                  : attn_locate_block<kThreads>(a, kTile, kMinTiles, s_sum, &s_pos);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   AttnRec rec{};
   AttnWalk w;
@@ -97,10 +97,10 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
       for (int e = 0; e < 2; ++e) {
         const int pe = base + b * 8 + 2 * t + e;
         // rows beyond the last are computed on zeros and not written: nothing to mask
-        lim[b][e] = pe < rows ? attn_seen(w.q, pe / a.group) : 0x7fffffff;
+        lim[b][e] = pe < rows ? attn_seen(w.q, a.by_group(pe)) : 0x7fffffff;
       }
     }
-    low = attn_seen(w.q, base / a.group);  // what the first row sees: no less than nothing is masked
+    low = attn_seen(w.q, a.by_group(base));  // what the first row sees: no less than nothing is masked
 
     float m[NR][2], l[NR][2];
     float o[NR][D / 16][4];
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
     failed = __syncthreads_or(failed);
     if (tid == 0) *a.status = failed ? 3 : 0;
   }
-  if (!(rec.x & kRecTail) || attn_packed_row(row0, rec.w, rec.z, a.block_rows, a.block_used) < 0) return;
+  if (!(rec.x & kRecTail) || attn_packed_row(a, row0, rec.w, rec.z) < 0) return;
   if (warp == 0) {
     // the unit's slots, in CTA order
     int n = 1;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
   const int n = s_n;
   const int row = row0 + tid % C::kRows, group = C::kGroups > 1 ? tid / 64 : 0;
   const int quad = q0 + tid / C::kRows % C::kStep;
-  const int p = attn_packed_row(row, rec.w, rec.z, a.block_rows, a.block_used);
+  const int p = attn_packed_row(a, row, rec.w, rec.z);
   const float4* const src = reinterpret_cast<const float4*>(a.part) + (size_t)quad * slot_rows + row;
   const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + row;
   Merge acc[C::kPasses];

@@ -32,6 +32,23 @@ constexpr int kRecEnd = 2;      // and the unit ends there
 constexpr int kRecTail = 4;     // slot 2c + 1 holds the first part of a unit
 constexpr int kRecFailed = 8;   // a bounded wait of this CTA gave up
 
+// x / d for 0 <= x < 2^31 by a multiplication: with s = ceil(log2 d) and m = floor(2^(31 + s) /
+// d) + 1, m d exceeds 2^(31 + s) by at most d <= 2^s, so x m / 2^(31 + s) lies in [x / d, x / d +
+// 1 / d) and its floor is the quotient.
+struct FastDiv {
+  unsigned m = 0;
+  int s = 0, d = 1;
+  FastDiv() = default;
+  explicit FastDiv(int div) : d(div) {
+    while ((1LL << s) < div) ++s;
+    m = (unsigned)((1ULL << (31 + s)) / (unsigned)div + 1);
+    s += 31;
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return (int)(((unsigned long long)(unsigned)x * m) >> s);
+  }
+};
+
 struct AttnArgs {
   const void* q;
   const void* k;
@@ -47,7 +64,8 @@ struct AttnArgs {
   int page_shift, max_pages, n_pages;
   int max_kv;          // no request sees more keys than this (paged: max_pages pages)
   int unit_rows;       // packed rows of a unit
-  int block_rows, block_used;  // the unit's rows sit in blocks of block_rows, of which block_used are used
+  int block_shift, block_used;  // the unit's rows sit in blocks of 2^block_shift, of which block_used are used
+  FastDiv by_group, by_unit;     // group, unit_rows
   float scale_log2;    // scale * log2(e)
   float* part;         // [2 * grid][slot rows][D] unnormalised outputs
   float* part_ml;      // [2 * grid][slot rows][2] max (log2 domain), sum
@@ -109,7 +127,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
   } else {
     q.kv = q.n_new;
   }
-  q.units = (q.n_new * a.group + a.unit_rows - 1) / a.unit_rows;
+  q.units = a.by_unit(q.n_new * a.group + a.unit_rows - 1);
   return q;
 }
 
@@ -120,18 +138,18 @@ __device__ __forceinline__ int attn_seen(const AttnRequest& q, int t) {
 }
 // Keys that the last row of unit j sees.
 __device__ __forceinline__ int attn_unit_end(const AttnArgs& a, const AttnRequest& q, int j) {
-  const int t = ((j + 1) * a.unit_rows - 1) / a.group;  // tokens * heads < 2^30
+  const int t = a.by_group((j + 1) * a.unit_rows - 1);  // tokens * heads < 2^30
   return attn_seen(q, t < q.n_new - 1 ? t : q.n_new - 1);
 }
 // Tiles of unit j; a unit that sees nothing still counts as one, its rows are written too.
 __device__ __forceinline__ int attn_unit_tiles(const AttnArgs& a, const AttnRequest& q, int j, int kv_tile) {
-  const int n = (attn_unit_end(a, q, j) + kv_tile - 1) / kv_tile;
+  const int n = (int)((unsigned)(attn_unit_end(a, q, j) + kv_tile - 1) / (unsigned)kv_tile);
   return n < 1 ? 1 : n;
 }
 
 struct AttnPos {
-  int r, h, j, t;    // request, key/value head, unit of the head, first tile
-  long long tiles;   // tiles of this CTA's range (0: none)
+  int r, h, j, t;  // request, key/value head, unit of the head, first tile
+  unsigned tiles;  // tiles of this CTA's range (0: none)
 };
 
 // How a batch is divided. Plain: all tiles in one line, cut into equal ranges. Where the
@@ -141,27 +159,30 @@ struct AttnPos {
 // keys in L2. (64 rows of 6 heads behind 98,304 tokens of 4 x 256: 1.6 GB from memory and
 // 232 us with the plain cut.)
 struct AttnCut {
-  long long tiles;  // of the batch
-  int units;        // of the batch; 0: the plain cut
+  unsigned tiles;  // of the batch
+  int units;       // of the batch; 0: the plain cut
   int ctas;
 };
-// What unit j counts: its tiles, or the CTAs that are its own.
-__device__ __forceinline__ int attn_unit_cost(const AttnArgs& a, const AttnRequest& q, int j, int kv_tile,
-                                              int min_tiles, const AttnCut& cut) {
-  const int n = attn_unit_tiles(a, q, j, kv_tile);
+// What unit j counts: its tiles, or the CTAs that are its own. (The batch's tiles stay below
+// 2^32: the entry points check a bound.)
+__device__ __forceinline__ unsigned attn_unit_cost(const AttnArgs& a, const AttnRequest& q, int j, int kv_tile,
+                                                   int min_tiles, const AttnCut& cut) {
+  const unsigned n = attn_unit_tiles(a, q, j, kv_tile);
   if (cut.units == 0) return n;
-  const int c = 1 + (int)((long long)(cut.ctas - cut.units) * n / cut.tiles), most = n / min_tiles;
+  const unsigned spare = cut.ctas - cut.units, most = n / min_tiles;
+  // at most the exact share, so that all shares fit the grid: the factor outweighs three roundings
+  const unsigned c = 1 + (unsigned)((float)spare * n / cut.tiles * 0.999999f);
   return c <= most ? c : (most < 1 ? 1 : most);
 }
 
 // Cost of each lane's request (0 beyond the last), found by the whole warp where a request
 // has many units.
-__device__ __forceinline__ long long attn_costs(const AttnArgs& a, int r, int kv_tile, int min_tiles,
-                                                const AttnCut& cut, int lane, int* units) {
+__device__ __forceinline__ unsigned attn_costs(const AttnArgs& a, int r, int kv_tile, int min_tiles,
+                                               const AttnCut& cut, int lane, int* units) {
   AttnRequest q{};
   if (r < a.requests) q = attn_request(a, r);
   *units = q.units;
-  long long c = 0;
+  unsigned c = 0;
   if (q.units <= 4)
     for (int j = 0; j < q.units; ++j) c += attn_unit_cost(a, q, j, kv_tile, min_tiles, cut);
   unsigned big = __ballot_sync(0xffffffffu, q.units > 4);
@@ -169,163 +190,214 @@ __device__ __forceinline__ long long attn_costs(const AttnArgs& a, int r, int kv
     const int src = __ffs(big) - 1;
     big &= big - 1;
     AttnRequest o;
-    o.q0 = __shfl_sync(0xffffffffu, q.q0, src);
+    o.q0 = 0;
     o.n_new = __shfl_sync(0xffffffffu, q.n_new, src);
     o.kv = __shfl_sync(0xffffffffu, q.kv, src);
     o.units = __shfl_sync(0xffffffffu, q.units, src);
-    long long s = 0;
+    unsigned s = 0;
     for (int j = lane; j < o.units; j += 32) s += attn_unit_cost(a, o, j, kv_tile, min_tiles, cut);
-#pragma unroll
-    for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    s = __reduce_add_sync(0xffffffffu, s);
     if (lane == src) c = s;
   }
   return c * a.kv_heads;
 }
 
-// Sums the batch's costs: this thread's own in *mine and the sum before it in *before.
-// Thread i looks after requests [i * per, (i + 1) * per), so the order is the requests'.
-template <int kThreads>
-__device__ __forceinline__ long long attn_sum(const AttnArgs& a, int kv_tile, int min_tiles, const AttnCut& cut,
-                                              long long* sm, long long* mine, long long* before, int* units,
-                                              int* most) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.requests + kThreads - 1) / kThreads;
-  *mine = 0;
-  *units = *most = 0;
-  for (int i = 0; i < per; ++i) {
-    int u;
-    *mine += attn_costs(a, tid * per + i, kv_tile, min_tiles, cut, lane, &u);
-    *units += u * a.kv_heads;
-    *most = u > *most ? u : *most;
+// This CTA's range of `total`, in tiles (plain cut) or as the number of a CTA.
+__device__ __forceinline__ void attn_range(const AttnCut& cut, unsigned total, int min_tiles, unsigned* s0,
+                                           unsigned* s1) {
+  const unsigned c = blockIdx.x;
+  if (cut.units) {
+    *s0 = c;
+    *s1 = c < total ? c + 1 : c;
+    return;
   }
-  long long incl = *mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) sm[warp] = incl;
-  __syncthreads();
-  long long total = 0;
-  *before = incl - *mine;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) *before += sm[w];
-    total += sm[w];
-  }
-  return total;
+  unsigned live = total / min_tiles;
+  live = live < 1 ? 1 : (live > (unsigned)cut.ctas ? cut.ctas : live);
+  const unsigned each = total / live, more = total - each * live;  // the first `more` CTAs take one more
+  *s0 = c < live ? each * c + (c < more ? c : more) : total;
+  *s1 = c < live ? *s0 + each + (c < more ? 1 : 0) : total;
 }
 
-// Finds this CTA's range. Every thread of the CTA calls it; `sm` is shared memory for
-// kThreads / 32 + 1 sums and `pos` the shared result (valid after the call's barrier).
-template <int kThreads>
-__device__ __forceinline__ void attn_locate(const AttnArgs& a, int kv_tile, int min_tiles, long long* sm,
+// The whole warp: where inside request r (whose cost is `cost`) offset `off` falls.
+__device__ __forceinline__ void attn_inside(const AttnArgs& a, int r, unsigned cost, unsigned off, int kv_tile,
+                                            int min_tiles, const AttnCut& cut, unsigned plain, int lane,
                                             AttnPos* pos) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int per = (a.requests + kThreads - 1) / kThreads;
-  AttnCut cut{0, 0, (int)gridDim.x};
-  long long mine, before;
-  int units, most;
-  long long total = attn_sum<kThreads>(a, kv_tile, min_tiles, cut, sm, &mine, &before, &units, &most);
-  cut.tiles = total;
-  long long s0, s1;
-  if (__syncthreads_or(most > 1)) {
-    // several row blocks share a request's keys: are the units few?
-    if (tid == 0) *reinterpret_cast<int*>(sm) = 0;
-    __syncthreads();
-    if (units) atomicAdd(reinterpret_cast<int*>(sm), units < (int)gridDim.x ? units : (int)gridDim.x);
-    __syncthreads();
-    const int all = *reinterpret_cast<int*>(sm);
-    __syncthreads();
-    if (2 * all <= (int)gridDim.x) {
-      cut.units = all;
-      total = attn_sum<kThreads>(a, kv_tile, min_tiles, cut, sm, &mine, &before, &units, &most);
+  const unsigned per_head = cost / a.kv_heads;
+  const AttnRequest q = attn_request(a, r);
+  const int h = (int)(off / per_head);
+  unsigned left = off - h * per_head;
+  int j = 0, at = 0, n = 0;
+  for (int j0 = 0; j0 < q.units; j0 += 32) {
+    const int mine = j0 + lane;
+    const unsigned c = mine < q.units ? attn_unit_cost(a, q, mine, kv_tile, min_tiles, cut) : 0;
+    unsigned in = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, in, d);
+      if (lane >= d) in += o;
     }
+    const unsigned here = __ballot_sync(0xffffffffu, left >= in - c && left < in);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      j = j0 + src;
+      n = (int)__shfl_sync(0xffffffffu, c, src);
+      at = (int)(left - __shfl_sync(0xffffffffu, in, src)) + n;
+      break;
+    }
+    left -= __shfl_sync(0xffffffffu, in, 31);
   }
-  const long long c = blockIdx.x;
-  if (cut.units) {
-    s0 = c;
-    s1 = c < total ? c + 1 : c;
+  pos->r = r;
+  pos->h = h;
+  pos->j = j;
+  if (cut.units) {  // CTA `at` of the unit's n
+    const unsigned long long tiles = attn_unit_tiles(a, q, j, kv_tile);
+    pos->t = (int)(tiles * at / n);
+    pos->tiles = (unsigned)(tiles * (at + 1) / n) - pos->t;
   } else {
-    long long live = total / min_tiles;
-    live = live < 1 ? 1 : (live > gridDim.x ? gridDim.x : live);
-    if (total < (1 << 20)) {  // 32 bits are enough, and a 64-bit division is slow
-      const unsigned n = (unsigned)total, l = (unsigned)live, i = (unsigned)c;
-      s0 = i < l ? n * i / l : n;
-      s1 = i < l ? n * (i + 1) / l : n;
-    } else {
-      s0 = c < live ? total * c / live : total;
-      s1 = c < live ? total * (c + 1) / live : total;
-    }
+    pos->t = at;
+    pos->tiles = plain;
   }
-  if (tid == 0) pos->tiles = cut.units ? 0 : s1 - s0;
+}
+
+// Few requests: every warp finds the CTA's range by itself, without a barrier.
+constexpr int kWarpRequests = 128;
+__device__ __forceinline__ AttnPos attn_locate_warp(const AttnArgs& a, int kv_tile, int min_tiles) {
+  const int lane = threadIdx.x & 31, per = (a.requests + 31) / 32;
+  AttnCut cut{0, 0, (int)gridDim.x};
+  AttnPos pos{};
+  unsigned mine, total, before;
+  for (int pass = 0;; ++pass) {
+    int units = 0, most = 0;
+    mine = 0;
+    for (int i = 0; i < per; ++i) {
+      int u;
+      mine += attn_costs(a, lane * per + i, kv_tile, min_tiles, cut, lane, &u);
+      units += u * a.kv_heads < cut.ctas ? u * a.kv_heads : cut.ctas;
+      most = u > most ? u : most;
+    }
+    unsigned incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    before = incl - mine;
+    if (pass || !__any_sync(0xffffffffu, most > 1)) break;
+    const int all = __reduce_add_sync(0xffffffffu, units);
+    if (2 * all > cut.ctas) break;
+    cut.tiles = total;
+    cut.units = all;
+  }
+  unsigned s0, s1;
+  attn_range(cut, total, min_tiles, &s0, &s1);
+  if (s1 <= s0) return pos;
+  for (int i = 0; i < per; ++i) {
+    int u;
+    const int r = lane * per + i;
+    const unsigned cost = per == 1 ? mine : attn_costs(a, r, kv_tile, min_tiles, cut, lane, &u);
+    const unsigned hit = __ballot_sync(0xffffffffu, before <= s0 && s0 < before + cost);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      attn_inside(a, __shfl_sync(0xffffffffu, r, src), __shfl_sync(0xffffffffu, cost, src),
+                  s0 - __shfl_sync(0xffffffffu, before, src), kv_tile, min_tiles, cut, s1 - s0, lane, &pos);
+      break;
+    }
+    before += cost;
+  }
+  return pos;
+}
+
+// Many requests: the CTA's warps share them. Thread i looks after requests [i * per, (i + 1) *
+// per), so the order is the requests'. Every thread of the CTA calls it; `sm` is shared memory
+// for 3 * kThreads / 32 sums and `result` the shared result.
+template <int kThreads>
+__device__ __noinline__ AttnPos attn_locate_block(const AttnArgs& a, int kv_tile, int min_tiles, unsigned* sm,
+                                                  AttnPos* result) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.requests + kThreads - 1) / kThreads;
+  AttnCut cut{0, 0, (int)gridDim.x};
+  unsigned mine, total, before;
+  for (int pass = 0;; ++pass) {
+    int units = 0, most = 0;
+    mine = 0;
+    for (int i = 0; i < per; ++i) {
+      int u;
+      mine += attn_costs(a, tid * per + i, kv_tile, min_tiles, cut, lane, &u);
+      units += u * a.kv_heads < cut.ctas ? u * a.kv_heads : cut.ctas;
+      most = u > most ? u : most;
+    }
+    unsigned incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    units = __reduce_add_sync(0xffffffffu, units);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+      sm[warp] = incl;
+      sm[kWarps + warp] = units;
+      sm[2 * kWarps + warp] = most;
+    }
+    __syncthreads();
+    unsigned all = 0, big = 0;
+    total = 0;
+    before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm[w];
+      total += sm[w];
+      all += sm[kWarps + w];
+      big = sm[2 * kWarps + w] > big ? sm[2 * kWarps + w] : big;
+    }
+    __syncthreads();
+    if (pass || big <= 1 || 2 * all > (unsigned)cut.ctas) break;
+    cut.tiles = total;
+    cut.units = (int)all;
+  }
+  unsigned s0, s1;
+  attn_range(cut, total, min_tiles, &s0, &s1);
+  if (tid == 0) result->tiles = 0;
   __syncthreads();
-  const long long warp_end = __shfl_sync(0xffffffffu, before + mine, 31);
+  const unsigned warp_end = __shfl_sync(0xffffffffu, before + mine, 31);
   if (s1 > s0 && __shfl_sync(0xffffffffu, before, 0) <= s0 && s0 < warp_end) {
     // this warp's requests hold the range's start
-    long long lo = before;
     for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
       int u;
-      const long long cost = attn_costs(a, r, kv_tile, min_tiles, cut, lane, &u);
-      const unsigned hit = __ballot_sync(0xffffffffu, lo <= s0 && s0 < lo + cost);
+      const int r = tid * per + i;
+      const unsigned cost = attn_costs(a, r, kv_tile, min_tiles, cut, lane, &u);
+      const unsigned hit = __ballot_sync(0xffffffffu, before <= s0 && s0 < before + cost);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        const int rr = __shfl_sync(0xffffffffu, r, src);
-        const long long per_head = __shfl_sync(0xffffffffu, cost, src) / a.kv_heads;
-        const long long off = s0 - __shfl_sync(0xffffffffu, lo, src);
-        const AttnRequest q = attn_request(a, rr);
-        const int h = (int)(off / per_head);
-        long long left = off - (long long)h * per_head;
-        for (int j0 = 0; j0 < q.units; j0 += 32) {
-          const int j = j0 + lane;
-          const int n = j < q.units ? attn_unit_cost(a, q, j, kv_tile, min_tiles, cut) : 0;
-          int in = n;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, in, d);
-            if (lane >= d) in += o;
-          }
-          const bool here = left >= in - n && left < in;
-          if (here) {
-            pos->r = rr;
-            pos->h = h;
-            pos->j = j;
-            const int at = (int)(left - (in - n));
-            if (cut.units) {  // CTA `at` of the unit's n
-              const long long tiles = attn_unit_tiles(a, q, j, kv_tile);
-              pos->t = (int)(tiles * at / n);
-              pos->tiles = tiles * (at + 1) / n - pos->t;
-            } else {
-              pos->t = at;
-            }
-          }
-          if (__ballot_sync(0xffffffffu, here)) break;
-          left -= __shfl_sync(0xffffffffu, in, 31);
-        }
+        AttnPos pos{};
+        attn_inside(a, __shfl_sync(0xffffffffu, r, src), __shfl_sync(0xffffffffu, cost, src),
+                    s0 - __shfl_sync(0xffffffffu, before, src), kv_tile, min_tiles, cut, s1 - s0, lane, &pos);
+        if (lane == 0) *result = pos;
         break;
       }
-      lo += cost;
+      before += cost;
     }
   }
   __syncthreads();
+  return *result;
 }
 
 // Walks a CTA's range unit by unit.
 struct AttnWalk {
   AttnRequest q;
   int r, h, j, t0, t1, n, end;  // tiles [t0, t1) of the unit's n; end: keys its last row sees
-  long long left;               // tiles of the range from this unit on
+  unsigned left;                // tiles of the range from this unit on
 
   __device__ __forceinline__ void unit(const AttnArgs& a, int kv_tile) {
     end = attn_unit_end(a, q, j);
-    n = (end + kv_tile - 1) / kv_tile;
+    n = (int)((unsigned)(end + kv_tile - 1) / (unsigned)kv_tile);
     if (n < 1) n = 1;
-    t1 = left < (long long)(n - t0) ? t0 + (int)left : n;
+    t1 = left < (unsigned)(n - t0) ? t0 + (int)left : n;
   }
   __device__ __forceinline__ bool start(const AttnArgs& a, const AttnPos& p, int kv_tile) {
     left = p.tiles;
-    if (left <= 0) return false;
+    if (left == 0) return false;
     r = p.r;
     h = p.h;
     j = p.j;
@@ -336,7 +408,7 @@ struct AttnWalk {
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, int kv_tile) {
     left -= t1 - t0;
-    if (left <= 0) return false;
+    if (left == 0) return false;
     t0 = 0;
     if (++j >= q.units) {
       j = 0;
@@ -360,15 +432,15 @@ struct RowPlace {
   int head;
 };
 __device__ __forceinline__ RowPlace row_place(const AttnArgs& a, int q0, int kv_head, int p) {
-  const int t = p / a.group;
+  const int t = a.by_group(p);
   return {(long long)(q0 + t), kv_head * a.group + (p - t * a.group)};
 }
 
 // The packed row (of the request) at row i of a unit that starts at packed row `base`, or -1.
-__device__ __forceinline__ int attn_packed_row(int i, int base, int rows, int block_rows, int block_used) {
-  const int b = i / block_rows, o = i - b * block_rows;
-  const int p = base + b * block_used + o;
-  return o < block_used && p < rows ? p : -1;
+__device__ __forceinline__ int attn_packed_row(const AttnArgs& a, int i, int base, int rows) {
+  const int b = i >> a.block_shift, o = i - (b << a.block_shift);
+  const int p = base + b * a.block_used + o;
+  return o < a.block_used && p < rows ? p : -1;
 }
 
 // The two kernels and the combining pass.

@@ -282,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   float* const s_max = reinterpret_cast<float*>(misc);                 // [2][2][128]
   unsigned long long* const bars = reinterpret_cast<unsigned long long*>(misc + 2048);  // 40
   AttnPos* const s_pos = reinterpret_cast<AttnPos*>(misc + 2048 + 320);
-  long long* const s_sum = reinterpret_cast<long long*>(misc + 2048 + 384);  // kThreads / 32
-  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(misc + 2048 + 512);
-  volatile int* const abort = reinterpret_cast<volatile int*>(misc + 2048 + 516);
+  unsigned* const s_sum = reinterpret_cast<unsigned*>(misc + 2048 + 384);  // 3 * kThreads / 32
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(misc + 2048 + 704);
+  volatile int* const abort = reinterpret_cast<volatile int*>(misc + 2048 + 708);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
@@ -320,16 +320,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kTmaWarp && lane < 3) {  // the descriptors' first fetch, ahead of the copies
+    const CUtensorMap* const m = lane == 0 ? &maps.q : (lane == 1 ? &maps.k : &maps.v);
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
-  attn_locate<kThreads>(a, kTile, kMinTiles, s_sum, s_pos);  // its barriers order the set-up above, too
+  const AttnPos pos = a.requests <= kWarpRequests ? attn_locate_warp(a, kTile, kMinTiles)
+                                                  : attn_locate_block<kThreads>(a, kTile, kMinTiles, s_sum, s_pos);
+  __syncthreads();  // the set-up above
   tc_after();
   const uint32_t tmem = *s_tmem;
-  const AttnPos pos = *s_pos;
   // Once a wait gave up (`dead`, the same for the whole warp), the copy and MMA warps issue nothing
   // more; the softmax warps, which meet at barriers, walk on over what is there.
   bool dead = false;
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
                         ? first + block * a.block_used + row
                         : -1;
       const bool live = __any_sync(0xffffffffu, p >= 0);  // dead warps only keep the barriers
-      const int lim = p >= 0 ? attn_seen(w.q, p / a.group) : 0;
+      const int lim = p >= 0 ? attn_seen(w.q, a.by_group(p)) : 0;
       float m = -INFINITY, l = 0.f;
       if (w.end > 0) {
         for (int t = w.t0; t < w.t1; ++t, ++tiles) {
