@@ -316,52 +316,81 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
 // ---------------------------------------------------------------- combining pass
 //
 // The parts of a split unit are slot 2c + 1 of the CTA c that began it and then slot 2c' of the
-// CTAs behind, up to the one that ends it. Block (c, y) takes rows and columns y of the unit
-// that CTA c began, if it did. A thread sums four columns of a row over the parts with a
-// running maximum, in CTA order; the row kernel's units, of few rows and often very many
+// CTAs right behind, up to the one that ends it. Block (c, y) takes rows and columns y of the
+// unit that CTA c began, if it did. A thread sums four columns of a row over the parts, in CTA
+// order, a batch of parts at a time; the row kernel's units, of few rows and often very many
 // parts, get 32 columns a block and four groups of threads, each a fixed quarter of the
-// parts. Bound by latency: the records, then the parts, three dependent reads in all.
+// parts. Bound by latency, so there are two dependent reads in all: the records, then the
+// parts. Only one warp of a block reads records: they are few lines of L2, and all warps of all
+// blocks asking for them took longer than the sums.
 constexpr int kCThreads = 256;
 constexpr int kMaxGrid = 608;  // CTAs of an attention kernel
+
+template <bool kWide, int D>
+struct CombineCfg {
+  static constexpr int kRows = kWide ? 16 : 8;      // rows of a block
+  static constexpr int kQuads = kWide ? 16 : 8;     // its columns, in fours, of one pass
+  static constexpr int kPasses = kWide ? D / 64 : 1;
+  static constexpr int kGroups = kWide ? 1 : 4;     // groups of threads that share the parts
+  static constexpr int kBatch = 4;                   // parts read at once
+  static constexpr int kAcross = D / 4 / kQuads / kPasses;    // blocks over the columns
+  static_assert(kRows * kQuads * kGroups == kCThreads, "a thread per row, four columns and group");
+};
 
 struct Merge {  // running maximum (log2 domain), sum and four columns
   float m, l;
   float4 o;
-  __device__ __forceinline__ void add(float pm, float pl, float4 po) {
-    const float up = fmaxf(m, pm);
-    const float f = m == up ? 1.f : ex2(m - up), g = pm == up ? 1.f : ex2(pm - up);
+  __device__ __forceinline__ void scale(float up) {
+    const float f = m == up ? 1.f : ex2(m - up);  // equal infinities: nothing to rescale
     m = up;
-    l = l * f + pl * g;
-    o.x = o.x * f + po.x * g;
-    o.y = o.y * f + po.y * g;
-    o.z = o.z * f + po.z * g;
-    o.w = o.w * f + po.w * g;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
   }
-};
-
-template <bool kWide, int D>
-struct CombineCfg {
-  static constexpr int kRows = kWide ? 16 : 8;     // rows of a block
-  static constexpr int kQuads = kWide ? D / 4 : 8;  // its columns, in fours
-  static constexpr int kGroups = kWide ? 1 : 4;     // groups of threads that share the parts
-  static constexpr int kStep = kCThreads / kRows / kGroups;  // fours per pass over the columns
-  static constexpr int kPasses = kQuads / kStep;
+  __device__ __forceinline__ void add(float pm, float pl, const float4& po) {  // pm <= m
+    const float f = pm == m ? 1.f : ex2(pm - m);
+    l += f * pl;
+    o.x += f * po.x;
+    o.y += f * po.y;
+    o.z += f * po.z;
+    o.w += f * po.w;
+  }
 };
 
 template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int grid,
                                                                  int slot_rows) {
   using C = CombineCfg<kWide, D>;
-  __shared__ short s_parts[kMaxGrid];
-  __shared__ int s_n;
   __shared__ Merge s_merge[C::kGroups > 1 ? C::kGroups - 1 : 1][64];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
-  constexpr int kAcross = D / 4 / C::kQuads;  // blocks over the columns
-  const int row0 = (int)blockIdx.y / kAcross * C::kRows, q0 = (int)blockIdx.y % kAcross * C::kQuads;
+  __shared__ int4 s_rec;  // of the unit: parts (0: none), q0, rows, base
+  __shared__ int s_head;
+  const int tid = threadIdx.x, c = blockIdx.x;
+  const int row0 = (int)blockIdx.y / C::kAcross * C::kRows, q0 = (int)blockIdx.y % C::kAcross * C::kQuads;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel has ended
-  // from L2 throughout: this block may have started before the records were written
-  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + c));  // flags, q0, rows, base
-  const int head = __ldcg(&a.rec[c].head);
+  if (tid < 32) {
+    // from L2: this block may have started before the records were written
+    int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + c));  // flags, q0, rows, base
+    const int head = __ldcg(&a.rec[c].head);
+    int flags = c + 1 + tid < grid ? __ldcg(&a.rec[c + 1 + tid].flags) : kRecEnd;
+    int n = 0;
+    if ((rec.x & kRecTail) && attn_packed_row(a, row0, rec.w, rec.z) >= 0) {
+      // parts: up to the first CTA that ends the unit
+      for (n = 1;;) {
+        const unsigned ends = __ballot_sync(0xffffffffu, flags & kRecEnd);
+        n += ends ? __ffs(ends) : 32;
+        if (ends) break;
+        flags = c + n + tid < grid ? __ldcg(&a.rec[c + n + tid].flags) : kRecEnd;
+      }
+      if (n > grid - c) n = grid - c;
+    }
+    rec.x = n;
+    if (tid == 0) {
+      s_rec = rec;
+      s_head = head;
+    }
+  }
   if (c == 0 && blockIdx.y == 0) {
     // the workspace's status word: whether a wait of any CTA gave up
     int failed = 0;
@@ -369,69 +398,61 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
     failed = __syncthreads_or(failed);
     if (tid == 0) *a.status = failed ? 3 : 0;
   }
-  if (!(rec.x & kRecTail) || attn_packed_row(a, row0, rec.w, rec.z) < 0) return;
-  if (warp == 0) {
-    // the unit's slots, in CTA order
-    int n = 1;
-    if (lane == 0) s_parts[0] = (short)(2 * c + 1);
-    for (int i0 = c + 1; i0 < grid; i0 += 32) {
-      const int i = i0 + lane;
-      const int f = i < grid ? __ldcg(&a.rec[i].flags) : 0;
-      const unsigned ends = __ballot_sync(0xffffffffu, (f & (kRecHead | kRecEnd)) == (kRecHead | kRecEnd));
-      const unsigned upto = ends ? (2u << (__ffs(ends) - 1)) - 1u : 0xffffffffu;
-      const unsigned has = __ballot_sync(0xffffffffu, f & kRecHead) & upto;
-      if (has >> lane & 1) s_parts[n + __popc(has & ((1u << lane) - 1u))] = (short)(2 * i);
-      n += __popc(has);
-      if (ends) break;
-    }
-    if (lane == 0) s_n = n;
-  }
   __syncthreads();
-  const int n = s_n;
-  const int row = row0 + tid % C::kRows, group = C::kGroups > 1 ? tid / 64 : 0;
-  const int quad = q0 + tid / C::kRows % C::kStep;
+  const int4 rec = s_rec;
+  const int n = rec.x;
+  if (n == 0) return;
+  const int row = row0 + tid % C::kRows, group = tid / (C::kRows * C::kQuads);
   const int p = attn_packed_row(a, row, rec.w, rec.z);
-  const float4* const src = reinterpret_cast<const float4*>(a.part) + (size_t)quad * slot_rows + row;
+  const RowPlace rp = row_place(a, rec.y, s_head, p < 0 ? 0 : p);
+  const bool ok = p >= 0 && VQ3_IN(rp.token, a.tokens, 6);
   const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + row;
-  Merge acc[C::kPasses];
+#pragma unroll 1
+  for (int pass = 0; pass < C::kPasses; ++pass) {
+    const int quad = q0 + pass * C::kQuads + tid / C::kRows % C::kQuads;
+    const float4* const src = reinterpret_cast<const float4*>(a.part) + (size_t)quad * slot_rows + row;
+    Merge acc = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (ok) {
+      for (int i0 = group; i0 < n; i0 += C::kGroups * C::kBatch) {
+        float2 w[C::kBatch];
+        float4 x[C::kBatch];
 #pragma unroll
-  for (int k = 0; k < C::kPasses; ++k) acc[k] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (p >= 0) {
-#pragma unroll 4
-    for (int i = group; i < n; i += C::kGroups) {
-      const size_t slot = s_parts[i];
-      if (!VQ3_IN(slot, 2 * grid, 5)) continue;
-      const float2 x = __ldcg(ml + slot * slot_rows);
+        for (int k = 0; k < C::kBatch; ++k) {
+          const int i = i0 + k * C::kGroups;
+          const size_t slot = 2 * (c + i) + (i == 0);
+          const bool in = i < n && VQ3_IN(slot, 2 * grid, 5);
+          w[k] = in ? __ldcg(ml + slot * slot_rows) : make_float2(-INFINITY, 0.f);
+          x[k] = in ? __ldcg(src + slot * (D / 4) * slot_rows) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float up = acc.m;
 #pragma unroll
-      for (int k = 0; k < C::kPasses; ++k)
-        acc[k].add(x.x, x.y, __ldcg(src + (slot * (D / 4) + k * C::kStep) * slot_rows));
+        for (int k = 0; k < C::kBatch; ++k) up = fmaxf(up, w[k].x);
+        acc.scale(up);
+#pragma unroll
+        for (int k = 0; k < C::kBatch; ++k) acc.add(w[k].x, w[k].y, x[k]);
+      }
     }
-  }
-  if constexpr (C::kGroups > 1) {
-    if (group) s_merge[group - 1][tid & 63] = acc[0];
-    __syncthreads();
-    if (group) return;
+    if constexpr (C::kGroups > 1) {
+      if (group) s_merge[group - 1][tid & 63] = acc;
+      __syncthreads();
+      if (group) return;
 #pragma unroll
-    for (int v = 0; v < C::kGroups - 1; ++v) {
-      const Merge x = s_merge[v][tid];
-      acc[0].add(x.m, x.l, x.o);
+      for (int v = 0; v < C::kGroups - 1; ++v) {
+        const Merge x = s_merge[v][tid];
+        acc.scale(fmaxf(acc.m, x.m));
+        acc.add(x.m, x.l, x.o);
+      }
     }
-  }
-  if (p < 0) return;
-  const RowPlace rp = row_place(a, rec.y, head, p);
-  if (!VQ3_IN(rp.token, a.tokens, 6)) return;
-  T* const dst = static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head;
-  const float sum = acc[0].l, inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int k = 0; k < C::kPasses; ++k) {
+    if (!ok) return;
+    const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
     uint2 y;
-    y.x = pack2<T>(acc[k].o.x * inv, acc[k].o.y * inv);
-    y.y = pack2<T>(acc[k].o.z * inv, acc[k].o.w * inv);
-    *reinterpret_cast<uint2*>(dst + 4 * (quad + k * C::kStep)) = y;
+    y.x = pack2<T>(acc.o.x * inv, acc.o.y * inv);
+    y.y = pack2<T>(acc.o.z * inv, acc.o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + rp.token * a.o_token + rp.head * a.o_head + 4 * quad) = y;
+    if (a.lse && quad == 0)
+      a.lse[rp.token * a.heads + rp.head] =
+          acc.l == 0.f ? -INFINITY : (acc.m - AttnType<T>::kOff + log2f(acc.l)) * 0.6931471805599453f;
   }
-  if (a.lse && quad == 0)
-    a.lse[rp.token * a.heads + rp.head] =
-        sum == 0.f ? -INFINITY : (acc[0].m - AttnType<T>::kOff + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T, int D, int NR>
@@ -450,7 +471,7 @@ template <typename T, int D, bool kWide>
 cudaError_t launch_combine(const AttnArgs& a, int grid, int slot_rows, cudaStream_t st) {
   using C = CombineCfg<kWide, D>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, slot_rows / C::kRows * (D / 4 / C::kQuads));
+  cfg.gridDim = dim3(grid, slot_rows / C::kRows * C::kAcross);
   cfg.blockDim = dim3(kCThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
