@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   // more; the softmax warps, which meet at barriers, walk on over what is there.
   bool dead = false;
   const auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
     dead = __any_sync(0xffffffffu, !mbar_wait(bar, parity, abort)) || dead;
   };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -426,40 +427,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     int tiles[2] = {0, 0};      // tiles of block b (one block: all, [0])
     int outs[2] = {0, 0};       // units of block b
     AttnWalk w;
-    // S buffer `buf` = Q of block b times the stages at `at`; the last block's products release them
-    const auto qk = [&](int b, int buf, Place at, bool last) {
+    // A wait or a commit between two products leaves the tensor pipe idle once the few that are
+    // queued have run, so the waits for stages (mostly long since filled) and the releases of
+    // stages sit between the parts of a product, not between two products.
+    // Part of S buffer `buf` = Q of block b times the stages at `at`
+    const auto qk = [&](int b, int buf, Place at, int part) {
       if (dead) return;
-      tc_after();
 #pragma unroll
-      for (int part = 0; part < C::kParts; ++part) {
+      for (int c = 0; c < C::kCb; ++c)
+        mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, part * C::kCb + c), 16),
+                desc_sw128(stage_at(at.plus(part).s) + (uint32_t)(c * C::kCbBytes), 16), id_qk, part + c > 0);
+    };
+    // Part of O of block b (+)= P in S buffer `buf`, steps [k0, k1) of 16 keys, times the stages at `at`
+    const auto pv = [&](int b, int buf, Place at, int part, int k0, int k1, bool first) {
+      if (dead) return;
+      const uint32_t p = tmem + (uint32_t)(buf * kTile);
+      const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
+      const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
 #pragma unroll
-        for (int c = 0; c < C::kCb; ++c)
-          mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, part * C::kCb + c), 16),
-                  desc_sw128(stage_at(at.plus(part).s) + (uint32_t)(c * C::kCbBytes), 16), id_qk, part + c > 0);
-        if (part == C::kParts - 1) mma_commit(s_full(buf));
-        if (last) mma_commit(empty(at.plus(part).s));
+      for (int h = 0; h < 2; ++h) {
+        if (k0 <= 4 * h && k1 >= 4 * h + 4) {
+          mma_ts4(o, p + 64u * h, v + 512u * h, id_pv, !first || h > 0);
+        } else {
+          for (int k = k0 > 4 * h ? k0 : 4 * h; k < k1 && k < 4 * h + 4; ++k)
+            mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
+        }
       }
     };
-    // O of block b (+)= P in S buffer `buf`, steps [k0, k1) of 16 keys, times the stages at `at`
-    const auto pv = [&](int b, int buf, Place at, int k0, int k1, bool first, bool last) {
-      if (dead) return;
-      tc_after();
-      const uint32_t p = tmem + (uint32_t)(buf * kTile);
+    const auto release = [&](Place at) {
 #pragma unroll
-      for (int part = 0; part < C::kParts; ++part) {
-        const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
-        const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (k0 <= 4 * h && k1 >= 4 * h + 4) {
-            mma_ts4(o, p + 64u * h, v + 512u * h, id_pv, !first || h > 0);
-          } else {
-            for (int k = k0 > 4 * h ? k0 : 4 * h; k < k1 && k < 4 * h + 4; ++k)
-              mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
-          }
-        }
-        if (last) mma_commit(empty(at.plus(part).s));
-      }
+      for (int p = 0; p < C::kParts; ++p) mma_commit(empty(at.plus(p).s));
     };
     const auto wait_stages = [&](Place at) {
 #pragma unroll
@@ -486,58 +483,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
       wait(q_full, (uint32_t)(units & 1));
       ++units;
       wait_stages(it);
+      tc_after();
       if constexpr (NB == 2) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          if (b < blocks) qk(b, b, it, b + 1 == blocks);
+        for (int b = 0; b < 2; ++b) {
+          if (b >= blocks) continue;
+          qk(b, b, it, 0);
+          mma_commit(s_full(b));
+        }
+        release(it);
         it = it.plus(1);
         if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+        wait_stages(it);
         for (int t = w.t0; t < w.t1; ++t) {
           const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
-          const Place vs = it, ks = it.plus(1);
+          const Place vs = it, ks = it.plus(1), next = it.plus(2);
           const bool more = t + 1 < w.t1;
-          wait_stages(vs);
           clear_tail(vs, keys);
-          if (more) wait_stages(ks);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b >= blocks) continue;
+            const bool last = b + 1 == blocks;
             if (t == w.t0 && outs[b]) wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1));
             wait(p_half(b), (uint32_t)(tiles[b] & 1));
-            pv(b, b, vs, 0, steps < 4 ? steps : 4, t == w.t0, false);
+            tc_after();
+            pv(b, b, vs, 0, 0, steps < 4 ? steps : 4, t == w.t0);
+            if (b == 0 && more) wait_stages(ks);
             wait(p_full(b), (uint32_t)(tiles[b] & 1));
-            pv(b, b, vs, 4, steps, false, b + 1 == blocks);
+            tc_after();
+            pv(b, b, vs, 0, 4, steps, false);
             ++tiles[b];
-            if (more)
-              qk(b, b, ks, b + 1 == blocks);
-            else
+            if (more) {
+              if (last) wait_stages(next);  // the next tile's values
+              qk(b, b, ks, 0);
+              mma_commit(s_full(b));
+            } else {
               mma_commit(pv_done(b));
+            }
           }
+          release(vs);
+          if (more) release(ks);
           if (t + 2 == w.t1) mma_commit(q_empty);
-          it = it.plus(more ? 2 : 1);
+          it = more ? next : ks;
         }
         ++outs[0];
         if (blocks == 2) ++outs[1];
       } else {
-        qk(0, tiles[0] & 1, it, true);
+#pragma unroll
+        for (int p = 0; p < C::kParts; ++p) qk(0, tiles[0] & 1, it, p);
+        mma_commit(s_full(tiles[0] & 1));
+        release(it);
         it = it.plus(C::kParts);
         if (w.t1 - w.t0 == 1) mma_commit(q_empty);
-        for (int t = w.t0; t < w.t1; ++t) {
-          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile;
-          if (t + 1 < w.t1) {
-            wait_stages(it);
-            qk(0, (tiles[0] + 1) & 1, it, true);
-            it = it.plus(C::kParts);
+        for (int t = w.t0; t < w.t1; ++t, ++tiles[0]) {
+          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
+          const int buf = tiles[0] & 1;
+          const bool more = t + 1 < w.t1;
+          const Place ks = it, vs = more ? it.plus(C::kParts) : it, next = vs.plus(C::kParts);
+          if (more) {  // S of the next tile; its keys have been waited for
+            wait_stages(ks);
+            tc_after();
+            qk(0, buf ^ 1, ks, 0);
+            qk(0, buf ^ 1, ks, 1);
+            mma_commit(s_full(buf ^ 1));
+            release(ks);
             if (t + 2 == w.t1) mma_commit(q_empty);
           }
-          wait_stages(it);
-          clear_tail(it, keys);
+          wait_stages(vs);
+          clear_tail(vs, keys);
           if (t == w.t0 && outs[0]) wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1));
-          wait(p_full(tiles[0] & 1), (uint32_t)((tiles[0] >> 1) & 1));
-          pv(0, tiles[0] & 1, it, 0, (keys + 15) / 16, t == w.t0, true);
-          mma_commit(pv_done(tiles[0] & 1));
-          it = it.plus(C::kParts);
-          ++tiles[0];
+          wait(p_full(buf), (uint32_t)((tiles[0] >> 1) & 1));
+          tc_after();
+          pv(0, buf, vs, 0, 0, steps, t == w.t0);
+          pv(0, buf, vs, 1, 0, steps, t == w.t0);
+          mma_commit(pv_done(buf));
+          release(vs);
+          it = next;
         }
         ++outs[0];
       }
