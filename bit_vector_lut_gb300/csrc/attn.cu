@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, rows_occ<D, NR>()) attn_rows_kernel(
         rec.rows = rows;
         rec.base = base;
         rec.head = w.h;
+        rec.used = w.q.used;
       }
     }
     for (int i = tid; i < kRows * (D / 4); i += kThreads) {
@@ -365,17 +366,17 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
   using C = CombineCfg<kWide, D>;
   __shared__ Merge s_merge[C::kGroups > 1 ? C::kGroups - 1 : 1][64];
   __shared__ int4 s_rec;  // of the unit: parts (0: none), q0, rows, base
-  __shared__ int s_head;
+  __shared__ int2 s_more;  // key/value head, rows of a block that are used
   const int tid = threadIdx.x, c = blockIdx.x;
   const int row0 = (int)blockIdx.y / C::kAcross * C::kRows, q0 = (int)blockIdx.y % C::kAcross * C::kQuads;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel has ended
   if (tid < 32) {
     // from L2: this block may have started before the records were written
     int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + c));  // flags, q0, rows, base
-    const int head = __ldcg(&a.rec[c].head);
+    const int2 more = make_int2(__ldcg(&a.rec[c].head), __ldcg(&a.rec[c].used));
     int flags = c + 1 + tid < grid ? __ldcg(&a.rec[c + 1 + tid].flags) : kRecEnd;
     int n = 0;
-    if ((rec.x & kRecTail) && attn_packed_row(a, row0, rec.w, rec.z) >= 0) {
+    if ((rec.x & kRecTail) && attn_packed_row(a, row0, rec.w, rec.z, more.y) >= 0) {
       // parts: up to the first CTA that ends the unit
       for (n = 1;;) {
         const unsigned ends = __ballot_sync(0xffffffffu, flags & kRecEnd);
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
     rec.x = n;
     if (tid == 0) {
       s_rec = rec;
-      s_head = head;
+      s_more = more;
     }
   }
   if (c == 0 && blockIdx.y == 0) {
@@ -403,8 +404,8 @@ __global__ void __launch_bounds__(kCThreads) attn_combine_kernel(const __grid_co
   const int n = rec.x;
   if (n == 0) return;
   const int row = row0 + tid % C::kRows, group = tid / (C::kRows * C::kQuads);
-  const int p = attn_packed_row(a, row, rec.w, rec.z);
-  const RowPlace rp = row_place(a, rec.y, s_head, p < 0 ? 0 : p);
+  const int p = attn_packed_row(a, row, rec.w, rec.z, s_more.y);
+  const RowPlace rp = row_place(a, rec.y, s_more.x, p < 0 ? 0 : p);
   const bool ok = p >= 0 && VQ3_IN(rp.token, a.tokens, 6);
   const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + row;
 #pragma unroll 1

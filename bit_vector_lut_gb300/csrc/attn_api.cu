@@ -133,14 +133,14 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.heads = at->heads;
   a.kv_heads = kv_heads;
   a.group = group;
-  const int block_rows = c.wide ? 128 : c.slot_rows;
-  a.block_shift = log2_of(block_rows);
-  a.block_used = c.wide ? 128 / group * group : c.slot_rows;
-  a.unit_rows = c.slot_rows / block_rows * a.block_used;
+  a.unit_blocks = c.wide ? attn_wide_blocks(head_dim) : 1;
+  a.block_rows = c.slot_rows / a.unit_blocks;
+  a.token_rows = c.wide ? a.block_rows / group * group : a.block_rows;
   a.by_group = FastDiv(group);
-  a.by_unit = FastDiv(a.unit_rows);
+  a.by_unit = FastDiv(c.slot_rows);
+  a.by_token_unit = FastDiv(a.unit_blocks * a.token_rows);
   // the kernels count tiles of 64 or 128 keys in 32 bits
-  const double units = (double)at->tokens * group / a.unit_rows + at->requests;
+  const double units = (double)at->tokens * group / (a.unit_blocks * a.token_rows) + at->requests;
   if (units * kv_heads * (a.max_kv / (c.wide ? 128.0 : 64.0) + 1) > 4e9)
     return report_error(VQ3_EUNSUPPORTED, "%s: too many (row block, key tile) pairs: %d tokens, keys up to %d", who,
                         at->tokens, a.max_kv);

@@ -37,9 +37,15 @@ constexpr int kMinTiles = 2;    // fewest tiles per CTA
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 12 * 32;  // warps 10 and 11 fill up the third warpgroup
 // Registers per thread: at launch 168; the softmax warpgroups take what the third gives up.
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "the shares come from the launch's registers");
+template <int D>
+constexpr int kRegsSoftmax = D == 256 ? 200 : 208;  // a row's 64 or 128 scores and what goes with them
+template <int D>
+constexpr int kRegsOther = 3 * 168 - 2 * kRegsSoftmax<D>;
+static_assert(kRegsOther<128> % 8 == 0 && kRegsOther<256> % 8 == 0, "register shares");
+constexpr int kBlock = 128;  // rows of a block
 constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after one second
+// A try_wait sleeps up to this long: a warp that polls takes issue slots from the softmax warps.
+constexpr uint32_t kSuspendNs = 1000000;
 constexpr unsigned long long kDrainNs = 100000000ull;   // the end-of-kernel drain waits at most 0.1 s
 
 // ---------------------------------------------------------------- PTX
@@ -57,9 +63,9 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
       : "memory");
   return ok != 0;
 }
@@ -68,25 +74,19 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for the phase of parity `parity`, at most kWaitNs (the clock is read only every 256
-// polls: a read stalls the warp for longer than a tile's wait). `abort`: the CTA's shared
-// flag; once a wait gave up, every wait returns at once. False: it gave up.
+// Waits for the phase of parity `parity`, at most kWaitNs. `abort`: the CTA's shared flag; once
+// a wait gave up, every wait returns at once. False: it gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  unsigned long long t0 = 0;
-  for (unsigned it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 0u && *abort) return false;
-    if ((it & 255u) == 0u) {
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kWaitNs) {
-        *abort = 1;
-        return false;
-      }
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
     }
   }
+  return true;
 }
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -267,7 +267,7 @@ struct Ring {
 };
 
 struct WideMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, q_token, q_row, k, v;  // of q: a block of whole tokens, one token's group of heads, one row
 };
 
 template <typename T, int D>
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kTmaWarp && lane < 3) {  // the descriptors' first fetch, ahead of the copies
-    const CUtensorMap* const m = lane == 0 ? &maps.q : (lane == 1 ? &maps.k : &maps.v);
+  if (warp == kTmaWarp && lane < 5) {  // the descriptors' first fetch, ahead of the copies
+    const CUtensorMap* const m = &maps.q + lane;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
   if (warp == kMmaWarp) {
@@ -345,30 +345,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<D>));
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ copies
     const int box = a.table ? (1 << a.page_shift < kTile ? 1 << a.page_shift : kTile) : kTile;  // rows per copy
     const int boxes = kTile / box;
     const int my_box = lane & (boxes - 1), my_cb = lane / boxes;  // this lane's copy of a stage
-    const int tt = a.block_used / a.group;                        // tokens of a row block
     Ring<C::kStages> at;
     int it = 0, units = 0;
     AttnWalk w;
     for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
       if (w.end == 0) continue;
-      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
-      if (units) wait(q_empty, (uint32_t)((units - 1) & 1));
-      if (dead) break;
-      const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
-      if (lane == 0) {
-        mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.block_used * 128));
-        for (int b = 0; b < blocks; ++b)
-          for (int cb = 0; cb < D / 64; ++cb)
-            tma_3d(q_at(b, cb), &maps.q, cb * 64, w.h * a.group, w.q.q0 + (w.j * NB + b) * tt, q_full);
-      }
-      __syncwarp();
-      ++units;
+      const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
+      // Q of the unit, once the last one's is used up
+      const auto copy_q = [&] {
+        if (units) wait(q_empty, (uint32_t)((units - 1) & 1));
+        if (dead) return;
+        const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
+        if (w.q.used == a.token_rows) {
+          if (lane == 0) {
+            mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.token_rows * 128));
+            for (int b = 0; b < blocks; ++b)
+              for (int cb = 0; cb < D / 64; ++cb)
+                tma_3d(q_at(b, cb), &maps.q, cb * 64, w.h * a.group, w.q.q0 + a.by_group(first + b * a.token_rows),
+                       q_full);
+          }
+        } else {
+          // a lane per token: its heads in one copy, or row by row where the block cuts them
+          const int last = first + blocks * kBlock < rows ? first + blocks * kBlock : rows;
+          if (lane == 0) mbar_expect_tx(q_full, (uint32_t)((last - first) * (D / 64) * 128));
+          __syncwarp();
+          for (int b = 0; b < blocks; ++b) {
+            const int p0 = first + b * kBlock, p1 = p0 + kBlock < last ? p0 + kBlock : last;
+            for (int t = a.by_group(p0) + lane; t * a.group < p1; t += 32) {
+              const int r0 = t * a.group > p0 ? t * a.group : p0, r1 = (t + 1) * a.group < p1 ? (t + 1) * a.group : p1;
+              for (int cb = 0; cb < D / 64; ++cb) {
+                if (r1 - r0 == a.group) {
+                  tma_3d(q_at(b, cb) + (uint32_t)(r0 - p0) * 128, &maps.q_token, cb * 64, w.h * a.group, w.q.q0 + t,
+                         q_full);
+                } else {
+                  for (int r = r0; r < r1; ++r)
+                    tma_3d(q_at(b, cb) + (uint32_t)(r - p0) * 128, &maps.q_row, cb * 64,
+                           w.h * a.group + r - t * a.group, w.q.q0 + t, q_full);
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        ++units;
+      };
       // the page of this lane's rows of tile t
       const auto page_of = [&](int t) -> int {
         const int x = t * kTile + my_box * box;
@@ -393,17 +419,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
                    part * C::kStageCols + my_cb * 64, row, w.h, a.table ? page : 0, full(s));
         }
       };
+      // the first keys go ahead of Q: their stage is free sooner
       int page = page_of(w.t0);
+      copy(&maps.k, w.t0, page);
+      copy_q();
       if constexpr (NB == 2) {
         for (int t = w.t0; t < w.t1; ++t) {
           const int next = page_of(t + 1);
-          copy(&maps.k, t, page);
+          if (t > w.t0) copy(&maps.k, t, page);
           copy(&maps.v, t, page);
           page = next;
         }
       } else {
         int ahead = page_of(w.t0 + 1);
-        copy(&maps.k, w.t0, page);
         for (int t = w.t0; t < w.t1; ++t) {
           const int next = page_of(t + 2);
           if (t + 1 < w.t1) copy(&maps.k, t + 1, ahead);
@@ -478,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     };
     for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
       if (w.end == 0) continue;
-      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
-      const int blocks = NB == 2 && first + a.block_used < rows ? 2 : 1;
+      const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
+      const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
       wait(q_full, (uint32_t)(units & 1));
       ++units;
       wait_stages(it);
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   }
   } else {
     // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax<D>));
     constexpr int kCols = NB == 2 ? 128 : 64;  // key columns of a thread
     constexpr int kOut = NB == 2 ? D : 128;    // output columns of a thread
     const int wg = warp >> 2, sub = warp & 3, row = sub * 32 + lane;
@@ -583,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
     AttnWalk w;
     const auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + sub) : "memory"); };
     for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
-      const int rows = w.q.n_new * a.group, first = w.j * a.unit_rows;
+      const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
       const bool whole = w.whole();
       if (!whole) {
         if (w.t0 > 0) {
@@ -594,12 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
           rec.rows = rows;
           rec.base = first;
           rec.head = w.h;
+          rec.used = w.q.used;
         }
       }
-      if (NB == 2 && block == 1 && first + a.block_used >= rows) continue;  // no rows in block B
-      const int p = row < a.block_used && first + block * a.block_used + row < rows
-                        ? first + block * a.block_used + row
-                        : -1;
+      if (NB == 2 && block == 1 && first + w.q.used >= rows) continue;  // no rows in block B
+      const int p = row < w.q.used && first + block * w.q.used + row < rows ? first + block * w.q.used + row : -1;
       const bool live = __any_sync(0xffffffffu, p >= 0);  // dead warps only keep the barriers
       const int lim = p >= 0 ? attn_seen(w.q, a.by_group(p)) : 0;
       float m = -INFINITY, l = 0.f;
@@ -829,8 +856,12 @@ cudaError_t launch_wide(const AttnArgs& a, cudaStream_t st) {
   {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.heads, (cuuint64_t)a.tokens};
     const long long strides[2] = {a.q_head, a.q_token};
-    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(a.block_used / a.group)};
-    if (!tensor_map(&maps.q, bf16, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(a.token_rows / a.group)};
+    const cuuint32_t token[3] = {64, (cuuint32_t)a.group, 1}, row[3] = {64, 1, 1};
+    if (!tensor_map(&maps.q, bf16, a.q, 3, dims, strides, box) ||
+        !tensor_map(&maps.q_token, bf16, a.q, 3, dims, strides, token) ||
+        !tensor_map(&maps.q_row, bf16, a.q, 3, dims, strides, row))
+      return cudaErrorInvalidValue;
   }
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(a.table ? page : a.tokens), (cuuint64_t)a.kv_heads,
                               (cuuint64_t)(a.table ? a.n_pages : 1)};
