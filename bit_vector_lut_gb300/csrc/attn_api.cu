@@ -206,6 +206,8 @@ int vq3_paged_plan(const int* cached, const int* fresh, int requests, int page_s
                         max_tokens, max_pages, ring_size);
   if (requests > kMaxRequests)
     return report_error(VQ3_EUNSUPPORTED, "paged_plan: requests=%d above %d", requests, kMaxRequests);
+  if (max_tokens > (1 << 30))
+    return report_error(VQ3_EUNSUPPORTED, "paged_plan: max_tokens=%d above 2^30", max_tokens);
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
     return report_error(VQ3_EUNSUPPORTED, "paged_plan: page_size=%d must be a power of two in [16, 256]", page_size);
   if (!ring || !ring_state || !q_start || !ring_state_out || !status ||
@@ -214,7 +216,7 @@ int vq3_paged_plan(const int* cached, const int* fresh, int requests, int page_s
   if (!on(cached, 4) || !on(fresh, 4) || !on(ring, 4) || !on(ring_state, 4) || !on(table, 4) || !on(q_start, 4) ||
       !on(kv_len, 4) || !on(slots, 8) || !on(positions, 4) || !on(ring_state_out, 4) || !on(status, 4))
     return report_error(VQ3_EALIGN, "paged_plan: pointers must be 4-byte (slots 8-byte) aligned");
-  if (ring_state == ring_state_out || table == ring || kv_len == cached || kv_len == fresh)
+  if (ring_state == ring_state_out || (requests && (table == ring || kv_len == cached || kv_len == fresh)))
     return report_error(VQ3_EINVAL, "paged_plan: outputs must not alias inputs");
   PlanArgs a{cached, fresh,     ring,           ring_state, table,    q_start,           kv_len,    slots,
              positions, ring_state_out, status,     requests, log2_of(page_size), ring_size, max_pages, max_tokens};

@@ -313,9 +313,9 @@ VQ3_API int vq3_delta_rule_forward(const uint16_t* q, const uint16_t* k, const u
  * q_start[r] .. q_start[r + 1] - 1 of q, out and lse, q_start ascending from
  * q_start[0]. Rows behind q_start[requests] are neither read nor written. All
  * lengths live in device memory, so that a captured graph serves any step that
- * fits its sizes. Strides are in elements and multiples of 8, pointers to FP16 or
- * BF16 data 16-byte aligned; the head_dim axis is contiguous; an axis of one
- * element may have any stride.
+ * fits its sizes. Strides are in elements, multiples of 8 and at least head_dim,
+ * pointers to FP16 or BF16 data 16-byte aligned; the head_dim axis is contiguous; an
+ * axis of one element may have any stride.
  * ---------------------------------------------------------------------------
  */
 #define VQ3_TYPE_F16 0
@@ -384,7 +384,8 @@ typedef struct vq3_attn {
  *              taken: table and ring state stay, q_start and kv_len are 0 and every slot
  *              and position -1, so that the step's other calls do nothing.
  * All device memory. One launch; calls with the same inputs write the same outputs.
- * requests at most 8192. Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ * requests at most 8192, max_tokens at most 2^30. Errors: VQ3_EINVAL, VQ3_EALIGN,
+ * VQ3_EUNSUPPORTED, VQ3_ECUDA.
  */
 #define VQ3_PLAN_NO_PAGES 1        /* fewer free pages than needed */
 #define VQ3_PLAN_NARROW_TABLE 2    /* a request needs more than max_pages pages */
@@ -420,11 +421,14 @@ VQ3_API size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_d
  * with scores, softmax statistics and sums in FP32, the probabilities rounded once to
  * the type of v (as the operand of the second product) and out rounded once. A row
  * that sees no key (kv_len < n) gets zeros and lse = -infinity. Keys and values behind
- * kv_len are never used, whatever the pages hold there; those of the request's own
- * tokens are finite. kv_len is cut to max_pages pages; a page number outside the cache
- * reads as zeros.
+ * kv_len are never used, whatever the pages hold there, and keys that a row does not
+ * see may hold anything; the values of the request's own tokens are finite (one that
+ * is not may make rows NaN that do not see it). kv_len is cut to max_pages pages; a
+ * page number outside the cache reads as zeros.
  * table: device [requests][max_pages]; kv_len: device [requests]; max_pages *
- * page_size at most 2^30, tokens * heads below 2^30. out does not overlap an input.
+ * page_size at most 2^30, tokens * heads below 2^30, and the batch's (row block, 64
+ * keys) pairs below 4e9, counted with max_pages pages a request (a prompt of a million
+ * tokens with 32 heads passes). out does not overlap an input.
  * Deterministic; results do not depend on where the pages lie.
  * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ENOSPACE, VQ3_ECUDA.
  */
@@ -434,7 +438,7 @@ VQ3_API int vq3_paged_attention(const vq3_attn* attn, const vq3_kv_cache* cache,
 /*
  * Causal attention over whole prompts, packed: row i of request r sees rows q_start[r]
  * .. q_start[r] + i of k and v (which have the same rows as q). Otherwise as
- * vq3_paged_attention.
+ * vq3_paged_attention; other requests' keys and values may hold anything.
  */
 VQ3_API int vq3_prompt_attention(const vq3_attn* attn, const vq3_kv_rows* rows, void* workspace, size_t ws_bytes,
                                  void* stream);

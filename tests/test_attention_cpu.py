@@ -109,6 +109,14 @@ def test_other_refusals():
     assert lib.vq3_kv_append(None, P, ctypes.byref(cache()), None) == INVALID
 
 
+def test_sizes_beyond_the_kernels_counters():
+    # tokens * heads of 2^30 and more, and (row block, key tile) pairs beyond 32 bits
+    assert paged(attn(tokens=1 << 27, heads=8)) == UNSUPPORTED
+    a = attn(tokens=1 << 26, heads=8, requests=8000)
+    assert paged(a, max_pages=1 << 23, n=1 << 40) == UNSUPPORTED
+    assert "pairs" in vq3.lib.vq3_last_error().decode()
+
+
 def test_axes_of_one_element_have_any_stride():
     # past every check up to the workspace, which is too small
     a = attn(tokens=1, heads=4, q_token=1, out_token=3)
@@ -133,7 +141,7 @@ def plan_call(**kw):
 @pytest.mark.parametrize("bad,code", [
     (dict(requests=-1), INVALID), (dict(requests=8193), UNSUPPORTED), (dict(page=24), UNSUPPORTED),
     (dict(page=8), UNSUPPORTED), (dict(ring_size=0), INVALID), (dict(max_pages=0), INVALID),
-    (dict(max_tokens=-1), INVALID), (dict(cached=None), INVALID), (dict(fresh=None), INVALID), (dict(ring=None), INVALID),
+    (dict(max_tokens=-1), INVALID), (dict(max_tokens=(1 << 30) + 1), UNSUPPORTED), (dict(cached=None), INVALID), (dict(fresh=None), INVALID), (dict(ring=None), INVALID),
     (dict(state=None), INVALID), (dict(table=None), INVALID), (dict(q_start=None), INVALID), (dict(kv_len=None), INVALID),
     (dict(slots=None), INVALID), (dict(positions=None), INVALID), (dict(out=None), INVALID), (dict(status=None), INVALID),
     (dict(slots=P + 4), ALIGN), (dict(table=P + 2), ALIGN), (dict(out=P), INVALID), (dict(kv_len=P), INVALID),

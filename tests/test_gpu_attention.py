@@ -199,6 +199,90 @@ def test_batch_that_memory_cannot_keep_up_with(vq3, heads):
     assert torch.equal(out[:n], again[:n]) and torch.equal(lse[:n], lse2[:n])
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (6, 1, 256), (2, 2, 64)])
+@pytest.mark.parametrize("requests,new", [(129, 1), (700, 1), (200, 7), (140, 30)])
+def test_many_requests(vq3, heads, requests, new):
+    # above 128 requests the CTAs' warps share the search for their range; some have no new tokens, some no keys
+    rng = np.random.default_rng(requests + new)
+    reqs = [(int(kv), int(min(kv + 2, n))) for kv, n in zip(rng.integers(0, 200, requests), rng.integers(0, new + 1, requests))]
+    reqs[0], reqs[-1] = (0, 0), (50, 0)
+    b = Batch(22, reqs, *heads, 16, "f16")
+    b.check(vq3)
+    b.check(vq3, max_new=0)
+
+
+def test_most_requests(vq3):
+    b = Batch(23, [(1 + i % 23, 1) for i in range(8192)], 2, 1, 64, 16, "bf16")
+    out, lse = b.run(vq3)
+    again, lse2 = b.run(vq3, max_new=0)
+    pick = [0, 1, 22, 4095, 8190, 8191]
+    for r in pick:
+        check(out[r : r + 1], lse[r : r + 1], b.q[r : r + 1], [b.keys[r]], [b.values[r]], [0, 1], [b.seen[r]], 64**-0.5, "bf16")
+        check(again[r : r + 1], lse2[r : r + 1], b.q[r : r + 1], [b.keys[r]], [b.values[r]], [0, 1], [b.seen[r]],
+              64**-0.5, "bf16")
+
+
+# groups that leave rows of a block over, that cut tokens between blocks, as large as a block and larger
+@pytest.mark.parametrize("group", [3, 5, 7, 12, 24, 43, 65, 96, 128, 160])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_groups(vq3, group, dim):
+    reqs = [(70, 64), (5, 1), (200, 3), (150, 11)]
+    Batch(24, reqs, 2 * group, 2, dim, 32, "bf16").check(vq3)
+
+
+@pytest.mark.parametrize("group", [3, 6, 48])
+def test_prompt_groups(vq3, group):
+    g = torch.Generator().manual_seed(25)
+    lens = [64, 85, 21, 2, 130]
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    for D in (64, 128, 256):
+        q, k, v = (normal(g, (sum(lens), h, D), "f16") for h in (2 * group, 2, 2))
+        out = vq3.prompt_attention(q, k, v, ints(starts), max_new=130)
+        cut = [slice(starts[r], starts[r + 1]) for r in range(len(lens))]
+        check(out, None, q, [k[c] for c in cut], [v[c] for c in cut], starts, [[i + 1 for i in range(n)] for n in lens],
+              D**-0.5, "f16")
+
+
+def test_two_streams_at_once(vq3):
+    # calls that overlap on the GPU, each with its own workspace, over one cache
+    a, b = (Batch(s, [(9000, n), (300, n)], 8, 2, 128, 64, "f16") for s, n in ((26, 1), (27, 90)))
+    want = [x.run(vq3)[0] for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for x, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                outs.append((x, vq3.paged_attention(x.q, x.k, x.v, x.table, x.q_start, x.kv_len, max_new=x.max_new)))
+    torch.cuda.synchronize()
+    for x, o in outs:
+        n = x.starts[-1]
+        assert torch.equal(o[:n], want[0 if x is a else 1][:n])
+
+
+def test_graphs_that_share_a_workspace(vq3):
+    # two captured calls of different kinds and sizes on one workspace, replayed in turn
+    a, b = (Batch(s, [(2000, n), (130, n)], 8, 2, 128, 64, "f16") for s, n in ((28, 1), (29, 70)))
+    ws = torch.full((max(vq3.attention_workspace_bytes(8, 2, 128, n) for n in (1, 70)),), 0xCD, dtype=torch.uint8,
+                    device=DEV)
+    want = [x.run(vq3)[0] for x in (a, b)]
+    graphs = []
+    for x in (a, b):
+        out = torch.empty_like(x.q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            vq3.paged_attention(x.q, x.k, x.v, x.table, x.q_start, x.kv_len, max_new=x.max_new, out=out, ws=ws)
+        graphs.append((g, out, x))
+    for i in range(9):
+        for j in ((0, 1), (1, 0), (0, 0, 1, 1))[i % 3]:
+            graphs[j][1].fill_(3.0)
+            graphs[j][0].replay()
+            n = graphs[j][2].starts[-1]
+            assert torch.equal(graphs[j][1][:n], want[j][:n])
+            assert vq3.workspace_status(ws) == 0
+
+
 def test_wrong_max_new_is_only_slower(vq3):
     b = Batch(9, [(300, 70), (20, 1)], 8, 2, 128, 16, "f16")
     for hint in (0, 1, 3, 1000):
@@ -384,6 +468,25 @@ def test_plan_that_cannot_be_met_takes_nothing(vq3, what, status):
     assert np.array_equal(t.cpu().numpy(), table)
     assert p.q_start.tolist() == [0] * 4 and p.kv_len.tolist() == [0] * 3
     assert (p.slots == -1).all() and (p.positions == -1).all() and p.ring_state.tolist() == [head, count]
+
+
+def test_empty_calls(vq3):
+    # no requests, no tokens: nothing written, the ring stays
+    table = torch.empty(0, 4, dtype=torch.int32, device=DEV)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    p = vq3.paged_plan(none, none, table, ints([1, 2]), ints([1, 2]), 16, 5)
+    assert p.status.item() == 0 and p.q_start.tolist() == [0] and p.ring_state.tolist() == [1, 2]
+    assert (p.slots == -1).all() and (p.positions == -1).all()
+    p = vq3.paged_plan(ints([3]), ints([0]), ints([[7]]), ints([1]), ints([0, 1]), 16, 0)
+    assert p.status.item() == 0 and p.slots.numel() == 0 and p.kv_len.tolist() == [3]
+    pages = torch.zeros(2, 16, 2, 64, dtype=torch.float16, device=DEV)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=DEV)
+    out = torch.full_like(q, 7.0)
+    vq3.paged_attention(q, pages, pages, table, ints([0]), none, out=out)
+    vq3.prompt_attention(q, q[:, :2], q[:, 2:], ints([0]), out=out)
+    assert (out == 7.0).all()
+    assert vq3.prompt_attention(q[:0], q[:0, :2], q[:0, 2:], ints([0, 0])).shape == (0, 4, 64)
+    vq3.kv_append(q[:0, :2], q[:0, 2:], torch.empty(0, dtype=torch.int64, device=DEV), pages, pages.clone())
 
 
 def test_plan_most_requests(vq3):
