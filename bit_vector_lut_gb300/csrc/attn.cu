@@ -494,6 +494,8 @@ cudaError_t launch_combine_t(const AttnArgs& a, int d, int grid, int slot_rows, 
 
 int attn_rows_limit(int head_dim) { return head_dim == 256 ? 8 : 16; }
 
+int attn_rows_unit_cost() { return 1; }
+
 int attn_rows_grid(int head_dim, int rows) {
   const bool one = rows <= 8;
   const int occ = head_dim == 256   ? rows_occ<256, 1>()

@@ -133,6 +133,7 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.heads = at->heads;
   a.kv_heads = kv_heads;
   a.group = group;
+  a.unit_cost = c.wide ? attn_wide_unit_cost(head_dim) : attn_rows_unit_cost();
   a.unit_blocks = c.wide ? attn_wide_blocks(head_dim) : 1;
   a.block_rows = c.slot_rows / a.unit_blocks;
   a.token_rows = c.wide ? a.block_rows / group * group : a.block_rows;
@@ -141,7 +142,7 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.by_token_unit = FastDiv(a.unit_blocks * a.token_rows);
   // the kernels count tiles of 64 or 128 keys in 32 bits
   const double units = (double)at->tokens * group / (a.unit_blocks * a.token_rows) + at->requests;
-  if (units * kv_heads * (a.max_kv / (c.wide ? 128.0 : 64.0) + 1) > 4e9)
+  if (units * kv_heads * (a.max_kv / (c.wide ? 128.0 : 64.0) + 8) > 4e9)
     return report_error(VQ3_EUNSUPPORTED, "%s: too many (row block, key tile) pairs: %d tokens, keys up to %d", who,
                         at->tokens, a.max_kv);
   a.scale_log2 = at->scale * 1.4426950408889634f;

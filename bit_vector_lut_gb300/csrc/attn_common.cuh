@@ -5,8 +5,9 @@
 // rows of a key/value head are (new token, query head of its group), row p = token p / G,
 // query head p % G, so the G heads of a group share every key and value that is read. A
 // unit's keys [0, end) are walked in tiles of kv_tile; end is what its last row sees.
-// All tiles of all units, laid end to end (request, key/value head, row block, tile), are
-// cut into equal contiguous ranges, one per CTA. A CTA that holds all of a unit writes its
+// All units, laid end to end (request, key/value head, row block), each as long as its tiles
+// and unit_cost more for starting and ending it, are cut into equal contiguous ranges, one
+// per CTA. (Without the unit_cost, CTAs with many short units ran 25% longer than the mean.) A CTA that holds all of a unit writes its
 // output; otherwise it leaves (max, sum, unnormalised output) in a slot of its own, at most
 // two per CTA: slot 2c for a unit that an earlier CTA began, slot 2c + 1 for one that it
 // begins and does not end. The combining pass sums a unit's slots in CTA order, so results
@@ -67,6 +68,7 @@ struct AttnArgs {
   // A unit has unit_blocks blocks of block_rows rows, all of them used, or only token_rows of them
   // so that a block holds whole tokens (see attn_request).
   int unit_blocks, block_rows, token_rows;
+  int unit_cost;       // what a unit costs beside its tiles, in tiles
   FastDiv by_group, by_unit, by_token_unit;  // group, unit_blocks * block_rows, unit_blocks * token_rows
   float scale_log2;    // scale * log2(e)
   float* part;         // [2 * grid][slot rows][D] unnormalised outputs
@@ -163,8 +165,8 @@ __device__ __forceinline__ int attn_unit_tiles(const AttnArgs& a, const AttnRequ
 }
 
 struct AttnPos {
-  int r, h, j, t;  // request, key/value head, unit of the head, first tile
-  unsigned tiles;  // tiles of this CTA's range (0: none)
+  int r, h, j, at;  // request, key/value head, unit of the head, offset in it: unit_cost, then its tiles
+  unsigned cost;    // length of this CTA's range (0: none)
 };
 
 // How a batch is divided. Plain: all tiles in one line, cut into equal ranges. Where the
@@ -174,19 +176,19 @@ struct AttnPos {
 // keys in L2. (64 rows of 6 heads behind 98,304 tokens of 4 x 256: 1.6 GB from memory and
 // 232 us with the plain cut.)
 struct AttnCut {
-  unsigned tiles;  // of the batch
-  int units;       // of the batch; 0: the plain cut
+  unsigned cost;  // of the batch
+  int units;      // of the batch; 0: the plain cut
   int ctas;
 };
-// What unit j counts: its tiles, or the CTAs that are its own. (The batch's tiles stay below
+// What unit j counts: its cost, or the CTAs that are its own. (The batch's costs stay below
 // 2^32: the entry points check a bound.)
 __device__ __forceinline__ unsigned attn_unit_cost(const AttnArgs& a, const AttnRequest& q, int j, int kv_tile,
                                                    int min_tiles, const AttnCut& cut) {
   const unsigned n = attn_unit_tiles(a, q, j, kv_tile);
-  if (cut.units == 0) return n;
+  if (cut.units == 0) return n + a.unit_cost;
   const unsigned spare = cut.ctas - cut.units, most = n / min_tiles;
   // at most the exact share, so that all shares fit the grid: the factor outweighs three roundings
-  const unsigned c = 1 + (unsigned)((float)spare * n / cut.tiles * 0.999999f);
+  const unsigned c = 1 + (unsigned)((float)spare * (n + a.unit_cost) / cut.cost * 0.999999f);
   return c <= most ? c : (most < 1 ? 1 : most);
 }
 
@@ -267,11 +269,12 @@ __device__ __forceinline__ void attn_inside(const AttnArgs& a, int r, unsigned c
   pos->j = j;
   if (cut.units) {  // CTA `at` of the unit's n
     const unsigned long long tiles = attn_unit_tiles(a, q, j, kv_tile);
-    pos->t = (int)(tiles * at / n);
-    pos->tiles = (unsigned)(tiles * (at + 1) / n) - pos->t;
+    const unsigned t0 = (unsigned)(tiles * at / n), t1 = (unsigned)(tiles * (at + 1) / n);
+    pos->at = t0 ? (int)t0 + a.unit_cost : 0;
+    pos->cost = t1 + a.unit_cost - pos->at;
   } else {
-    pos->t = at;
-    pos->tiles = plain;
+    pos->at = at;
+    pos->cost = plain;
   }
 }
 
@@ -302,7 +305,7 @@ __device__ __forceinline__ AttnPos attn_locate_warp(const AttnArgs& a, int kv_ti
     if (pass || !__any_sync(0xffffffffu, most > 1)) break;
     const int all = __reduce_add_sync(0xffffffffu, units);
     if (2 * all > cut.ctas) break;
-    cut.tiles = total;
+    cut.cost = total;
     cut.units = all;
   }
   unsigned s0, s1;
@@ -369,12 +372,12 @@ __device__ __noinline__ AttnPos attn_locate_block(const AttnArgs& a, int kv_tile
     }
     __syncthreads();
     if (pass || big <= 1 || 2 * all > (unsigned)cut.ctas) break;
-    cut.tiles = total;
+    cut.cost = total;
     cut.units = (int)all;
   }
   unsigned s0, s1;
   attn_range(cut, total, min_tiles, &s0, &s1);
-  if (tid == 0) result->tiles = 0;
+  if (tid == 0) result->cost = 0;
   __syncthreads();
   const unsigned warp_end = __shfl_sync(0xffffffffu, before + mine, 31);
   if (s1 > s0 && __shfl_sync(0xffffffffu, before, 0) <= s0 && s0 < warp_end) {
@@ -403,29 +406,30 @@ __device__ __noinline__ AttnPos attn_locate_block(const AttnArgs& a, int kv_tile
 struct AttnWalk {
   AttnRequest q;
   int r, h, j, t0, t1, n, end;  // tiles [t0, t1) of the unit's n; end: keys its last row sees
-  unsigned left;                // tiles of the range from this unit on
+  unsigned left;                // cost of the range from this unit on
 
-  __device__ __forceinline__ void unit(const AttnArgs& a, int kv_tile) {
+  // The range's share of unit j from offset `at` on. False: it ends before the unit's first tile.
+  __device__ __forceinline__ bool unit(const AttnArgs& a, int kv_tile, int at) {
     end = attn_unit_end(a, q, j);
     n = (int)((unsigned)(end + kv_tile - 1) / (unsigned)kv_tile);
     if (n < 1) n = 1;
-    t1 = left < (unsigned)(n - t0) ? t0 + (int)left : n;
+    const int whole = n + a.unit_cost, stop = left < (unsigned)(whole - at) ? at + (int)left : whole;
+    t0 = at > a.unit_cost ? at - a.unit_cost : 0;
+    t1 = stop > a.unit_cost ? stop - a.unit_cost : 0;
+    left -= stop - at;
+    return t1 > t0;
   }
   __device__ __forceinline__ bool start(const AttnArgs& a, const AttnPos& p, int kv_tile) {
-    left = p.tiles;
+    left = p.cost;
     if (left == 0) return false;
     r = p.r;
     h = p.h;
     j = p.j;
-    t0 = p.t;
     q = attn_request(a, r);
-    unit(a, kv_tile);
-    return true;
+    return unit(a, kv_tile, p.at);
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, int kv_tile) {
-    left -= t1 - t0;
     if (left == 0) return false;
-    t0 = 0;
     if (++j >= q.units) {
       j = 0;
       if (++h >= a.kv_heads) {
@@ -436,8 +440,7 @@ struct AttnWalk {
         } while (q.units == 0);
       }
     }
-    unit(a, kv_tile);
-    return true;
+    return unit(a, kv_tile, 0);
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
 };
@@ -462,6 +465,8 @@ __device__ __forceinline__ int attn_packed_row(const AttnArgs& a, int i, int bas
 // The two kernels and the combining pass.
 int attn_rows_limit(int head_dim);          // most packed rows of a request that the row kernel takes
 int attn_rows_grid(int head_dim, int rows); // CTAs of the row kernel
+int attn_rows_unit_cost();                  // AttnArgs::unit_cost
+int attn_wide_unit_cost(int head_dim);
 int attn_wide_grid();
 int attn_wide_blocks(int head_dim);  // row blocks of 128 of a unit of the tensor-core kernel
 cudaError_t launch_attn_rows(const AttnArgs& a, int head_dim, bool bf16, int nr, cudaStream_t st);

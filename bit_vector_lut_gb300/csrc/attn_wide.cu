@@ -883,6 +883,7 @@ cudaError_t launch_wide_t(const AttnArgs& a, int d, cudaStream_t st) {
 }  // namespace
 
 int attn_wide_grid() { return device_sm_count() < 608 ? device_sm_count() : 608; }
+int attn_wide_unit_cost(int head_dim) { return head_dim == 256 ? 3 : 2; }
 int attn_wide_blocks(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
 cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st) {
