@@ -173,8 +173,8 @@ struct AttnPos {
 // units of a request share its keys (several row blocks) and units are few, every unit gets
 // CTAs of its own instead, in proportion to its tiles, and its tiles are cut evenly among
 // them: units of equal length are then walked in step and all but the first read find the
-// keys in L2. (64 rows of 6 heads behind 98,304 tokens of 4 x 256: 1.6 GB from memory and
-// 232 us with the plain cut.)
+// keys in L2. (64 tokens of 24 heads behind 98,304 keys of 4 x 256, 12 units: 142 us, with the
+// plain cut 203.)
 struct AttnCut {
   unsigned cost;  // of the batch
   int units;      // of the batch; 0: the plain cut

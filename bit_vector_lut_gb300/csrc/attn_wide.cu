@@ -345,257 +345,257 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const __grid_con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<D>));
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------ copies
-    const int box = a.table ? (1 << a.page_shift < kTile ? 1 << a.page_shift : kTile) : kTile;  // rows per copy
-    const int boxes = kTile / box;
-    const int my_box = lane & (boxes - 1), my_cb = lane / boxes;  // this lane's copy of a stage
-    Ring<C::kStages> at;
-    int it = 0, units = 0;
-    AttnWalk w;
-    for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
-      if (w.end == 0) continue;
-      const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
-      // Q of the unit, once the last one's is used up
-      const auto copy_q = [&] {
-        if (units) wait(q_empty, (uint32_t)((units - 1) & 1));
-        if (dead) return;
-        const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
-        if (w.q.used == a.token_rows) {
-          if (lane == 0) {
-            mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.token_rows * 128));
-            for (int b = 0; b < blocks; ++b)
-              for (int cb = 0; cb < D / 64; ++cb)
-                tma_3d(q_at(b, cb), &maps.q, cb * 64, w.h * a.group, w.q.q0 + a.by_group(first + b * a.token_rows),
-                       q_full);
-          }
-        } else {
-          // a lane per token: its heads in one copy, or row by row where the block cuts them
-          const int last = first + blocks * kBlock < rows ? first + blocks * kBlock : rows;
-          if (lane == 0) mbar_expect_tx(q_full, (uint32_t)((last - first) * (D / 64) * 128));
-          __syncwarp();
-          for (int b = 0; b < blocks; ++b) {
-            const int p0 = first + b * kBlock, p1 = p0 + kBlock < last ? p0 + kBlock : last;
-            for (int t = a.by_group(p0) + lane; t * a.group < p1; t += 32) {
-              const int r0 = t * a.group > p0 ? t * a.group : p0, r1 = (t + 1) * a.group < p1 ? (t + 1) * a.group : p1;
-              for (int cb = 0; cb < D / 64; ++cb) {
-                if (r1 - r0 == a.group) {
-                  tma_3d(q_at(b, cb) + (uint32_t)(r0 - p0) * 128, &maps.q_token, cb * 64, w.h * a.group, w.q.q0 + t,
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<D>));
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------ copies
+      const int box = a.table ? (1 << a.page_shift < kTile ? 1 << a.page_shift : kTile) : kTile;  // rows per copy
+      const int boxes = kTile / box;
+      const int my_box = lane & (boxes - 1), my_cb = lane / boxes;  // this lane's copy of a stage
+      Ring<C::kStages> at;
+      int it = 0, units = 0;
+      AttnWalk w;
+      for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+        if (w.end == 0) continue;
+        const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
+        // Q of the unit, once the last one's is used up
+        const auto copy_q = [&] {
+          if (units) wait(q_empty, (uint32_t)((units - 1) & 1));
+          if (dead) return;
+          const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
+          if (w.q.used == a.token_rows) {
+            if (lane == 0) {
+              mbar_expect_tx(q_full, (uint32_t)(blocks * (D / 64) * a.token_rows * 128));
+              for (int b = 0; b < blocks; ++b)
+                for (int cb = 0; cb < D / 64; ++cb)
+                  tma_3d(q_at(b, cb), &maps.q, cb * 64, w.h * a.group, w.q.q0 + a.by_group(first + b * a.token_rows),
                          q_full);
-                } else {
-                  for (int r = r0; r < r1; ++r)
-                    tma_3d(q_at(b, cb) + (uint32_t)(r - p0) * 128, &maps.q_row, cb * 64,
-                           w.h * a.group + r - t * a.group, w.q.q0 + t, q_full);
+            }
+          } else {
+            // a lane per token: its heads in one copy, or row by row where the block cuts them
+            const int last = first + blocks * kBlock < rows ? first + blocks * kBlock : rows;
+            if (lane == 0) mbar_expect_tx(q_full, (uint32_t)((last - first) * (D / 64) * 128));
+            __syncwarp();
+            for (int b = 0; b < blocks; ++b) {
+              const int p0 = first + b * kBlock, p1 = p0 + kBlock < last ? p0 + kBlock : last;
+              for (int t = a.by_group(p0) + lane; t * a.group < p1; t += 32) {
+                const int r0 = t * a.group > p0 ? t * a.group : p0, r1 = (t + 1) * a.group < p1 ? (t + 1) * a.group : p1;
+                for (int cb = 0; cb < D / 64; ++cb) {
+                  if (r1 - r0 == a.group) {
+                    tma_3d(q_at(b, cb) + (uint32_t)(r0 - p0) * 128, &maps.q_token, cb * 64, w.h * a.group, w.q.q0 + t,
+                           q_full);
+                  } else {
+                    for (int r = r0; r < r1; ++r)
+                      tma_3d(q_at(b, cb) + (uint32_t)(r - p0) * 128, &maps.q_row, cb * 64,
+                             w.h * a.group + r - t * a.group, w.q.q0 + t, q_full);
+                  }
                 }
               }
             }
           }
-        }
-        __syncwarp();
-        ++units;
-      };
-      // the page of this lane's rows of tile t
-      const auto page_of = [&](int t) -> int {
-        const int x = t * kTile + my_box * box;
-        if (!a.table || t >= w.t1 || x >= w.end) return 0;
-        const size_t at = (size_t)w.r * a.max_pages + (x >> a.page_shift);
-        return VQ3_IN(at, (size_t)a.requests * a.max_pages, 1) ? __ldg(a.table + at) : -1;
-      };
-      const auto copy = [&](const CUtensorMap* map, int t, int page) {
-        const int left = w.end - t * kTile;  // keys of the tile that count
-        const int n = a.table ? ((left < kTile ? left : kTile) + box - 1) / box : 1;
-        const int x = t * kTile + my_box * box;
-        const int row = a.table ? x & ((1 << a.page_shift) - 1) : w.q.q0 + x;
-#pragma unroll
-        for (int part = 0; part < C::kParts; ++part, ++it, at = at.plus(1)) {
-          const int s = at.s;
-          if (it >= C::kStages) wait(empty(s), at.phase ^ 1u);
-          if (dead) return;
-          if (lane == 0) mbar_expect_tx(full(s), (uint32_t)(n * C::kCb * box * 128));
           __syncwarp();
-          if (my_box < n && my_cb < C::kCb)
-            tma_4d(stage_at(s) + (uint32_t)(my_cb * C::kCbBytes + my_box * box * 128), map,
-                   part * C::kStageCols + my_cb * 64, row, w.h, a.table ? page : 0, full(s));
+          ++units;
+        };
+        // the page of this lane's rows of tile t
+        const auto page_of = [&](int t) -> int {
+          const int x = t * kTile + my_box * box;
+          if (!a.table || t >= w.t1 || x >= w.end) return 0;
+          const size_t at = (size_t)w.r * a.max_pages + (x >> a.page_shift);
+          return VQ3_IN(at, (size_t)a.requests * a.max_pages, 1) ? __ldg(a.table + at) : -1;
+        };
+        const auto copy = [&](const CUtensorMap* map, int t, int page) {
+          const int left = w.end - t * kTile;  // keys of the tile that count
+          const int n = a.table ? ((left < kTile ? left : kTile) + box - 1) / box : 1;
+          const int x = t * kTile + my_box * box;
+          const int row = a.table ? x & ((1 << a.page_shift) - 1) : w.q.q0 + x;
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part, ++it, at = at.plus(1)) {
+            const int s = at.s;
+            if (it >= C::kStages) wait(empty(s), at.phase ^ 1u);
+            if (dead) return;
+            if (lane == 0) mbar_expect_tx(full(s), (uint32_t)(n * C::kCb * box * 128));
+            __syncwarp();
+            if (my_box < n && my_cb < C::kCb)
+              tma_4d(stage_at(s) + (uint32_t)(my_cb * C::kCbBytes + my_box * box * 128), map,
+                     part * C::kStageCols + my_cb * 64, row, w.h, a.table ? page : 0, full(s));
+          }
+        };
+        // the first keys go ahead of Q: their stage is free sooner
+        int page = page_of(w.t0);
+        copy(&maps.k, w.t0, page);
+        copy_q();
+        if constexpr (NB == 2) {
+          for (int t = w.t0; t < w.t1; ++t) {
+            const int next = page_of(t + 1);
+            if (t > w.t0) copy(&maps.k, t, page);
+            copy(&maps.v, t, page);
+            page = next;
+          }
+        } else {
+          int ahead = page_of(w.t0 + 1);
+          for (int t = w.t0; t < w.t1; ++t) {
+            const int next = page_of(t + 2);
+            if (t + 1 < w.t1) copy(&maps.k, t + 1, ahead);
+            copy(&maps.v, t, page);
+            page = ahead;
+            ahead = next;
+          }
+        }
+      }
+      // no copy is in flight when the CTA ends (they have all been used unless a wait gave up)
+      if (units) mbar_drain(q_full, (uint32_t)((units - 1) & 1));
+      for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+        mbar_drain(full(j % C::kStages), (uint32_t)((j / C::kStages) & 1));
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t id_qk = idesc(kTile, kBf16, false), id_pv = idesc(C::kStageCols, kBf16, true);
+      using Place = Ring<C::kStages>;
+      Place it;                   // the next stage of the ring
+      int units = 0;
+      int tiles[2] = {0, 0};      // tiles of block b (one block: all, [0])
+      int outs[2] = {0, 0};       // units of block b
+      AttnWalk w;
+      // A wait or a commit between two products leaves the tensor pipe idle once the few that are
+      // queued have run, so the waits for stages (mostly long since filled) and the releases of
+      // stages sit between the parts of a product, not between two products.
+      // Part of S buffer `buf` = Q of block b times the stages at `at`
+      const auto qk = [&](int b, int buf, Place at, int part) {
+        if (dead) return;
+#pragma unroll
+        for (int c = 0; c < C::kCb; ++c)
+          mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, part * C::kCb + c), 16),
+                  desc_sw128(stage_at(at.plus(part).s) + (uint32_t)(c * C::kCbBytes), 16), id_qk, part + c > 0);
+      };
+      // Part of O of block b (+)= P in S buffer `buf`, steps [k0, k1) of 16 keys, times the stages at `at`
+      const auto pv = [&](int b, int buf, Place at, int part, int k0, int k1, bool first) {
+        if (dead) return;
+        const uint32_t p = tmem + (uint32_t)(buf * kTile);
+        const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
+        const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (k0 <= 4 * h && k1 >= 4 * h + 4) {
+            mma_ts4(o, p + 64u * h, v + 512u * h, id_pv, !first || h > 0);
+          } else {
+            for (int k = k0 > 4 * h ? k0 : 4 * h; k < k1 && k < 4 * h + 4; ++k)
+              mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
+          }
         }
       };
-      // the first keys go ahead of Q: their stage is free sooner
-      int page = page_of(w.t0);
-      copy(&maps.k, w.t0, page);
-      copy_q();
-      if constexpr (NB == 2) {
-        for (int t = w.t0; t < w.t1; ++t) {
-          const int next = page_of(t + 1);
-          if (t > w.t0) copy(&maps.k, t, page);
-          copy(&maps.v, t, page);
-          page = next;
+      const auto release = [&](Place at) {
+#pragma unroll
+        for (int p = 0; p < C::kParts; ++p) mma_commit(empty(at.plus(p).s));
+      };
+      const auto wait_stages = [&](Place at) {
+#pragma unroll
+        for (int p = 0; p < C::kParts; ++p) wait(full(at.plus(p).s), at.plus(p).phase);
+      };
+      // V rows of the last step that lie behind the keys: zero (the probabilities there are zero,
+      // but what the memory holds need not be finite)
+      const auto clear_tail = [&](Place at, int keys) {
+        if (keys % 16 == 0 || dead) return;
+        const int r0 = keys, r1 = (keys + 15) & ~15;
+        for (int i = lane; i < (r1 - r0) * C::kCb * C::kParts * 8; i += 32) {
+          const int chunk = i & 7, cb = (i >> 3) % (C::kCb * C::kParts), r = r0 + (i >> 3) / (C::kCb * C::kParts);
+          const uint32_t p = stage_at(at.plus(cb / C::kCb).s) +
+                             (uint32_t)((cb % C::kCb) * C::kCbBytes + r * 128 + chunk * 16);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
         }
-      } else {
-        int ahead = page_of(w.t0 + 1);
-        for (int t = w.t0; t < w.t1; ++t) {
-          const int next = page_of(t + 2);
-          if (t + 1 < w.t1) copy(&maps.k, t + 1, ahead);
-          copy(&maps.v, t, page);
-          page = ahead;
-          ahead = next;
-        }
-      }
-    }
-    // no copy is in flight when the CTA ends (they have all been used unless a wait gave up)
-    if (units) mbar_drain(q_full, (uint32_t)((units - 1) & 1));
-    for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
-      mbar_drain(full(j % C::kStages), (uint32_t)((j / C::kStages) & 1));
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t id_qk = idesc(kTile, kBf16, false), id_pv = idesc(C::kStageCols, kBf16, true);
-    using Place = Ring<C::kStages>;
-    Place it;                   // the next stage of the ring
-    int units = 0;
-    int tiles[2] = {0, 0};      // tiles of block b (one block: all, [0])
-    int outs[2] = {0, 0};       // units of block b
-    AttnWalk w;
-    // A wait or a commit between two products leaves the tensor pipe idle once the few that are
-    // queued have run, so the waits for stages (mostly long since filled) and the releases of
-    // stages sit between the parts of a product, not between two products.
-    // Part of S buffer `buf` = Q of block b times the stages at `at`
-    const auto qk = [&](int b, int buf, Place at, int part) {
-      if (dead) return;
-#pragma unroll
-      for (int c = 0; c < C::kCb; ++c)
-        mma_ss4(tmem + (uint32_t)(buf * kTile), desc_sw128(q_at(b, part * C::kCb + c), 16),
-                desc_sw128(stage_at(at.plus(part).s) + (uint32_t)(c * C::kCbBytes), 16), id_qk, part + c > 0);
-    };
-    // Part of O of block b (+)= P in S buffer `buf`, steps [k0, k1) of 16 keys, times the stages at `at`
-    const auto pv = [&](int b, int buf, Place at, int part, int k0, int k1, bool first) {
-      if (dead) return;
-      const uint32_t p = tmem + (uint32_t)(buf * kTile);
-      const uint64_t v = desc_sw128(stage_at(at.plus(part).s), C::kCbBytes);
-      const uint32_t o = tmem + C::kO + (uint32_t)(b * D + part * C::kStageCols);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (k0 <= 4 * h && k1 >= 4 * h + 4) {
-          mma_ts4(o, p + 64u * h, v + 512u * h, id_pv, !first || h > 0);
-        } else {
-          for (int k = k0 > 4 * h ? k0 : 4 * h; k < k1 && k < 4 * h + 4; ++k)
-            mma_ts1(o, p + p_col(k), v + 128u * k, id_pv, !first || k > 0);
-        }
-      }
-    };
-    const auto release = [&](Place at) {
-#pragma unroll
-      for (int p = 0; p < C::kParts; ++p) mma_commit(empty(at.plus(p).s));
-    };
-    const auto wait_stages = [&](Place at) {
-#pragma unroll
-      for (int p = 0; p < C::kParts; ++p) wait(full(at.plus(p).s), at.plus(p).phase);
-    };
-    // V rows of the last step that lie behind the keys: zero (the probabilities there are zero,
-    // but what the memory holds need not be finite)
-    const auto clear_tail = [&](Place at, int keys) {
-      if (keys % 16 == 0 || dead) return;
-      const int r0 = keys, r1 = (keys + 15) & ~15;
-      for (int i = lane; i < (r1 - r0) * C::kCb * C::kParts * 8; i += 32) {
-        const int chunk = i & 7, cb = (i >> 3) % (C::kCb * C::kParts), r = r0 + (i >> 3) / (C::kCb * C::kParts);
-        const uint32_t p = stage_at(at.plus(cb / C::kCb).s) +
-                           (uint32_t)((cb % C::kCb) * C::kCbBytes + r * 128 + chunk * 16);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-    };
-    for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
-      if (w.end == 0) continue;
-      const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
-      const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
-      wait(q_full, (uint32_t)(units & 1));
-      ++units;
-      wait_stages(it);
-      tc_after();
-      if constexpr (NB == 2) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b >= blocks) continue;
-          qk(b, b, it, 0);
-          mma_commit(s_full(b));
-        }
-        release(it);
-        it = it.plus(1);
-        if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      for (bool on = w.start(a, pos, kTile); on; on = w.next(a, kTile)) {
+        if (w.end == 0) continue;
+        const int rows = w.q.n_new * a.group, first = w.j * NB * w.q.used;
+        const int blocks = NB == 2 && first + w.q.used < rows ? 2 : 1;
+        wait(q_full, (uint32_t)(units & 1));
+        ++units;
         wait_stages(it);
-        for (int t = w.t0; t < w.t1; ++t) {
-          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
-          const Place vs = it, ks = it.plus(1), next = it.plus(2);
-          const bool more = t + 1 < w.t1;
-          clear_tail(vs, keys);
+        tc_after();
+        if constexpr (NB == 2) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b >= blocks) continue;
-            const bool last = b + 1 == blocks;
-            if (t == w.t0 && outs[b]) wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1));
-            wait(p_half(b), (uint32_t)(tiles[b] & 1));
-            tc_after();
-            pv(b, b, vs, 0, 0, steps < 4 ? steps : 4, t == w.t0);
-            if (b == 0 && more) wait_stages(ks);
-            wait(p_full(b), (uint32_t)(tiles[b] & 1));
-            tc_after();
-            pv(b, b, vs, 0, 4, steps, false);
-            ++tiles[b];
-            if (more) {
-              if (last) wait_stages(next);  // the next tile's values
-              qk(b, b, ks, 0);
-              mma_commit(s_full(b));
-            } else {
-              mma_commit(pv_done(b));
-            }
+            qk(b, b, it, 0);
+            mma_commit(s_full(b));
           }
-          release(vs);
-          if (more) release(ks);
-          if (t + 2 == w.t1) mma_commit(q_empty);
-          it = more ? next : ks;
-        }
-        ++outs[0];
-        if (blocks == 2) ++outs[1];
-      } else {
+          release(it);
+          it = it.plus(1);
+          if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+          wait_stages(it);
+          for (int t = w.t0; t < w.t1; ++t) {
+            const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
+            const Place vs = it, ks = it.plus(1), next = it.plus(2);
+            const bool more = t + 1 < w.t1;
+            clear_tail(vs, keys);
 #pragma unroll
-        for (int p = 0; p < C::kParts; ++p) qk(0, tiles[0] & 1, it, p);
-        mma_commit(s_full(tiles[0] & 1));
-        release(it);
-        it = it.plus(C::kParts);
-        if (w.t1 - w.t0 == 1) mma_commit(q_empty);
-        for (int t = w.t0; t < w.t1; ++t, ++tiles[0]) {
-          const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
-          const int buf = tiles[0] & 1;
-          const bool more = t + 1 < w.t1;
-          const Place ks = it, vs = more ? it.plus(C::kParts) : it, next = vs.plus(C::kParts);
-          if (more) {  // S of the next tile; its keys have been waited for
-            wait_stages(ks);
-            tc_after();
-            qk(0, buf ^ 1, ks, 0);
-            qk(0, buf ^ 1, ks, 1);
-            mma_commit(s_full(buf ^ 1));
-            release(ks);
+            for (int b = 0; b < 2; ++b) {
+              if (b >= blocks) continue;
+              const bool last = b + 1 == blocks;
+              if (t == w.t0 && outs[b]) wait(o_empty(b), (uint32_t)((outs[b] - 1) & 1));
+              wait(p_half(b), (uint32_t)(tiles[b] & 1));
+              tc_after();
+              pv(b, b, vs, 0, 0, steps < 4 ? steps : 4, t == w.t0);
+              if (b == 0 && more) wait_stages(ks);
+              wait(p_full(b), (uint32_t)(tiles[b] & 1));
+              tc_after();
+              pv(b, b, vs, 0, 4, steps, false);
+              ++tiles[b];
+              if (more) {
+                if (last) wait_stages(next);  // the next tile's values
+                qk(b, b, ks, 0);
+                mma_commit(s_full(b));
+              } else {
+                mma_commit(pv_done(b));
+              }
+            }
+            release(vs);
+            if (more) release(ks);
             if (t + 2 == w.t1) mma_commit(q_empty);
+            it = more ? next : ks;
           }
-          wait_stages(vs);
-          clear_tail(vs, keys);
-          if (t == w.t0 && outs[0]) wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1));
-          wait(p_full(buf), (uint32_t)((tiles[0] >> 1) & 1));
-          tc_after();
-          pv(0, buf, vs, 0, 0, steps, t == w.t0);
-          pv(0, buf, vs, 1, 0, steps, t == w.t0);
-          mma_commit(pv_done(buf));
-          release(vs);
-          it = next;
+          ++outs[0];
+          if (blocks == 2) ++outs[1];
+        } else {
+#pragma unroll
+          for (int p = 0; p < C::kParts; ++p) qk(0, tiles[0] & 1, it, p);
+          mma_commit(s_full(tiles[0] & 1));
+          release(it);
+          it = it.plus(C::kParts);
+          if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+          for (int t = w.t0; t < w.t1; ++t, ++tiles[0]) {
+            const int keys = w.end - t * kTile < kTile ? w.end - t * kTile : kTile, steps = (keys + 15) / 16;
+            const int buf = tiles[0] & 1;
+            const bool more = t + 1 < w.t1;
+            const Place ks = it, vs = more ? it.plus(C::kParts) : it, next = vs.plus(C::kParts);
+            if (more) {  // S of the next tile; its keys have been waited for
+              wait_stages(ks);
+              tc_after();
+              qk(0, buf ^ 1, ks, 0);
+              qk(0, buf ^ 1, ks, 1);
+              mma_commit(s_full(buf ^ 1));
+              release(ks);
+              if (t + 2 == w.t1) mma_commit(q_empty);
+            }
+            wait_stages(vs);
+            clear_tail(vs, keys);
+            if (t == w.t0 && outs[0]) wait(o_empty(0), (uint32_t)((outs[0] - 1) & 1));
+            wait(p_full(buf), (uint32_t)((tiles[0] >> 1) & 1));
+            tc_after();
+            pv(0, buf, vs, 0, 0, steps, t == w.t0);
+            pv(0, buf, vs, 1, 0, steps, t == w.t0);
+            mma_commit(pv_done(buf));
+            release(vs);
+            it = next;
+          }
+          ++outs[0];
         }
-        ++outs[0];
       }
+      // every product has completed before tensor memory is freed
+      mma_commit(drain);
+      mbar_drain(drain, 0);
+      __syncwarp();
     }
-    // every product has completed before tensor memory is freed
-    mma_commit(drain);
-    mbar_drain(drain, 0);
-    __syncwarp();
-  }
   } else {
     // ------------------------------------------------------------ softmax and output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax<D>));
@@ -883,7 +883,9 @@ cudaError_t launch_wide_t(const AttnArgs& a, int d, cudaStream_t st) {
 }  // namespace
 
 int attn_wide_grid() { return device_sm_count() < 608 ? device_sm_count() : 608; }
-int attn_wide_unit_cost(int head_dim) { return head_dim == 256 ? 3 : 2; }
+// Measured on an 8,192-token prompt of 32 x 128 (0 / 1 / 2 tiles: 506 / 459 / 463 us), packed prompts of
+// 16 x 64 (45.2 / 42.3 / 43.2 us) and ragged prompts of 24 x 256 (0 / 2 / 3 / 4: 391 / 337 / 327 / 333 us).
+int attn_wide_unit_cost(int head_dim) { return head_dim == 256 ? 3 : 1; }
 int attn_wide_blocks(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
 cudaError_t launch_attn_wide(const AttnArgs& a, int head_dim, bool bf16, cudaStream_t st) {

@@ -11,7 +11,8 @@ namespace {
 // the requests are taken from the ring of free pages in request order. Every CTA finds the
 // prefix sums of all requests itself (8 bytes a request, from L2: cheaper than handing them
 // over between CTAs or launches) and then writes its share of the tokens, new pages and
-// requests. Bound by latency: two dependent reads from memory and one scan.
+// requests. Bound by latency: two dependent reads from memory and one scan (4 requests 3.2 us;
+// 700 requests with 63K new tokens 6.3 us, 0.8 MB written).
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 1024;  // tokens per CTA
 
@@ -153,7 +154,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 //
 // Copies row t of k and v to its slot's place, 16 bytes a thread and step, keys and values
 // together. Bound by memory: rows are read once past L1, the cache lines written stay in L2
-// for the attention that reads them next.
+// for the attention that reads them next. 16,411 tokens of 8 x 128 (134 MB in and out): 23.5 us,
+// 5.7 TB/s, 84% of a plain copy's rate; two or four chunks a thread in flight took 24.0 and
+// 27.3 us.
 constexpr int kAppThreads = 256;
 
 __device__ __forceinline__ uint4 ldg_once(const uint16_t* p) {
