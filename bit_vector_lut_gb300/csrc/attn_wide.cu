@@ -883,8 +883,9 @@ cudaError_t launch_wide_t(const AttnArgs& a, int d, cudaStream_t st) {
 }  // namespace
 
 int attn_wide_grid() { return device_sm_count() < 608 ? device_sm_count() : 608; }
-// Measured on an 8,192-token prompt of 32 x 128 (0 / 1 / 2 tiles: 506 / 459 / 463 us), packed prompts of
-// 16 x 64 (45.2 / 42.3 / 43.2 us) and ragged prompts of 24 x 256 (0 / 2 / 3 / 4: 391 / 337 / 327 / 333 us).
+// Measured on an 8,192-token prompt of 32 x 128 (0 tiles: 506 us; 1 and 2: 459 to 466 us, which of the two
+// leads changed with the build), packed prompts of 16 x 64 (0 / 1 / 2: 45.2 / 42.3 / 43.2 us) and ragged
+// prompts of 24 x 256 (0 / 2 / 3 / 4: 391 / 337 / 327 / 333 us).
 int attn_wide_unit_cost(int head_dim) { return head_dim == 256 ? 3 : 1; }
 int attn_wide_blocks(int head_dim) { return head_dim == 256 ? 1 : 2; }
 
