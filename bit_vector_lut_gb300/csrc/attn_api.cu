@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxRequests = 8192;
 constexpr int kMaxKeys = 1 << 30;  // of one request
+constexpr float kLog2e = 1.4426950408889634f;
 
 bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -145,7 +146,7 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   if (units * kv_heads * (a.max_kv / (c.wide ? 128.0 : 64.0) + 8) > 4e9)
     return report_error(VQ3_EUNSUPPORTED, "%s: too many (row block, key tile) pairs: %d tokens, keys up to %d", who,
                         at->tokens, a.max_kv);
-  a.scale_log2 = at->scale * 1.4426950408889634f;
+  a.scale_log2 = at->scale * kLog2e;
   a.status = reinterpret_cast<int*>(ws);
   a.rec = reinterpret_cast<AttnRec*>(ws + w.rec);
   a.part_ml = reinterpret_cast<float*>(ws + w.ml);
@@ -171,8 +172,9 @@ int check_attn(vq3_attn* at, int kv_heads, int head_dim, const char* who, bool* 
     return report_error(VQ3_EUNSUPPORTED, "%s: requests=%d above %d", who, at->requests, kMaxRequests);
   if ((long long)at->tokens * at->heads > 0x3fffffffLL)
     return report_error(VQ3_EUNSUPPORTED, "%s: tokens * heads above 2^30", who);
-  if (!(at->scale > 0.f) || !std::isfinite(at->scale))
-    return report_error(VQ3_EINVAL, "%s: scale=%g must be positive and finite", who, (double)at->scale);
+  // the kernels use scale * log2(e): that has to be finite, too
+  if (!(at->scale > 0.f) || !std::isfinite(at->scale * kLog2e))
+    return report_error(VQ3_EINVAL, "%s: scale=%g must be positive and at most 2e38", who, (double)at->scale);
   if (at->tokens == 0 || at->requests == 0) {
     *done = true;
     return VQ3_OK;

@@ -355,7 +355,7 @@ typedef struct vq3_attn {
   int requests; /* at most 8192 */
   int max_new;  /* most new tokens of a request, 0 if unknown. Only picks the kernel: a wrong
                    value costs time, not correctness */
-  float scale;  /* of the scores, positive (1 / sqrt(head_dim) for instance) */
+  float scale;  /* of the scores, positive, at most 2e38 (1 / sqrt(head_dim) for instance) */
   const void* q;
   void* out;
   float* lse;   /* [tokens][heads] natural logarithm of the softmax's sum, or NULL */

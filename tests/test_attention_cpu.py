@@ -206,3 +206,9 @@ def test_oracle_plan_pins():
     assert st == 0 and tab.tolist() == [[4, 3, -1], [7, 2, -1]] and qs == [0, 2, 3] and kv == [18, 21]
     assert slots == [48, 49, 36, -1, -1] and pos == [16, 17, 20, -1, -1] and state == (0, 1)
     assert A.plan([16, 20], [2, 1], table, [9, 5, 3], 2, 0, 16, 2)[0] == 5
+
+
+@pytest.mark.parametrize("scale,code", [(3e38, INVALID), (2.4e38, INVALID), (2.3e38, SPACE), (1e-30, SPACE)])
+def test_scale_in_the_kernels_domain(scale, code):
+    # scale * log2(e) is what the kernels use: 2.36e38 * 1.4427 is the largest FP32 number
+    assert paged(attn(scale=scale), n=1) == code and prompt(attn(scale=scale), n=1) == code
