@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMaxRequests = 8192;
 constexpr int kMaxKeys = 1 << 30;  // of one request
+constexpr int kMaxKvHeads = 1 << 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -19,6 +20,12 @@ int log2_of(int v) {
   return s;
 }
 
+// The append counts a row's 16-byte chunks (up to 32 a head) in 32 bits.
+int check_kv_heads(int n, const char* who) {
+  if (n <= 0) return report_error(VQ3_EINVAL, "%s: kv_heads=%d", who, n);
+  if (n > kMaxKvHeads) return report_error(VQ3_EUNSUPPORTED, "%s: kv_heads=%d above %d", who, n, kMaxKvHeads);
+  return VQ3_OK;
+}
 int check_head_dim(int d, const char* who) {
   if (d != 64 && d != 128 && d != 256)
     return report_error(VQ3_EUNSUPPORTED, "%s: head_dim=%d must be 64, 128 or 256", who, d);
@@ -38,7 +45,7 @@ int check_stride(long long* s, long long extent, long long row, const char* who,
 }
 
 int check_cache(vq3_kv_cache* c, const char* who) {
-  if (c->kv_heads <= 0) return report_error(VQ3_EINVAL, "%s: kv_heads=%d", who, c->kv_heads);
+  if (int rc = check_kv_heads(c->kv_heads, who)) return rc;
   if (int rc = check_head_dim(c->head_dim, who)) return rc;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return report_error(VQ3_EUNSUPPORTED, "%s: page_size=%d must be a power of two in [16, 256]", who, c->page_size);
@@ -58,7 +65,7 @@ int check_cache(vq3_kv_cache* c, const char* who) {
 }
 
 int check_rows(vq3_kv_rows* r, const char* who) {
-  if (r->kv_heads <= 0) return report_error(VQ3_EINVAL, "%s: kv_heads=%d", who, r->kv_heads);
+  if (int rc = check_kv_heads(r->kv_heads, who)) return rc;
   if (int rc = check_head_dim(r->head_dim, who)) return rc;
   if (r->tokens < 0) return report_error(VQ3_EINVAL, "%s: tokens=%d", who, r->tokens);
   if (r->tokens == 0) return VQ3_OK;

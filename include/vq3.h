@@ -323,7 +323,7 @@ VQ3_API int vq3_delta_rule_forward(const uint16_t* q, const uint16_t* k, const u
 
 /* The cache: pages of page_size tokens. Token x of a request is row x % page_size of
  * page table[r][x / page_size]. Any order of the page, token and head axes.
- * kv_heads >= 1; head_dim 64, 128 or 256; page_size a power of two in [16, 256]. */
+ * kv_heads 1 to 65536; head_dim 64, 128 or 256; page_size a power of two in [16, 256]. */
 typedef struct vq3_kv_cache {
   int kv_heads;
   int head_dim;

@@ -212,3 +212,13 @@ def test_oracle_plan_pins():
 def test_scale_in_the_kernels_domain(scale, code):
     # scale * log2(e) is what the kernels use: 2.36e38 * 1.4427 is the largest FP32 number
     assert paged(attn(scale=scale), n=1) == code and prompt(attn(scale=scale), n=1) == code
+
+
+@pytest.mark.parametrize("n", [(1 << 16) + 1, 5 << 25, 1 << 30])
+def test_more_heads_than_a_row_counts(n):
+    # 5 * 2^25 heads of 32 chunks are 2^30 in 32 bits: another row's size, not an overflow that shows
+    c, r = cache(kv_heads=n, head_dim=256, k_head=256, v_head=256), rows(kv_heads=n, head_dim=256, k_head=256, v_head=256)
+    c.k_token = c.v_token = r.k_token = r.v_token = 256 * n
+    c.k_page = c.v_page = 256 * n
+    assert append(r, c=c) == UNSUPPORTED and "kv_heads" in vq3.lib.vq3_last_error().decode()
+    assert paged(c=c) == UNSUPPORTED and prompt(r=r) == UNSUPPORTED
