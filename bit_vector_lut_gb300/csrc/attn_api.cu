@@ -166,6 +166,15 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   return report_ok();
 }
 
+// A call without rows or requests: only the status word of its workspace, if it has one.
+int nothing(void* workspace, size_t ws_bytes, void* stream, const char* who) {
+  if (!workspace || ws_bytes < sizeof(int)) return report_ok();
+  if (!on(workspace, 256)) return report_error(VQ3_EALIGN, "%s: workspace must be 256-byte aligned", who);
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(VQ3_ECUDA, "%s: status word: %s", who, cudaGetErrorString(e));
+  return report_ok();
+}
+
 // Checks of the query side that both forms share. *done: a valid call with nothing to do.
 int check_attn(vq3_attn* at, int kv_heads, int head_dim, const char* who, bool* done) {
   *done = false;
@@ -276,7 +285,7 @@ int vq3_paged_attention(const vq3_attn* attn, const vq3_kv_cache* cache, const i
   if (max_pages <= 0) return report_error(VQ3_EINVAL, "paged_attention: max_pages=%d", max_pages);
   if ((long long)max_pages * c.page_size > kMaxKeys)
     return report_error(VQ3_EUNSUPPORTED, "paged_attention: max_pages * page_size above 2^30");
-  if (done) return report_ok();
+  if (done) return nothing(workspace, ws_bytes, stream, "paged_attention");
   if (!table || !kv_len) return report_error(VQ3_EINVAL, "paged_attention: null table or kv_len");
   if (!on(table, 4) || !on(kv_len, 4))
     return report_error(VQ3_EALIGN, "paged_attention: table and kv_len must be 4-byte aligned");
@@ -308,7 +317,7 @@ int vq3_prompt_attention(const vq3_attn* attn, const vq3_kv_rows* rows, void* wo
   if (int rc = check_attn(&at, r.kv_heads, r.head_dim, "prompt_attention", &done)) return rc;
   if (r.tokens != at.tokens)
     return report_error(VQ3_EINVAL, "prompt_attention: %d rows of k and v for %d of q", r.tokens, at.tokens);
-  if (done) return report_ok();
+  if (done) return nothing(workspace, ws_bytes, stream, "prompt_attention");
   AttnArgs a{};
   a.k = r.k;
   a.v = r.v;

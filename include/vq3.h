@@ -407,8 +407,10 @@ VQ3_API int vq3_kv_append(const vq3_kv_rows* rows, const long long* slots, const
 
 /*
  * Workspace of the two attention calls (bytes; 0 for unsupported sizes). It needs no
- * initialisation. Calls that share one must not overlap on the GPU. Its first 32-bit
- * word is 0 after a call, or 3 if a wait inside a kernel gave up (about a second), the
+ * initialisation. Calls that share one must not overlap on the GPU, and it is not one of
+ * the MLP and linear calls, whose counters these calls overwrite (vq3_workspace_init makes
+ * it theirs again). Its first 32-bit word is 0 after a call (one without rows or requests,
+ * too, where a workspace is given), or 3 if a wait inside a kernel gave up (about a second), the
  * call's outputs being invalid then: vq3_workspace_status reads it.
  */
 VQ3_API size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_dim, int max_new);

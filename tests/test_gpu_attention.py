@@ -489,6 +489,20 @@ def test_empty_calls(vq3):
     vq3.kv_append(q[:0, :2], q[:0, 2:], torch.empty(0, dtype=torch.int64, device=DEV), pages, pages.clone())
 
 
+def test_status_word_of_empty_calls(vq3):
+    # a workspace that held something else: 0 after a call with nothing to do, as after any other
+    pages = torch.zeros(2, 16, 2, 64, dtype=torch.float16, device=DEV)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=DEV)
+    none, table = torch.empty(0, dtype=torch.int32, device=DEV), torch.empty(0, 4, dtype=torch.int32, device=DEV)
+    calls = [lambda ws: vq3.paged_attention(q, pages, pages, table, ints([0]), none, ws=ws),
+             lambda ws: vq3.prompt_attention(q, q[:, :2], q[:, 2:], ints([0]), ws=ws),
+             lambda ws: vq3.prompt_attention(q[:0], q[:0, :2], q[:0, 2:], ints([0, 0]), ws=ws)]
+    for call in calls:
+        ws = torch.full((vq3.attention_workspace_bytes(4, 2, 64),), 0xAB, dtype=torch.uint8, device=DEV)
+        call(ws)
+        assert vq3.workspace_status(ws) == 0
+
+
 def test_plan_most_requests(vq3):
     R = 8192
     rng = np.random.default_rng(7)
