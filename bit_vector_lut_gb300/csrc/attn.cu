@@ -18,7 +18,7 @@
 // while this group's products run. 64 requests decoding at up to 16K keys of 8 x 128 (1.23 GB):
 // 185-193 us, 6.4-6.6 TB/s, 94-98% of a plain copy's rate. A single request of 4,097 keys of
 // 4 x 256 takes 14.5 us (2.5 us at that rate): finding the range, the first keys from
-// memory, joining the 130 CTAs' parts.
+// memory, joining the 132 CTAs' parts.
 #include "attn_common.cuh"
 
 namespace vq3 {
