@@ -7,7 +7,6 @@
 namespace vq3 {
 namespace {
 
-constexpr int kMaxRequests = 8192;
 constexpr int kMaxKeys = 1 << 30;  // of one request
 constexpr int kMaxKvHeads = 1 << 16;
 constexpr float kLog2e = 1.4426950408889634f;

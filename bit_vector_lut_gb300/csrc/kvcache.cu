@@ -189,9 +189,13 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const __grid_con
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
-  const int smem = 2 * (a.requests + 1) * (int)sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // Without opting in a launch gets 48 KB, static shared memory counted in. The opt-in is the same for every
+  // call: one of a call's own size could be lowered by another host thread before the launch.
+  const auto bytes = [](int requests) { return 2 * (requests + 1) * (int)sizeof(int); };
+  const int smem = bytes(a.requests);
+  if (smem > 32 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxRequests));
     if (e != cudaSuccess) return e;
   }
   const int want = (a.max_tokens + kPlanTokens - 1) / kPlanTokens, cap = device_sm_count();

@@ -292,6 +292,7 @@ cudaError_t launch_lowrank(const uint16_t* xr, int rows, int d_in, const uint16_
 
 // Page plan of a serving step and append of new rows to the paged cache (layouts as
 // vq3_paged_plan and vq3_kv_append; strides in elements).
+constexpr int kMaxRequests = 8192;  // of a plan or an attention call
 struct PlanArgs {
   const int* cached;
   const int* fresh;
