@@ -8,6 +8,7 @@ module fails loudly when the library has not been built: there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint8, c_void_p
@@ -494,6 +495,8 @@ def _want(ok: bool, msg: str) -> None:
 
 
 # The calls below take a few microseconds on the GPU in a decode step: what Python does per call is kept short.
+# `stream`: where a call runs, the current stream by default. The caller orders it behind the inputs' writers and the
+# outputs' readers behind it.
 _INT, _LONG, _FLOAT = torch.int32, torch.int64, torch.float32
 _empty = torch.empty
 
@@ -515,10 +518,23 @@ def _launch(index: int, stream, call, *args) -> None:
         raise Vq3Error(rc, lib.vq3_last_error().decode())
 
 
-def _kept(stream, *tensors) -> None:
-    """Tensors made here and used on a stream of the caller's: their memory is not reused before that use."""
-    for t in tensors:
-        t.record_stream(stream)
+_HERE = contextlib.nullcontext()
+
+
+def _pool(stream):
+    """Context in which a call's buffers are made: they come from the pool of the stream that writes them. (A block
+    that was just freed on another stream may still be read or written by what is queued there.)"""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+def _handed_out(index: int, stream, *tensors) -> None:
+    """Tensors made on a stream of the caller's and returned: their memory is not given out again on that stream
+    before what the current one, on which the caller goes on, does with them."""
+    if stream is not None:
+        here = torch.cuda.current_stream(index)
+        if here != stream:
+            for t in tensors:
+                t.record_stream(here)
 
 
 def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, ring: torch.Tensor,
@@ -537,11 +553,12 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, r
                            "cached and fresh with one entry per table row, ring_state with two")
     if out is None:
         device, size = table.device, max(int(max_tokens), 0)
-        out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device), _empty(requests, dtype=_INT, device=device),
-                        _empty(size, dtype=_LONG, device=device), _empty(size, dtype=_INT, device=device),
-                        _empty(2, dtype=_INT, device=device), _empty(1, dtype=_INT, device=device))
-        if stream is not None:
-            _kept(stream, *out)
+        with _pool(stream):
+            out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device),
+                            _empty(requests, dtype=_INT, device=device), _empty(size, dtype=_LONG, device=device),
+                            _empty(size, dtype=_INT, device=device), _empty(2, dtype=_INT, device=device),
+                            _empty(1, dtype=_INT, device=device))
+        _handed_out(index, stream, *out)
     else:
         _want(_ints_ok(index, out.q_start) and _ints_ok(index, out.kv_len) and _ints_ok(index, out.positions) and
               _ints_ok(index, out.ring_state) and _ints_ok(index, out.status) and out.slots.dtype is _LONG and
@@ -607,10 +624,10 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
     tokens, heads, head_dim = shape
     if not _ints_ok(index, q_start) or q_start.numel() < 1:
         raise Vq3Error(-1, "q_start must be a contiguous int32 tensor [requests + 1] on q's device")
-    made = []
     if out is None:
-        out = _empty(shape, dtype=dtype, device=q.device)
-        made.append(out)
+        with _pool(stream):
+            out = _empty(shape, dtype=dtype, device=q.device)
+        _handed_out(index, stream, out)
     elif out.shape != shape or out.dtype is not dtype or out.get_device() != index:
         raise Vq3Error(-1, "out must be like q")
     if lse is not None and (lse.shape != shape[:2] or lse.dtype is not _FLOAT or not lse.is_contiguous()
@@ -622,11 +639,9 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
         raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
     if ws is None:
         # 256 bytes at least, for the status word
-        ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
-                    dtype=torch.uint8, device=q.device)
-        made.append(ws)
-    if stream is not None:
-        _kept(stream, *made)
+        size = max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256)
+        with _pool(stream):
+            ws = _empty(size, dtype=torch.uint8, device=q.device)
     a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
                  head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
                  None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)

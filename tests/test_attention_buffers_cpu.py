@@ -1,0 +1,147 @@
+"""Where the binding of the attention calls makes its buffers and what it asks of the library, with stand-ins for
+tensors, streams, devices and the library (no GPU)."""
+
+import contextlib
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+vq3 = pytest.importorskip("bit_vector_lut_gb300.vq3", reason="libvq3.so not built")
+
+DEVICE = 1  # of the tensors; device 0 is the current one unless a test says otherwise
+BYTES = {0: 1 << 20, 1: 3 << 20}  # workspace that a call needs on either device
+
+
+class Tensor:
+    def __init__(self, shape, dtype, strides=None, device=DEVICE, contiguous=True):
+        self.shape, self.dtype, self.index, self.contiguous = torch.Size(shape), dtype, device, contiguous
+        self.strides = strides or torch.empty(shape, device="meta").stride()
+        self.device = f"cuda:{device}"
+        self.recorded = []
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return self.strides
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return 0x10000
+
+    def record_stream(self, s):
+        self.recorded.append(s)
+
+
+class Stream:
+    def __init__(self, name, device=DEVICE):
+        self.name, self.device_index, self.cuda_stream = name, device, 77
+
+
+class World:
+    """The current device and stream, the buffers made and the library's calls, in order."""
+
+    def __init__(self, monkeypatch):
+        self.device, self.main = 0, Stream("main")
+        self.stream, self.made, self.calls = self.main, [], []
+        self.answers = []  # statuses of the next calls, 0 when they run out
+
+        @contextlib.contextmanager
+        def on_stream(s):
+            was = self.stream, self.device
+            self.stream, self.device = s, s.device_index
+            yield
+            self.stream, self.device = was
+
+        @contextlib.contextmanager
+        def on_device(i):
+            was, self.device = self.device, i
+            yield
+            self.device = was
+
+        def empty(*shape, dtype, device):
+            t = Tensor(shape[0] if isinstance(shape[0], (tuple, torch.Size)) else shape, dtype)
+            self.made.append((t, self.stream))
+            return t
+
+        def call(name):
+            def f(*args):
+                self.calls.append((name, self.device, self.stream, args))
+                return self.answers.pop(0) if self.answers else 0
+            return f
+
+        monkeypatch.setattr(torch.cuda, "stream", on_stream)
+        monkeypatch.setattr(torch.cuda, "device", on_device)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: self.stream)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.device, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 5, raising=False)
+        monkeypatch.setattr(vq3, "_empty", empty)
+        monkeypatch.setattr(vq3, "lib", types.SimpleNamespace(
+            vq3_paged_plan=call("plan"), vq3_paged_attention=call("paged"), vq3_prompt_attention=call("prompt"),
+            vq3_kv_append=call("append"), vq3_last_error=lambda: b"refused",
+            vq3_attention_workspace_bytes=lambda *a: BYTES[self.device]))
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+def ints(*shape):
+    return Tensor(shape, torch.int32)
+
+
+def half(*shape):
+    return Tensor(shape, torch.float16)
+
+
+def run_plan(**kw):
+    return tuple(vq3.paged_plan(ints(3), ints(3), ints(3, 5), ints(9), ints(2), 16, 20, **kw))
+
+
+def run_paged(**kw):
+    return (vq3.paged_attention(half(7, 8, 128), half(9, 16, 2, 128), half(9, 16, 2, 128), ints(3, 5), ints(4), ints(3),
+                                max_new=4, **kw),)
+
+
+def run_prompt(**kw):
+    return (vq3.prompt_attention(half(7, 8, 128), half(7, 2, 128), half(7, 2, 128), ints(4), max_new=4, **kw),)
+
+
+CALLS = [run_plan, run_paged, run_prompt]
+
+
+@pytest.mark.parametrize("run", CALLS)
+def test_buffers_come_from_the_stream_that_writes_them(world, run):
+    side = Stream("side")
+    got = run(stream=side)
+    assert world.made and all(s is side for _, s in world.made)
+    assert world.calls[-1][3][-1] == side.cuda_stream
+    # what is handed back is used on the current stream: not given out again before that
+    assert all(t.recorded == [world.main] for t in got)
+    assert world.stream is world.main and world.device == 0
+
+
+@pytest.mark.parametrize("run", CALLS)
+def test_without_a_stream_the_current_one_is_used(world, run):
+    got = run()
+    assert world.made and all(s is world.main for _, s in world.made)
+    assert world.calls[-1][3][-1] == 5 and not any(t.recorded for t in got)
+
+
+@pytest.mark.parametrize("run", CALLS)
+def test_the_current_stream_given_by_name(world, run):
+    got = run(stream=world.main)
+    assert all(s is world.main for _, s in world.made) and not any(t.recorded for t in got)
