@@ -505,26 +505,28 @@ def _ints_ok(index: int, t: torch.Tensor) -> bool:
     return t.dtype is _INT and t.is_contiguous() and t.get_device() == index
 
 
-def _launch(index: int, stream, call, *args) -> None:
-    """call(*args, stream) with CUDA device `index` current; the stream is the caller's or the device's current one."""
-    if index < 0:
-        raise Vq3Error(-1, "tensors must be on a CUDA device")
-    if index == torch._C._cuda_getDevice():
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(index):
-            rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-    if rc != VQ3_OK:
-        raise Vq3Error(rc, lib.vq3_last_error().decode())
-
-
 _HERE = contextlib.nullcontext()
 
 
-def _pool(stream):
-    """Context in which a call's buffers are made: they come from the pool of the stream that writes them. (A block
-    that was just freed on another stream may still be read or written by what is queued there.)"""
-    return _HERE if stream is None else torch.cuda.stream(stream)
+def _at(index: int, stream):
+    """Context in which a call makes its buffers and launches: CUDA device `index`, the tensors', is current (what the
+    library answers about sizes is about it), and so is the caller's stream, if there is one: the buffers come from the
+    pool of the stream that writes them. (A block that was just freed on another stream may still be read or written by
+    what is queued there.)"""
+    if index < 0:
+        raise Vq3Error(-1, "tensors must be on a CUDA device")
+    if stream is not None:
+        if stream.device_index != index:
+            raise Vq3Error(-1, f"stream of CUDA device {stream.device_index}, tensors on {index}")
+        return torch.cuda.stream(stream)
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
+def _launch(index: int, stream, call, *args) -> None:
+    """call(*args, stream) inside _at(index, stream)."""
+    rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if rc != VQ3_OK:
+        raise Vq3Error(rc, lib.vq3_last_error().decode())
 
 
 def _handed_out(index: int, stream, *tensors) -> None:
@@ -551,25 +553,27 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, r
             and ring_state.numel() == 2):
         raise Vq3Error(-1, "table, cached, fresh, ring and ring_state must be contiguous int32 tensors on one device, "
                            "cached and fresh with one entry per table row, ring_state with two")
-    if out is None:
-        device, size = table.device, max(int(max_tokens), 0)
-        with _pool(stream):
-            out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device),
-                            _empty(requests, dtype=_INT, device=device), _empty(size, dtype=_LONG, device=device),
-                            _empty(size, dtype=_INT, device=device), _empty(2, dtype=_INT, device=device),
-                            _empty(1, dtype=_INT, device=device))
-        _handed_out(index, stream, *out)
-    else:
+    made = out is None
+    if not made:
         _want(_ints_ok(index, out.q_start) and _ints_ok(index, out.kv_len) and _ints_ok(index, out.positions) and
               _ints_ok(index, out.ring_state) and _ints_ok(index, out.status) and out.slots.dtype is _LONG and
               out.slots.is_contiguous() and out.slots.get_device() == index and
               out.q_start.numel() == requests + 1 and out.kv_len.numel() == requests and
               out.positions.numel() == max_tokens and out.slots.numel() == max_tokens and
               out.ring_state.numel() == 2 and out.status.numel() == 1, "out is a plan of other sizes")
-    _launch(index, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
-            ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
-            out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
-            out.ring_state.data_ptr(), out.status.data_ptr())
+    with _at(index, stream):
+        if made:
+            device, size = table.device, max(int(max_tokens), 0)
+            out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device),
+                            _empty(requests, dtype=_INT, device=device), _empty(size, dtype=_LONG, device=device),
+                            _empty(size, dtype=_INT, device=device), _empty(2, dtype=_INT, device=device),
+                            _empty(1, dtype=_INT, device=device))
+        _launch(index, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
+                ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
+                out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+                out.ring_state.data_ptr(), out.status.data_ptr())
+    if made:
+        _handed_out(index, stream, *out)
     return out
 
 
@@ -609,11 +613,12 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: to
     if slots.dtype is not _LONG or not slots.is_contiguous() or slots.numel() < rows.tokens or \
             slots.get_device() != index:
         raise Vq3Error(-1, "slots must be a contiguous int64 tensor with an entry per row")
-    _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
+    with _at(index, stream):
+        _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
 
 
 def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new: int = 0) -> int:
-    """Workspace of paged_attention and prompt_attention; it needs no initialisation."""
+    """Workspace of paged_attention and prompt_attention on the current device; it needs no initialisation."""
     return int(lib.vq3_attention_workspace_bytes(heads, kv_heads, head_dim, max_new))
 
 
@@ -624,28 +629,29 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
     tokens, heads, head_dim = shape
     if not _ints_ok(index, q_start) or q_start.numel() < 1:
         raise Vq3Error(-1, "q_start must be a contiguous int32 tensor [requests + 1] on q's device")
-    if out is None:
-        with _pool(stream):
-            out = _empty(shape, dtype=dtype, device=q.device)
-        _handed_out(index, stream, out)
-    elif out.shape != shape or out.dtype is not dtype or out.get_device() != index:
+    made = out is None
+    if not made and (out.shape != shape or out.dtype is not dtype or out.get_device() != index):
         raise Vq3Error(-1, "out must be like q")
     if lse is not None and (lse.shape != shape[:2] or lse.dtype is not _FLOAT or not lse.is_contiguous()
                             or lse.get_device() != index):
         raise Vq3Error(-1, "lse must be a contiguous float32 tensor [tokens, heads]")
-    qt, qh, qd = q.stride()
-    ot, oh, od = out.stride()
-    if qd != 1 or od != 1:
-        raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
-    if ws is None:
-        # 256 bytes at least, for the status word
-        size = max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256)
-        with _pool(stream):
-            ws = _empty(size, dtype=torch.uint8, device=q.device)
-    a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
-                 head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
-                 None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
-    _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+    with _at(index, stream):
+        if made:
+            out = _empty(shape, dtype=dtype, device=q.device)
+        qt, qh, qd = q.stride()
+        ot, oh, od = out.stride()
+        if qd != 1 or od != 1:
+            raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
+        if ws is None:
+            # 256 bytes at least, for the status word
+            ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
+                        dtype=torch.uint8, device=q.device)
+        a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
+                     head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
+                     None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
+        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+    if made:
+        _handed_out(index, stream, out)
     return out
 
 

@@ -145,3 +145,26 @@ def test_without_a_stream_the_current_one_is_used(world, run):
 def test_the_current_stream_given_by_name(world, run):
     got = run(stream=world.main)
     assert all(s is world.main for _, s in world.made) and not any(t.recorded for t in got)
+
+
+@pytest.mark.parametrize("run", [run_paged, run_prompt])
+@pytest.mark.parametrize("current", [0, 1])
+def test_workspace_is_sized_on_the_tensors_device(world, run, current):
+    # the devices need not have the same number of SMs, on which the size depends
+    world.device = current
+    run()
+    name, device, _, args = world.calls[-1]
+    assert device == DEVICE and args[-2] == BYTES[DEVICE] and world.device == current
+
+
+def test_every_call_runs_on_the_tensors_device(world):
+    run_plan()
+    vq3.kv_append(half(7, 2, 128), half(7, 2, 128), Tensor((7,), torch.int64), half(9, 16, 2, 128), half(9, 16, 2, 128))
+    assert [(c[0], c[1]) for c in world.calls] == [("plan", DEVICE), ("append", DEVICE)] and world.device == 0
+
+
+@pytest.mark.parametrize("run", CALLS)
+def test_a_stream_of_another_device_is_refused(world, run):
+    with pytest.raises(vq3.Vq3Error, match="stream of CUDA device 0"):
+        run(stream=Stream("other", device=0))
+    assert not world.calls and not world.made
