@@ -646,10 +646,13 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
             # 256 bytes at least, for the status word
             ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
                         dtype=torch.uint8, device=q.device)
+        elif ws.get_device() != index or not ws.is_contiguous():
+            raise Vq3Error(-1, "ws must be a contiguous tensor on q's device")
         a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
                      head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
                      None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
-        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(),
+                ws.numel() * ws.element_size())
     if made:
         _handed_out(index, stream, out)
     return out

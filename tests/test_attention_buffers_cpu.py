@@ -168,3 +168,16 @@ def test_a_stream_of_another_device_is_refused(world, run):
     with pytest.raises(vq3.Vq3Error, match="stream of CUDA device 0"):
         run(stream=Stream("other", device=0))
     assert not world.calls and not world.made
+
+
+@pytest.mark.parametrize("run", [run_paged, run_prompt])
+def test_a_workspace_that_the_call_cannot_write_is_refused(world, run):
+    for ws in (Tensor((1 << 22,), torch.uint8, device=0),      # another device's
+               Tensor((1 << 22,), torch.uint8, device=-1),     # host memory
+               Tensor((1 << 22,), torch.uint8, strides=(0,), contiguous=False)):  # one byte, expanded
+        with pytest.raises(vq3.Vq3Error, match="ws must be"):
+            run(ws=ws)
+    assert not world.calls
+    # its size in bytes, whatever its type
+    run(ws=Tensor((1 << 20,), torch.float32))
+    assert world.calls[-1][3][-2] == 4 << 20
