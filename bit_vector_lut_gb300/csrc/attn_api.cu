@@ -104,6 +104,18 @@ Choice choose(int head_dim, int group, int rows) {
   return c;
 }
 
+// Rows of a block that are used where it holds whole tokens.
+int token_rows(int head_dim, int group, const Choice& c) {
+  if (!c.wide) return c.slot_rows;
+  return c.slot_rows / attn_wide_blocks(head_dim) / group * group;
+}
+// Whether the kernel's 32-bit count of tiles (64 or 128 keys) holds the batch, every request at max_kv keys.
+bool counts(const vq3_attn* at, int kv_heads, int head_dim, const Choice& c, int max_kv) {
+  const int group = at->heads / kv_heads, blocks = c.wide ? attn_wide_blocks(head_dim) : 1;
+  const double units = (double)at->tokens * group / (blocks * token_rows(head_dim, group, c)) + at->requests;
+  return units * kv_heads * (max_kv / (c.wide ? 128.0 : 64.0) + 8) <= 4e9;
+}
+
 struct Ws {
   size_t rec, ml, part, total;
 };
@@ -121,11 +133,19 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
         const char* who) {
   const int group = at->heads / kv_heads;
   const long long rows = (long long)at->max_new * group;
-  const Choice c = choose(head_dim, group, rows > (1 << 20) ? 1 << 20 : (int)rows);
+  Choice c = choose(head_dim, group, rows > (1 << 20) ? 1 << 20 : (int)rows);
+  // max_new only picks the kernel: one that is too small for the batch must not get it refused
+  const bool other = !c.wide && !counts(at, kv_heads, head_dim, c, a.max_kv);
+  if (other) c = choose(head_dim, group, 0);
+  if (!counts(at, kv_heads, head_dim, c, a.max_kv))
+    return report_error(VQ3_EUNSUPPORTED, "%s: too many (row block, key tile) pairs: %d tokens, keys up to %d", who,
+                        at->tokens, a.max_kv);
   const Ws w = carve(head_dim, c);
   if (!workspace) return report_error(VQ3_EINVAL, "%s: null workspace", who);
   if (!on(workspace, 256)) return report_error(VQ3_EALIGN, "%s: workspace must be 256-byte aligned", who);
-  if (ws_bytes < w.total) return report_error(VQ3_ENOSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, w.total);
+  if (ws_bytes < w.total)
+    return report_error(VQ3_ENOSPACE, "%s: workspace %zu < %zu bytes%s", who, ws_bytes, w.total,
+                        other ? ", those of max_new 0, which this batch needs" : "");
   char* ws = static_cast<char*>(workspace);
   a.q = at->q;
   a.out = at->out;
@@ -143,15 +163,10 @@ int run(const vq3_attn* at, int kv_heads, int head_dim, AttnArgs& a, void* works
   a.unit_cost = c.wide ? attn_wide_unit_cost(head_dim) : attn_rows_unit_cost();
   a.unit_blocks = c.wide ? attn_wide_blocks(head_dim) : 1;
   a.block_rows = c.slot_rows / a.unit_blocks;
-  a.token_rows = c.wide ? a.block_rows / group * group : a.block_rows;
+  a.token_rows = token_rows(head_dim, group, c);
   a.by_group = FastDiv(group);
   a.by_unit = FastDiv(c.slot_rows);
   a.by_token_unit = FastDiv(a.unit_blocks * a.token_rows);
-  // the kernels count tiles of 64 or 128 keys in 32 bits
-  const double units = (double)at->tokens * group / (a.unit_blocks * a.token_rows) + at->requests;
-  if (units * kv_heads * (a.max_kv / (c.wide ? 128.0 : 64.0) + 8) > 4e9)
-    return report_error(VQ3_EUNSUPPORTED, "%s: too many (row block, key tile) pairs: %d tokens, keys up to %d", who,
-                        at->tokens, a.max_kv);
   a.scale_log2 = at->scale * kLog2e;
   a.status = reinterpret_cast<int*>(ws);
   a.rec = reinterpret_cast<AttnRec*>(ws + w.rec);

@@ -21,7 +21,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # VQ3_LIB may name another build of the same library (the bounds-check build, libvq3_bc.so)
 LIB_PATH = os.environ.get("VQ3_LIB") or os.path.join(_PKG, "libvq3.so")
 
-VQ3_OK = 0
+VQ3_OK, VQ3_ENOSPACE = 0, -5
 ERRORS = {-1: "VQ3_EINVAL", -2: "VQ3_EALIGN", -3: "VQ3_EUNSUPPORTED", -4: "VQ3_ECUDA", -5: "VQ3_ENOSPACE"}
 
 
@@ -642,7 +642,8 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
         ot, oh, od = out.stride()
         if qd != 1 or od != 1:
             raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
-        if ws is None:
+        own = ws is None
+        if own:
             # 256 bytes at least, for the status word
             ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
                         dtype=torch.uint8, device=q.device)
@@ -651,8 +652,16 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
         a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
                      head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
                      None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
-        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(),
-                ws.numel() * ws.element_size())
+        try:
+            _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(),
+                    ws.numel() * ws.element_size())
+        except Vq3Error as e:
+            if not own or e.code != VQ3_ENOSPACE:
+                raise
+            # max_new is too small for so large a batch: what the kernel for any batch needs
+            ws = _empty(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, 0), dtype=torch.uint8,
+                        device=q.device)
+            _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
     if made:
         _handed_out(index, stream, out)
     return out

@@ -354,7 +354,8 @@ typedef struct vq3_attn {
   int tokens;   /* rows of q, out and lse */
   int requests; /* at most 8192 */
   int max_new;  /* most new tokens of a request, 0 if unknown. Only picks the kernel: a wrong
-                   value costs time, not correctness */
+                   value costs time, not correctness (one far too small for a very large batch
+                   also needs the workspace of max_new 0, see vq3_paged_attention) */
   float scale;  /* of the scores, positive, at most 2e38 (1 / sqrt(head_dim) for instance) */
   const void* q;
   void* out;
@@ -428,9 +429,11 @@ VQ3_API size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_d
  * is not may make rows NaN that do not see it). kv_len is cut to max_pages pages; a
  * page number outside the cache reads as zeros.
  * table: device [requests][max_pages]; kv_len: device [requests]; max_pages *
- * page_size at most 2^30, tokens * heads below 2^30, and the batch's (row block, 64
- * keys) pairs below 4e9, counted with max_pages pages a request (a prompt of a million
- * tokens with 32 heads passes). out does not overlap an input.
+ * page_size at most 2^30, tokens * heads below 2^30, and the batch's (row block, key
+ * tile) pairs below 4e9, counted with max_pages pages a request (a prompt of a million
+ * tokens with 32 heads passes). A batch with too many pairs for the kernel that max_new
+ * picks, whose blocks are smaller, is run by the other one (groups of up to 128 heads),
+ * if ws_bytes is what max_new 0 needs (else VQ3_ENOSPACE). out does not overlap an input.
  * Deterministic; results do not depend on where the pages lie.
  * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ENOSPACE, VQ3_ECUDA.
  */
