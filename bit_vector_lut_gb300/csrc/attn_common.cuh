@@ -118,7 +118,10 @@ struct AttnRequest {
   int used;                  // rows of a block that are used
 };
 
-// Lengths from device memory, clamped so that no later index leaves its buffer.
+// Lengths from device memory, clamped so that no later index leaves its buffer. Starts that do not
+// ascend make requests overlap; each still lies inside q and out, but the batch's cost, which the
+// entry points bound for ascending ones, may then pass 2^32: a range is cut wrongly, its place is
+// still one inside some request (an offset found in a request is below that request's own cost).
 __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int r) {
   AttnRequest q;
   int s = a.q_start[r], e = a.q_start[r + 1];
@@ -392,7 +395,14 @@ __device__ __noinline__ AttnPos attn_locate_block(const AttnArgs& a, int kv_tile
         AttnPos pos{};
         attn_inside(a, __shfl_sync(0xffffffffu, r, src), __shfl_sync(0xffffffffu, cost, src),
                     s0 - __shfl_sync(0xffffffffu, before, src), kv_tile, min_tiles, cut, s1 - s0, lane, &pos);
-        if (lane == 0) *result = pos;
+        // one writer, also where starts that do not ascend let the sums pass 2^32 and two warps find a
+        // place: a mixture of two would be none (a found place has a cost of at least 1)
+        if (lane == 0 && atomicCAS(&result->cost, 0u, pos.cost) == 0u) {
+          result->r = pos.r;
+          result->h = pos.h;
+          result->j = pos.j;
+          result->at = pos.at;
+        }
         break;
       }
       before += cost;
