@@ -280,8 +280,8 @@ int vq3_kv_append(const vq3_kv_rows* rows, const long long* slots, const vq3_kv_
 }
 
 size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_dim, int max_new) {
-  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || kv_heads <= 0 || heads <= 0 || heads % kv_heads ||
-      max_new < 0)
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || kv_heads <= 0 || kv_heads > kMaxKvHeads ||
+      heads <= 0 || heads % kv_heads || max_new < 0)
     return 0;
   const int group = heads / kv_heads;
   const long long rows = (long long)max_new * group;

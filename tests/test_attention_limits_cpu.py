@@ -61,3 +61,9 @@ def test_binding_makes_the_larger_workspace(world, monkeypatch):  # noqa: F811
         with pytest.raises(vq3.Vq3Error):
             run_paged(**kw)
         assert len(world.calls) == n + 1
+
+
+@pytest.mark.parametrize("kv_heads", [(1 << 16) + 1, 1 << 20])
+def test_no_workspace_size_for_what_the_calls_refuse(kv_heads):
+    assert vq3.attention_workspace_bytes(1 << 16, 1 << 16, 64) > 0
+    assert vq3.attention_workspace_bytes(kv_heads, kv_heads, 64) == 0
