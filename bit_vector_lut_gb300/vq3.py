@@ -8,7 +8,6 @@ module fails loudly when the library has not been built: there is no fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint8, c_void_p
@@ -496,7 +495,7 @@ def _want(ok: bool, msg: str) -> None:
 
 # The calls below take a few microseconds on the GPU in a decode step: what Python does per call is kept short.
 # `stream`: where a call runs, the current stream by default. The caller orders it behind the inputs' writers and the
-# outputs' readers behind it.
+# outputs' readers behind it. Making it current costs some microseconds: done only where a call makes buffers.
 _INT, _LONG, _FLOAT = torch.int32, torch.int64, torch.float32
 _empty = torch.empty
 
@@ -505,26 +504,32 @@ def _ints_ok(index: int, t: torch.Tensor) -> bool:
     return t.dtype is _INT and t.is_contiguous() and t.get_device() == index
 
 
-_HERE = contextlib.nullcontext()
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call that makes buffers has to run in _at, with another device or stream current."""
+    return index < 0 or stream is not None or index != torch._C._cuda_getDevice()
 
 
 def _at(index: int, stream):
-    """Context in which a call makes its buffers and launches: CUDA device `index`, the tensors', is current (what the
-    library answers about sizes is about it), and so is the caller's stream, if there is one: the buffers come from the
-    pool of the stream that writes them. (A block that was just freed on another stream may still be read or written by
-    what is queued there.)"""
+    """Context in which such a call runs: CUDA device `index`, the tensors', is current (what the library answers about
+    sizes is about it), and so is the caller's stream, if there is one: the buffers come from the pool of the stream
+    that writes them. (A block that was just freed on another stream may still be read or written by what is queued
+    there.)"""
     if index < 0:
         raise Vq3Error(-1, "tensors must be on a CUDA device")
-    if stream is not None:
-        if stream.device_index != index:
-            raise Vq3Error(-1, f"stream of CUDA device {stream.device_index}, tensors on {index}")
-        return torch.cuda.stream(stream)
-    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device_index != index:
+        raise Vq3Error(-1, f"stream of CUDA device {stream.device_index}, tensors on {index}")
+    return torch.cuda.stream(stream)
 
 
 def _launch(index: int, stream, call, *args) -> None:
-    """call(*args, stream) inside _at(index, stream)."""
-    rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    """call(*args, stream) with CUDA device `index` current; the stream is the caller's or the device's current one."""
+    if index >= 0 and index == torch._C._cuda_getDevice() and (stream is None or stream.device_index == index):
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    else:
+        with _at(index, stream):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != VQ3_OK:
         raise Vq3Error(rc, lib.vq3_last_error().decode())
 
@@ -553,27 +558,27 @@ def paged_plan(cached: torch.Tensor, fresh: torch.Tensor, table: torch.Tensor, r
             and ring_state.numel() == 2):
         raise Vq3Error(-1, "table, cached, fresh, ring and ring_state must be contiguous int32 tensors on one device, "
                            "cached and fresh with one entry per table row, ring_state with two")
-    made = out is None
-    if not made:
+    if out is None:
+        if _elsewhere(index, stream):
+            with _at(index, stream):
+                out = paged_plan(cached, fresh, table, ring, ring_state, page_size, max_tokens)
+            _handed_out(index, stream, *out)
+            return out
+        device, size = table.device, max(int(max_tokens), 0)
+        out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device), _empty(requests, dtype=_INT, device=device),
+                        _empty(size, dtype=_LONG, device=device), _empty(size, dtype=_INT, device=device),
+                        _empty(2, dtype=_INT, device=device), _empty(1, dtype=_INT, device=device))
+    else:
         _want(_ints_ok(index, out.q_start) and _ints_ok(index, out.kv_len) and _ints_ok(index, out.positions) and
               _ints_ok(index, out.ring_state) and _ints_ok(index, out.status) and out.slots.dtype is _LONG and
               out.slots.is_contiguous() and out.slots.get_device() == index and
               out.q_start.numel() == requests + 1 and out.kv_len.numel() == requests and
               out.positions.numel() == max_tokens and out.slots.numel() == max_tokens and
               out.ring_state.numel() == 2 and out.status.numel() == 1, "out is a plan of other sizes")
-    with _at(index, stream):
-        if made:
-            device, size = table.device, max(int(max_tokens), 0)
-            out = PagedPlan(_empty(requests + 1, dtype=_INT, device=device),
-                            _empty(requests, dtype=_INT, device=device), _empty(size, dtype=_LONG, device=device),
-                            _empty(size, dtype=_INT, device=device), _empty(2, dtype=_INT, device=device),
-                            _empty(1, dtype=_INT, device=device))
-        _launch(index, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
-                ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
-                out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
-                out.ring_state.data_ptr(), out.status.data_ptr())
-    if made:
-        _handed_out(index, stream, *out)
+    _launch(index, stream, lib.vq3_paged_plan, cached.data_ptr(), fresh.data_ptr(), requests, page_size,
+            ring.data_ptr(), ring.numel(), ring_state.data_ptr(), table.data_ptr(), max_pages, max_tokens,
+            out.q_start.data_ptr(), out.kv_len.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+            out.ring_state.data_ptr(), out.status.data_ptr())
     return out
 
 
@@ -613,8 +618,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: to
     if slots.dtype is not _LONG or not slots.is_contiguous() or slots.numel() < rows.tokens or \
             slots.get_device() != index:
         raise Vq3Error(-1, "slots must be a contiguous int64 tensor with an entry per row")
-    with _at(index, stream):
-        _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
+    _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
 
 
 def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new: int = 0) -> int:
@@ -635,35 +639,37 @@ def _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws,
     if lse is not None and (lse.shape != shape[:2] or lse.dtype is not _FLOAT or not lse.is_contiguous()
                             or lse.get_device() != index):
         raise Vq3Error(-1, "lse must be a contiguous float32 tensor [tokens, heads]")
-    with _at(index, stream):
+    if (made or ws is None) and _elsewhere(index, stream):
+        with _at(index, stream):
+            out = _attention(call, q, kv, dtype, index, q_start, max_new, scale, out, lse, ws, None, *more)
         if made:
-            out = _empty(shape, dtype=dtype, device=q.device)
-        qt, qh, qd = q.stride()
-        ot, oh, od = out.stride()
-        if qd != 1 or od != 1:
-            raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
-        own = ws is None
-        if own:
-            # 256 bytes at least, for the status word
-            ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
-                        dtype=torch.uint8, device=q.device)
-        elif ws.get_device() != index or not ws.is_contiguous():
-            raise Vq3Error(-1, "ws must be a contiguous tensor on q's device")
-        a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
-                     head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
-                     None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
-        try:
-            _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(),
-                    ws.numel() * ws.element_size())
-        except Vq3Error as e:
-            if not own or e.code != VQ3_ENOSPACE:
-                raise
-            # max_new is too small for so large a batch: what the kernel for any batch needs
-            ws = _empty(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, 0), dtype=torch.uint8,
-                        device=q.device)
-            _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.numel())
+            _handed_out(index, stream, out)
+        return out
     if made:
-        _handed_out(index, stream, out)
+        out = _empty(shape, dtype=dtype, device=q.device)
+    qt, qh, qd = q.stride()
+    ot, oh, od = out.stride()
+    if qd != 1 or od != 1:
+        raise Vq3Error(-1, "the head_dim axis of q and out must be contiguous")
+    own = ws is None
+    if own:
+        # 256 bytes at least, for the status word
+        ws = _empty(max(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, max_new), 256),
+                    dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise Vq3Error(-1, "ws must be a contiguous tensor on q's device")
+    a = vq3_attn(TYPES[dtype], heads, tokens, q_start.numel() - 1, max_new,
+                 head_dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
+                 None if lse is None else lse.data_ptr(), q_start.data_ptr(), qt, qh, ot, oh)
+    try:
+        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.nbytes)
+    except Vq3Error as e:
+        if not own or e.code != VQ3_ENOSPACE:
+            raise
+        # max_new is too small for so large a batch: what the kernel for any batch needs
+        ws = _empty(lib.vq3_attention_workspace_bytes(heads, kv.kv_heads, head_dim, 0), dtype=torch.uint8,
+                    device=q.device)
+        _launch(index, stream, call, ctypes.byref(a), ctypes.byref(kv), *more, ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -673,8 +679,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     stream=None) -> torch.Tensor:
     """Causal attention of packed new tokens q [tokens, heads, head_dim] over the paged cache (vq3_paged_attention):
     `table` [requests, max_pages], `q_start` [requests + 1], `kv_len` [requests] int32 on the device, kv_len with the
-    new tokens counted in. max_new: most new tokens of a request, 0 if unknown (it only picks the kernel). scale:
-    1 / sqrt(head_dim) by default. `lse` [tokens, heads] FP32 is filled if given."""
+    new tokens counted in. max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it
+    where it is known: single tokens take up to twice as long with 0. scale: 1 / sqrt(head_dim) by default. `lse` [tokens, heads] FP32 is filled if given."""
     cache = _kv_cache(k_pages, v_pages)
     index = k_pages.get_device()
     if not (_ints_ok(index, table) and _ints_ok(index, kv_len) and table.dim() == 2

@@ -29,8 +29,9 @@ class Tensor:
     def numel(self):
         return self.shape.numel()
 
-    def element_size(self):
-        return self.dtype.itemsize
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
 
     def is_contiguous(self):
         return self.contiguous
@@ -46,15 +47,15 @@ class Tensor:
 
 
 class Stream:
-    def __init__(self, name, device=DEVICE):
-        self.name, self.device_index, self.cuda_stream = name, device, 77
+    def __init__(self, name, device=DEVICE, handle=77):
+        self.name, self.device_index, self.cuda_stream = name, device, handle
 
 
 class World:
     """The current device and stream, the buffers made and the library's calls, in order."""
 
     def __init__(self, monkeypatch):
-        self.device, self.main = 0, Stream("main")
+        self.device, self.main = 0, Stream("main", handle=5)
         self.stream, self.made, self.calls = self.main, [], []
         self.answers = []  # statuses of the next calls, 0 when they run out
 
@@ -86,7 +87,7 @@ class World:
         monkeypatch.setattr(torch.cuda, "device", on_device)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: self.stream)
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.device, raising=False)
-        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 5, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: self.stream.cuda_stream, raising=False)
         monkeypatch.setattr(vq3, "_empty", empty)
         monkeypatch.setattr(vq3, "lib", types.SimpleNamespace(
             vq3_paged_plan=call("plan"), vq3_paged_attention=call("paged"), vq3_prompt_attention=call("prompt"),
@@ -155,6 +156,22 @@ def test_workspace_is_sized_on_the_tensors_device(world, run, current):
     run()
     name, device, _, args = world.calls[-1]
     assert device == DEVICE and args[-2] == BYTES[DEVICE] and world.device == current
+
+
+@pytest.mark.parametrize("run", [run_paged, run_prompt])
+def test_buffers_of_the_callers_on_a_stream_of_the_callers(world, run):
+    # nothing is made: only the call goes to that stream and device
+    side, out, ws = Stream("side"), half(7, 8, 128), Tensor((1 << 22,), torch.uint8)
+    assert run(out=out, ws=ws, stream=side)[0] is out and not world.made and not out.recorded
+    name, device, stream, args = world.calls[-1]
+    assert device == DEVICE and args[-1] == side.cuda_stream and world.stream is world.main
+    world.device = DEVICE
+    run(out=out, ws=ws, stream=side)
+    assert world.calls[-1][2] is world.main and world.calls[-1][3][-1] == side.cuda_stream
+    run(out=out, stream=side)  # a workspace is made
+    assert [s for _, s in world.made] == [side] and not out.recorded
+    with pytest.raises(vq3.Vq3Error, match="stream of CUDA device 0"):
+        run(out=out, ws=ws, stream=Stream("other", device=0))
 
 
 def test_every_call_runs_on_the_tensors_device(world):
