@@ -176,8 +176,12 @@ struct AttnPos {
 // units of a request share its keys (several row blocks) and units are few, every unit gets
 // CTAs of its own instead, in proportion to its tiles, and its tiles are cut evenly among
 // them: units of equal length are then walked in step and all but the first read find the
-// keys in L2. (64 tokens of 24 heads behind 98,304 keys of 4 x 256, 12 units: 142 us, with the
-// plain cut 203.)
+// keys in L2. Taken up to half as many units as CTAs. Behind 98,304 keys of 4 x 256, 24 heads, CTAs
+// of their own / the plain cut: 12 units (64 tokens) 141 / 203 us, 24 units 244 / 268, 52 units 673
+// / 738, 64 units 679 / 789. The shares are whole CTAs, rounded down, which costs most at the border:
+// 76 units (384 tokens) get one or two each, 1,323 us against 721. Above it both are far from their
+// operations, 100 units (512 tokens) 1,299 / 1,425 (666). 32 heads on 8 x 128: 8 units 103 to 134 /
+// 141, 32 units 385 / 348.
 struct AttnCut {
   unsigned cost;  // of the batch
   int units;      // of the batch; 0: the plain cut
@@ -281,7 +285,9 @@ __device__ __forceinline__ void attn_inside(const AttnArgs& a, int r, unsigned c
   }
 }
 
-// Few requests: every warp finds the CTA's range by itself, without a barrier.
+// Few requests: every warp finds the CTA's range by itself, without a barrier. (Single tokens of 32
+// heads on 8 x 128, up to 600 keys, each warp / the warps together: 48 requests 19.4 / 20.1 us, 100
+// and 120 no difference, 200 49.5 / 48.3, 800 168.7 / 159.6.)
 constexpr int kWarpRequests = 128;
 __device__ __forceinline__ AttnPos attn_locate_warp(const AttnArgs& a, int kv_tile, int min_tiles) {
   const int lane = threadIdx.x & 31, per = (a.requests + 31) / 32;

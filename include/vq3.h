@@ -421,7 +421,8 @@ VQ3_API size_t vq3_attention_workspace_bytes(int heads, int kv_heads, int head_d
  * tokens, verify steps, prefill chunks, mixed in one batch. Row i of request r (of
  * n = q_start[r + 1] - q_start[r]) sees the keys j < kv_len[r] - n + i + 1:
  *   out = sum_j softmax_j(scale q . k_j) v_j
- * with scores, softmax statistics and sums in FP32, the probabilities rounded once to
+ * with scores, softmax statistics and sums in FP32 (a score beyond its range has no
+ * defined answer), the probabilities rounded once to
  * the type of v (as the operand of the second product) and out rounded once. A row
  * that sees no key (kv_len < n) gets zeros and lse = -infinity. Keys and values behind
  * kv_len are never used, whatever the pages hold there, and keys that a row does not
