@@ -680,7 +680,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     """Causal attention of packed new tokens q [tokens, heads, head_dim] over the paged cache (vq3_paged_attention):
     `table` [requests, max_pages], `q_start` [requests + 1], `kv_len` [requests] int32 on the device, kv_len with the
     new tokens counted in. max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it
-    where it is known: single tokens take up to twice as long with 0. scale: 1 / sqrt(head_dim) by default. `lse` [tokens, heads] FP32 is filled if given."""
+    where it is known: single tokens take up to twice as long with 0. scale: 1 / sqrt(head_dim) by default. `lse`
+    [tokens, heads] FP32 is filled if given."""
     cache = _kv_cache(k_pages, v_pages)
     index = k_pages.get_device()
     if not (_ints_ok(index, table) and _ints_ok(index, kv_len) and table.dim() == 2
