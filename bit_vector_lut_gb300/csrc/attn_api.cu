@@ -2,6 +2,7 @@
 // and the choice of kernel.
 #include <cmath>
 
+#include "api_checks.h"
 #include "attn_common.cuh"
 
 namespace vq3 {
@@ -10,14 +11,6 @@ namespace {
 constexpr int kMaxKeys = 1 << 30;  // of one request
 constexpr int kMaxKvHeads = 1 << 16;
 constexpr float kLog2e = 1.4426950408889634f;
-
-bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
-}
 
 // The append counts a row's 16-byte chunks (up to 32 a head) in 32 bits.
 int check_kv_heads(int n, const char* who) {
@@ -30,19 +23,6 @@ int check_head_dim(int d, const char* who) {
     return report_error(VQ3_EUNSUPPORTED, "%s: head_dim=%d must be 64, 128 or 256", who, d);
   return VQ3_OK;
 }
-// A stride in elements of an axis of `extent`: whole 16-byte steps, rows of `row` elements apart.
-// An axis of one element has no stride to speak of: `row` is used.
-int check_stride(long long* s, long long extent, long long row, const char* who, const char* what) {
-  if (extent <= 1) {
-    *s = row;
-    return VQ3_OK;
-  }
-  if (*s < row || *s >= (1LL << 38))
-    return report_error(VQ3_EINVAL, "%s: %s stride %lld must be at least %lld (and below 2^38)", who, what, *s, row);
-  if (*s % 8) return report_error(VQ3_EALIGN, "%s: %s stride %lld is not a multiple of 8 elements", who, what, *s);
-  return VQ3_OK;
-}
-
 int check_cache(vq3_kv_cache* c, const char* who) {
   if (int rc = check_kv_heads(c->kv_heads, who)) return rc;
   if (int rc = check_head_dim(c->head_dim, who)) return rc;
@@ -81,6 +61,13 @@ int check_rows(vq3_kv_rows* r, const char* who) {
   for (auto& x : ax)
     if (int rc = check_stride(x.s, x.extent, r->head_dim, who, x.what)) return rc;
   return VQ3_OK;
+}
+
+AppendArgs append_args(const vq3_kv_rows& r, const vq3_kv_cache& c, const long long* slots) {
+  return AppendArgs{static_cast<const uint16_t*>(r.k), static_cast<const uint16_t*>(r.v), static_cast<uint16_t*>(c.k),
+                    static_cast<uint16_t*>(c.v), slots, r.k_token, r.k_head, r.v_token, r.v_head, c.k_page, c.k_token,
+                    c.k_head, c.v_page, c.v_token, c.v_head, r.tokens, r.kv_heads, log2_of(r.head_dim / 8), c.n_pages,
+                    log2_of(c.page_size)};
 }
 
 // Which kernel a call runs, how many CTAs and how many rows a partial slot has.
@@ -217,8 +204,7 @@ int check_attn(vq3_attn* at, int kv_heads, int head_dim, const char* who, bool* 
   if (int rc = check_stride(&at->q_head, at->heads, head_dim, who, "q head")) return rc;
   if (int rc = check_stride(&at->out_token, at->tokens, head_dim, who, "out token")) return rc;
   if (int rc = check_stride(&at->out_head, at->heads, head_dim, who, "out head")) return rc;
-  if (at->tokens > 1 && at->heads > 1 && at->out_token < (at->heads - 1) * at->out_head + head_dim &&
-      at->out_head < (at->tokens - 1) * at->out_token + head_dim)
+  if (rows_overlap(at->tokens, at->out_token, at->heads, at->out_head, head_dim))
     return report_error(VQ3_EINVAL, "%s: the rows of out overlap", who);
   if (at->out == at->q) return report_error(VQ3_EINVAL, "%s: out must not alias q", who);
   return VQ3_OK;
@@ -270,12 +256,63 @@ int vq3_kv_append(const vq3_kv_rows* rows, const long long* slots, const vq3_kv_
   if (r.tokens == 0) return report_ok();
   if (!slots) return report_error(VQ3_EINVAL, "kv_append: null slots");
   if (!on(slots, 8)) return report_error(VQ3_EALIGN, "kv_append: slots must be 8-byte aligned");
-  AppendArgs a{static_cast<const uint16_t*>(r.k), static_cast<const uint16_t*>(r.v), static_cast<uint16_t*>(c.k),
-               static_cast<uint16_t*>(c.v), slots, r.k_token, r.k_head, r.v_token, r.v_head, c.k_page, c.k_token,
-               c.k_head, c.v_page, c.v_token, c.v_head, r.tokens, r.kv_heads, log2_of(r.head_dim / 8), c.n_pages,
-               log2_of(c.page_size)};
+  const AppendArgs a = append_args(r, c, slots);
   const cudaError_t e = launch_kv_append(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(VQ3_ECUDA, "kv_append: launch: %s", cudaGetErrorString(e));
+  return report_ok();
+}
+
+int vq3_kv_append_rotary(const vq3_rotary* rotary, const vq3_kv_rows* rows, const long long* slots,
+                         const vq3_kv_cache* cache, void* stream) {
+  const char* who = "kv_append_rotary";
+  if (!rotary || !rows || !cache) return report_error(VQ3_EINVAL, "%s: null descriptor", who);
+  vq3_rotary t = *rotary;
+  vq3_kv_rows r = *rows;
+  vq3_kv_cache c = *cache;
+  if (t.type != VQ3_TYPE_F16 && t.type != VQ3_TYPE_BF16)
+    return report_error(VQ3_EUNSUPPORTED, "%s: unknown type %d", who, t.type);
+  if (int rc = check_cache(&c, who)) return rc;
+  if (r.kv_heads != c.kv_heads || r.head_dim != c.head_dim)
+    return report_error(VQ3_EINVAL, "%s: rows of %d x %d into a cache of %d x %d", who, r.kv_heads, r.head_dim,
+                        c.kv_heads, c.head_dim);
+  if (int rc = check_rows(&r, who)) return rc;
+  if (t.heads < 0) return report_error(VQ3_EINVAL, "%s: heads=%d", who, t.heads);
+  if (t.heads > kMaxKvHeads) return report_error(VQ3_EUNSUPPORTED, "%s: heads=%d above %d", who, t.heads, kMaxKvHeads);
+  if (t.rotated <= 0 || t.rotated > r.head_dim || t.rotated % 16)
+    return report_error(VQ3_EUNSUPPORTED, "%s: rotated=%d must be a multiple of 16 in [16, head_dim=%d]", who, t.rotated,
+                        r.head_dim);
+  if (r.tokens == 0) return report_ok();
+  if (!slots || !t.positions || !t.freq) return report_error(VQ3_EINVAL, "%s: null slots, positions or freq", who);
+  if (!on(slots, 8)) return report_error(VQ3_EALIGN, "%s: slots must be 8-byte aligned", who);
+  if (!on(t.positions, 4) || !on(t.freq, 4))
+    return report_error(VQ3_EALIGN, "%s: positions and freq must be 4-byte aligned", who);
+  if (t.heads) {
+    if (!t.q || !t.q_out) return report_error(VQ3_EINVAL, "%s: null q or q_out", who);
+    if (!on(t.q, 16) || !on(t.q_out, 16)) return report_error(VQ3_EALIGN, "%s: q and q_out must be 16-byte aligned", who);
+    if (int rc = check_stride(&t.q_token, r.tokens, r.head_dim, who, "q token")) return rc;
+    if (int rc = check_stride(&t.q_head, t.heads, r.head_dim, who, "q head")) return rc;
+    if (int rc = check_stride(&t.out_token, r.tokens, r.head_dim, who, "q_out token")) return rc;
+    if (int rc = check_stride(&t.out_head, t.heads, r.head_dim, who, "q_out head")) return rc;
+    if (rows_overlap(r.tokens, t.out_token, t.heads, t.out_head, r.head_dim))
+      return report_error(VQ3_EINVAL, "%s: the rows of q_out overlap", who);
+    if (t.q == t.q_out && (t.q_token != t.out_token || t.q_head != t.out_head))
+      return report_error(VQ3_EINVAL, "%s: in place q and q_out have the same strides", who);
+  }
+  RotaryArgs a{};
+  a.kv = append_args(r, c, slots);
+  a.q = static_cast<const uint16_t*>(t.q);
+  a.q_out = static_cast<uint16_t*>(t.q_out);
+  a.positions = t.positions;
+  a.freq = t.freq;
+  a.q_token = t.q_token;
+  a.q_head = t.q_head;
+  a.o_token = t.out_token;
+  a.o_head = t.out_head;
+  a.heads = t.heads;
+  a.half = t.rotated / 2;
+  a.interleaved = t.interleaved != 0;
+  const cudaError_t e = launch_kv_append_rotary(a, t.type == VQ3_TYPE_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(VQ3_ECUDA, "%s: launch: %s", who, cudaGetErrorString(e));
   return report_ok();
 }
 

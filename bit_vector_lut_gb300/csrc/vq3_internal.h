@@ -130,6 +130,9 @@ cudaError_t bounds_read_prefill_wide(unsigned* host, bool reset);
 cudaError_t bounds_read_attn(unsigned* host, bool reset);
 cudaError_t bounds_read_attn_wide(unsigned* host, bool reset);
 cudaError_t bounds_read_kvcache(unsigned* host, bool reset);
+cudaError_t bounds_read_delta_batch(unsigned* host, bool reset);
+cudaError_t bounds_read_conv(unsigned* host, bool reset);
+cudaError_t bounds_read_rotary(unsigned* host, bool reset);
 #else
 #define VQ3_BOUNDS_RECORD(name)
 #define VQ3_IN(idx, n, site) ((void)(n), true)  // the extent is used only by the check
@@ -319,6 +322,52 @@ struct AppendArgs {
   int tokens, kv_heads, chunk_shift, n_pages, page_shift;  // chunk_shift: log2(head_dim / 8)
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
+
+// The delta rule over packed requests with states in slots, the short convolution in front of it and the
+// append of rotated rows (layouts as vq3_delta_rule_batch, vq3_short_conv, vq3_kv_append_rotary; strides in
+// elements). slot_in, slot_out: or null.
+struct DeltaArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  const float* alpha;
+  const float* beta;
+  float* states;
+  const int* q_start;
+  const int* slot_in;
+  const int* slot_out;
+  long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head, alpha_token, beta_token, state_slot;
+  int tokens, requests, slots, v_heads, group, d_k, d_v, max_new;
+  float scale;
+};
+constexpr int kDeltaStepTokens = 2;  // max_new up to which single tokens' kernel runs
+cudaError_t launch_delta_batch(const DeltaArgs& a, bool bf16, cudaStream_t st);
+struct ConvArgs {
+  const uint16_t* x;
+  const uint16_t* weight;
+  const uint16_t* bias;  // or null
+  uint16_t* states;
+  uint16_t* out;
+  const int* q_start;
+  const int* slot_in;
+  const int* slot_out;
+  long long x_token, o_token, state_slot, state_row;
+  int tokens, requests, slots, channels, unit_channels, head_chunks;  // head_chunks: 8-channel chunks of a head
+  int silu;
+  float eps;
+};
+cudaError_t launch_short_conv(const ConvArgs& a, int width, bool bf16, cudaStream_t st);
+struct RotaryArgs {
+  AppendArgs kv;
+  const uint16_t* q;  // or null
+  uint16_t* q_out;
+  const int* positions;
+  const float* freq;
+  long long q_token, q_head, o_token, o_head;
+  int heads, half, interleaved;  // half: rotated / 2
+};
+cudaError_t launch_kv_append_rotary(const RotaryArgs& a, bool bf16, cudaStream_t st);
 
 // vq3_mlp_forward with passes of at most `pass_cap` rows (8, 16 or 32), and its
 // workspace size; vq3_mlp_forward itself uses 32.

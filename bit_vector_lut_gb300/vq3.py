@@ -68,6 +68,33 @@ class vq3_attn(ctypes.Structure):
                 ("q_token", c_longlong), ("q_head", c_longlong), ("out_token", c_longlong), ("out_head", c_longlong)]
 
 
+class vq3_rotary(ctypes.Structure):
+    _fields_ = [("type", c_int), ("heads", c_int), ("rotated", c_int), ("interleaved", c_int), ("freq", c_void_p),
+                ("positions", c_void_p), ("q", c_void_p), ("q_out", c_void_p), ("q_token", c_longlong),
+                ("q_head", c_longlong), ("out_token", c_longlong), ("out_head", c_longlong)]
+
+
+class vq3_batch(ctypes.Structure):
+    _fields_ = [("tokens", c_int), ("requests", c_int), ("slots", c_int), ("q_start", c_void_p), ("slot_in", c_void_p),
+                ("slot_out", c_void_p)]
+
+
+class vq3_delta(ctypes.Structure):
+    _fields_ = [("type", c_int), ("qk_heads", c_int), ("v_heads", c_int), ("d_k", c_int), ("d_v", c_int),
+                ("max_new", c_int), ("scale", c_float), ("q", c_void_p), ("k", c_void_p), ("v", c_void_p),
+                ("out", c_void_p), ("beta", c_void_p), ("alpha", c_void_p), ("states", c_void_p),
+                ("q_token", c_longlong), ("q_head", c_longlong), ("k_token", c_longlong), ("k_head", c_longlong),
+                ("v_token", c_longlong), ("v_head", c_longlong), ("out_token", c_longlong), ("out_head", c_longlong),
+                ("beta_token", c_longlong), ("alpha_token", c_longlong), ("state_slot", c_longlong)]
+
+
+class vq3_conv(ctypes.Structure):
+    _fields_ = [("type", c_int), ("channels", c_int), ("width", c_int), ("silu", c_int), ("unit_heads", c_int),
+                ("head_dim", c_int), ("eps", c_float), ("x", c_void_p), ("weight", c_void_p), ("bias", c_void_p),
+                ("states", c_void_p), ("out", c_void_p), ("x_token", c_longlong), ("out_token", c_longlong),
+                ("state_slot", c_longlong), ("state_row", c_longlong)]
+
+
 # VQ3_TYPE_* in vq3.h
 TYPES = {torch.float16: 0, torch.bfloat16: 1}
 
@@ -116,6 +143,10 @@ def _load() -> ctypes.CDLL:
         "vq3_paged_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_cache), c_void_p, c_int, c_void_p, c_void_p,
                                         c_size_t, c_void_p]),
         "vq3_prompt_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_rows), c_void_p, c_size_t, c_void_p]),
+        "vq3_kv_append_rotary": (c_int, [POINTER(vq3_rotary), POINTER(vq3_kv_rows), c_void_p, POINTER(vq3_kv_cache),
+                                         c_void_p]),
+        "vq3_delta_rule_batch": (c_int, [POINTER(vq3_batch), POINTER(vq3_delta), c_void_p]),
+        "vq3_short_conv": (c_int, [POINTER(vq3_batch), POINTER(vq3_conv), c_void_p]),
         "vq3_last_error": (ctypes.c_char_p, []),
         "vq3_version": (ctypes.c_char_p, []),
         "vq3_bounds_check": (c_int, [POINTER(ctypes.c_uint), c_int, c_int]),
@@ -151,7 +182,8 @@ def version() -> str:
     return lib.vq3_version().decode()
 
 
-BOUNDS_FILES = ("decode", "lowrank", "delta", "rotate", "prefill", "prefill_wide", "attn", "attn_wide", "kvcache")
+BOUNDS_FILES = ("decode", "lowrank", "delta", "rotate", "prefill", "prefill_wide", "attn", "attn_wide", "kvcache",
+                "delta_batch", "conv", "rotary")
 
 
 def bounds_check(reset: bool = True) -> dict[str, tuple[int, int]]:
@@ -621,6 +653,51 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: to
     _launch(index, stream, lib.vq3_kv_append, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
 
 
+def kv_append_rotary(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                     slots: torch.Tensor, freq: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """kv_append with the position rotation on the way (vq3_kv_append_rotary): the first 2 * freq.numel() entries of
+    every head of q [tokens, heads, head_dim] and k are turned by `positions` [>= tokens] int32 times `freq` FP32
+    (radians a position), entries i and i + freq.numel() as a pair, or 2 i and 2 i + 1 if interleaved. Turned queries
+    go to `q_out` (q itself: in place) and are returned, keys and values to `slots` of the cache. Rows with a negative
+    position (plan.positions behind the last) are left as they were. q None: keys and values only."""
+    cache, rows = _kv_cache(k_pages, v_pages), _kv_rows(k, v)
+    index, dtype = k.get_device(), k.dtype
+    if dtype is not k_pages.dtype or k_pages.get_device() != index:
+        raise Vq3Error(-1, "rows and cache must have one type and device")
+    if slots.dtype is not _LONG or not slots.is_contiguous() or slots.numel() < rows.tokens or \
+            slots.get_device() != index or not _ints_ok(index, positions) or positions.numel() < rows.tokens:
+        raise Vq3Error(-1, "slots (int64) and positions (int32) must be contiguous with an entry per row")
+    if freq.dtype is not _FLOAT or not freq.is_contiguous() or freq.get_device() != index:
+        raise Vq3Error(-1, "freq must be a contiguous float32 tensor on the rows' device")
+    rot = vq3_rotary(TYPES[dtype], 0, 2 * freq.numel(), bool(interleaved), freq.data_ptr(), positions.data_ptr())
+    if q is None:
+        if q_out is not None:
+            raise Vq3Error(-1, "q_out without q")
+    else:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != rows.tokens or shape[2] != rows.head_dim or q.dtype is not dtype or \
+                q.get_device() != index:
+            raise Vq3Error(-1, f"q must be [{rows.tokens}, heads, {rows.head_dim}] of the keys' type and device")
+        if q_out is None:
+            if _elsewhere(index, stream):
+                with _at(index, stream):
+                    q_out = kv_append_rotary(q, k, v, positions, slots, freq, k_pages, v_pages, interleaved)
+                _handed_out(index, stream, q_out)
+                return q_out
+            q_out = _empty(shape, dtype=dtype, device=q.device)
+        elif q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != index:
+            raise Vq3Error(-1, "q_out must be like q")
+        rot.heads, rot.q, rot.q_out = shape[1], q.data_ptr(), q_out.data_ptr()
+        rot.q_token, rot.q_head, qd = q.stride()
+        rot.out_token, rot.out_head, od = q_out.stride()
+        if qd != 1 or od != 1:
+            raise Vq3Error(-1, "the head_dim axis of q and q_out must be contiguous")
+    _launch(index, stream, lib.vq3_kv_append_rotary, ctypes.byref(rot), ctypes.byref(rows), slots.data_ptr(),
+            ctypes.byref(cache))
+    return q_out
+
+
 def attention_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_new: int = 0) -> int:
     """Workspace of paged_attention and prompt_attention on the current device; it needs no initialisation."""
     return int(lib.vq3_attention_workspace_bytes(heads, kv_heads, head_dim, max_new))
@@ -699,3 +776,98 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
     kv_heads, head_dim], request r at rows q_start[r] .. q_start[r + 1] - 1 of all three."""
     return _attention(lib.vq3_prompt_attention, q, _kv_rows(k, v), k.dtype, k.get_device(), q_start, max_new, scale, out,
                       lse, ws, stream)
+
+
+# ---------------------------------------------------------------- the delta rule for packed requests
+
+def _batch(index: int, tokens: int, slots: int, q_start, slot_in, slot_out) -> vq3_batch:
+    if not _ints_ok(index, q_start) or q_start.numel() < 1:
+        raise Vq3Error(-1, "q_start must be a contiguous int32 tensor [requests + 1] on the inputs' device")
+    requests = q_start.numel() - 1
+    for s in (slot_in, slot_out):
+        if s is not None and not (_ints_ok(index, s) and s.numel() == requests):
+            raise Vq3Error(-1, "slot_in and slot_out must be contiguous int32 tensors [requests] on the inputs' device")
+    return vq3_batch(tokens, requests, slots, q_start.data_ptr(), _ptr(slot_in), _ptr(slot_out))
+
+
+def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, alpha: torch.Tensor,
+                     states: torch.Tensor, q_start: torch.Tensor, slot_in: torch.Tensor | None = None,
+                     slot_out: torch.Tensor | None = None, max_new: int = 0, scale: float = 1.0,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gated delta rule over packed requests (vq3_delta_rule_batch): q, k [tokens, qk_heads, d_k], v [tokens,
+    v_heads, d_v] FP16 or BF16 (slices of one buffer, for instance), beta, alpha [tokens, v_heads] FP32, `states`
+    [slots, v_heads, d_k, d_v] FP32. Request r has rows q_start[r] .. q_start[r + 1] - 1, goes on from slot
+    slot_in[r] (negative, or slot_in None: from zeros) and leaves its state in slot_out[r] (negative, or None: nowhere).
+    max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it where it is known."""
+    index, dtype = v.get_device(), v.dtype
+    qs, vs, ss = q.shape, v.shape, states.shape
+    if dtype not in TYPES or len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or q.dtype is not dtype or \
+            k.dtype is not dtype or q.get_device() != index or k.get_device() != index:
+        raise Vq3Error(-1, "q and k [tokens, qk_heads, d_k] and v [tokens, v_heads, d_v] must be FP16 or BF16 tensors of "
+                           "one type and device")
+    tokens, heads, d_v = vs
+    d_k = qs[2]
+    for g in (beta, alpha):
+        if g.shape != vs[:2] or g.dtype is not _FLOAT or g.get_device() != index or (heads > 1 and g.stride(1) != 1):
+            raise Vq3Error(-1, "beta and alpha must be float32 [tokens, v_heads], the heads side by side")
+    if states.dtype is not _FLOAT or len(ss) != 4 or ss[1:] != (heads, d_k, d_v) or states.get_device() != index or \
+            states.stride()[1:] != (d_k * d_v, d_v, 1):
+        raise Vq3Error(-1, "states must be float32 [slots, v_heads, d_k, d_v], contiguous within a slot")
+    batch = _batch(index, tokens, ss[0], q_start, slot_in, slot_out)
+    if out is None:
+        if _elsewhere(index, stream):
+            with _at(index, stream):
+                out = delta_rule_batch(q, k, v, beta, alpha, states, q_start, slot_in, slot_out, max_new, scale)
+            _handed_out(index, stream, out)
+            return out
+        out = _empty(vs, dtype=dtype, device=v.device)
+    elif out.shape != vs or out.dtype is not dtype or out.get_device() != index:
+        raise Vq3Error(-1, "out must be like v")
+    (qt, qh, qd), (kt, kh, kd), (vt, vh, vd), (ot, oh, od) = q.stride(), k.stride(), v.stride(), out.stride()
+    if qd != 1 or kd != 1 or vd != 1 or od != 1:
+        raise Vq3Error(-1, "the last axis of q, k, v and out must be contiguous")
+    d = vq3_delta(TYPES[dtype], qs[1], heads, d_k, d_v, max_new, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                  out.data_ptr(), beta.data_ptr(), alpha.data_ptr(), states.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh,
+                  beta.stride(0), alpha.stride(0), states.stride(0))
+    _launch(index, stream, lib.vq3_delta_rule_batch, ctypes.byref(batch), ctypes.byref(d))
+    return out
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, states: torch.Tensor, q_start: torch.Tensor,
+               slot_in: torch.Tensor | None = None, slot_out: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, silu: bool = True, unit_heads: int = 0, head_dim: int = 0,
+               eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The short causal convolution over packed requests (vq3_short_conv): x [tokens, channels], weight [channels,
+    width], bias [channels] or None, `states` [slots, width - 1, channels] (the last inputs), all of one type; slots as
+    in delta_rule_batch. The first unit_heads heads of head_dim channels come out with unit length."""
+    index, dtype, xs = x.get_device(), x.dtype, x.shape
+    if dtype not in TYPES or len(xs) != 2 or weight.dim() != 2 or weight.shape[0] != xs[1] or weight.dtype is not dtype \
+            or not weight.is_contiguous() or weight.get_device() != index:
+        raise Vq3Error(-1, "x [tokens, channels] and weight [channels, width] must be FP16 or BF16 tensors of one type and "
+                           "device, weight contiguous")
+    tokens, channels = xs
+    width = weight.shape[1]
+    if bias is not None and (bias.shape != (channels,) or bias.dtype is not dtype or not bias.is_contiguous()
+                             or bias.get_device() != index):
+        raise Vq3Error(-1, "bias must be a contiguous tensor [channels] of x's type and device")
+    if states.dim() != 3 or states.shape[1:] != (width - 1, channels) or states.dtype is not dtype or \
+            states.get_device() != index or states.stride(2) != 1:
+        raise Vq3Error(-1, "states must be [slots, width - 1, channels] of x's type and device")
+    batch = _batch(index, tokens, states.shape[0], q_start, slot_in, slot_out)
+    if out is None:
+        if _elsewhere(index, stream):
+            with _at(index, stream):
+                out = short_conv(x, weight, states, q_start, slot_in, slot_out, bias, silu, unit_heads, head_dim, eps)
+            _handed_out(index, stream, out)
+            return out
+        out = _empty(xs, dtype=dtype, device=x.device)
+    elif out.shape != xs or out.dtype is not dtype or out.get_device() != index:
+        raise Vq3Error(-1, "out must be like x")
+    xt, xc = x.stride()
+    ot, oc = out.stride()
+    if xc != 1 or oc != 1:
+        raise Vq3Error(-1, "the channels of x and out must be contiguous")
+    c = vq3_conv(TYPES[dtype], channels, width, bool(silu), unit_heads, head_dim, eps, x.data_ptr(), weight.data_ptr(),
+                 _ptr(bias), states.data_ptr(), out.data_ptr(), xt, ot, states.stride(0), states.stride(1))
+    _launch(index, stream, lib.vq3_short_conv, ctypes.byref(batch), ctypes.byref(c))
+    return out

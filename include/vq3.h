@@ -450,6 +450,120 @@ VQ3_API int vq3_prompt_attention(const vq3_attn* attn, const vq3_kv_rows* rows, 
                                  void* stream);
 
 /*
+ * The append with the position rotation on the way. The first `rotated` entries of every query and key
+ * head are taken as rotated / 2 pairs, pair i turned by the angle position * freq[i]:
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
+ * entries i and i + rotated / 2 (interleaved 0) or 2 i and 2 i + 1 (interleaved 1); the others are copied.
+ * Queries go to q_out, keys and values to slot slots[t] of the cache as in vq3_kv_append (slots outside the
+ * cache are skipped there, their queries are turned all the same). A token with a negative position is left
+ * out altogether: its row of q_out and the cache stay. positions and slots are vq3_paged_plan's, for instance.
+ * Angles are exact to some 2^-25 of a turn for any position; products in FP32, rounded once.
+ * type is that of q, k, v and the cache. rotated: a multiple of 16 up to head_dim. heads 0: no queries, q and
+ * q_out unused; otherwise q_out may be q with the same strides (in place) and overlaps nothing else.
+ * The pages name no rotation: this library's, as the calls around it.
+ * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ */
+typedef struct vq3_rotary {
+  int type;
+  int heads;       /* query heads, any number up to 65536 */
+  int rotated;
+  int interleaved;
+  const float* freq;     /* device, [rotated / 2], radians a position */
+  const int* positions;  /* device, [tokens of the rows] */
+  const void* q;
+  void* q_out;
+  long long q_token, q_head; /* strides */
+  long long out_token, out_head;
+} vq3_rotary;
+VQ3_API int vq3_kv_append_rotary(const vq3_rotary* rotary, const vq3_kv_rows* rows, const long long* slots,
+                                 const vq3_kv_cache* cache, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The delta-rule token mixer for packed requests, each with a state of its own in a slot of a pool: the
+ * other kind of layer of the pages' hybrid decoder in serving form. They give no interface for it; the
+ * two calls below are this library's, their batch that of the attention calls (q_start as there).
+ * slot_in[r] is the slot that request r goes on from: an entry outside [0, slots), or slot_in NULL, starts it
+ * from zeros. slot_out[r] takes its state after the last new token: an entry outside [0, slots), or slot_out
+ * NULL, keeps none. They may be the same slot. So a verify step can leave its state unwritten and the accepted
+ * tokens be run again, a prefix be shared (one slot_in for many), and a request be forked. A slot that one
+ * request writes is neither read nor written by another one of the same call. A request without new tokens
+ * has its state copied from slot to slot.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct vq3_batch {
+  int tokens;            /* rows of the call's inputs and outputs */
+  int requests;          /* at most 8192 */
+  int slots;             /* of the pool */
+  const int* q_start;    /* device, [requests + 1] */
+  const int* slot_in;    /* device, [requests], or NULL */
+  const int* slot_out;   /* device, [requests], or NULL */
+} vq3_batch;
+
+/*
+ * The gated delta rule, as vq3_delta_rule_forward: per value head h and token t, with the query/key head
+ * h / (v_heads / qk_heads),
+ *   S <- alpha[t][h] S + beta[t][h] k_t (v_t - alpha[t][h] S^T k_t)^T,   out_t = scale S^T q_t.
+ * States, sums and gates are FP32 (products with 22 bits of the state at least), out is rounded once. alpha may
+ * be 0 (the state starts over). Rows outside the requests are neither read nor written. All lengths live in
+ * device memory. max_new picks the kernel (1 or 2: one that streams the states; 8, 16: short chunks; above or
+ * 0: chunks of 32 tokens); a wrong value costs time, not correctness. Deterministic, no workspace, one launch.
+ * d_k 64, 128 or 256; d_v a multiple of 16 up to 4096. Strides as in the attention calls; alpha and beta have
+ * their heads side by side. out and states overlap no other buffer.
+ * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ */
+typedef struct vq3_delta {
+  int type;      /* VQ3_TYPE_* of q, k, v and out */
+  int qk_heads;
+  int v_heads;   /* a multiple of qk_heads */
+  int d_k;
+  int d_v;
+  int max_new;   /* most new tokens of a request, 0 if unknown */
+  float scale;
+  const void* q; /* [tokens][qk_heads][d_k], as k */
+  const void* k;
+  const void* v; /* [tokens][v_heads][d_v], as out */
+  void* out;
+  const float* beta; /* [tokens][v_heads], as alpha */
+  const float* alpha;
+  float* states;     /* [slots][v_heads][d_k][d_v], 16-byte aligned, a slot contiguous */
+  long long q_token, q_head, k_token, k_head; /* strides */
+  long long v_token, v_head, out_token, out_head;
+  long long beta_token, alpha_token;
+  long long state_slot;  /* a multiple of 4 */
+} vq3_delta;
+VQ3_API int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* stream);
+
+/*
+ * The short convolution in front of the delta rule: per channel c and token t
+ *   y = bias[c] + sum_j weight[c][j] x_(t - width + 1 + j)[c],   z = silu ? y / (1 + exp(-y)) : y,
+ * over the request's own tokens and, before its first, the width - 1 inputs of its slot (the last one newest),
+ * which become its last inputs. The first unit_heads heads of head_dim channels are brought to unit length:
+ * out = z / sqrt(sum over the head of z^2 + eps), the others are z. In FP32, rounded once; states are copies.
+ * width 2, 3 or 4; channels a multiple of 8 up to 2^20; head_dim a power of two in [8, 256] (0 without heads).
+ * x, out: rows of channels with strides that are multiples of 8; weight [channels][width], bias [channels] or
+ * NULL and states [slots][width - 1][channels] of the same type; all 16-byte aligned. out and states overlap no
+ * other buffer. Deterministic, one launch. Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
+ */
+typedef struct vq3_conv {
+  int type;      /* VQ3_TYPE_* of everything */
+  int channels;
+  int width;
+  int silu;
+  int unit_heads;
+  int head_dim;
+  float eps;
+  const void* x;
+  const void* weight;
+  const void* bias;
+  void* states;
+  void* out;
+  long long x_token, out_token; /* strides */
+  long long state_slot, state_row;
+} vq3_conv;
+VQ3_API int vq3_short_conv(const vq3_batch* batch, const vq3_conv* conv, void* stream);
+
+/*
  * Cited as vq3_residual_rmsnorm and vq3_mlp_forward (the two fused).
  * One layer of the pre-norm residual stack: r' = fp16(r_in + delta) (r_in alone when
  * delta is NULL), n = fp16(r' / sqrt(mean(r'^2) + eps)) per row, out = the MLP block
@@ -597,11 +711,12 @@ VQ3_API const char* vq3_version(void);
  * number of the first one (0 if none), for f = 0 decode, 1 low-rank factors,
  * 2 delta rule, 3 rotation and residual, 4 prefill up to 128 rows, 5 prefill above,
  * 6 attention of few rows and the combining pass, 7 attention on tensor cores, 8 page
- * plan and append. reset != 0 clears the counts after reading. n_out: entries of out, at
+ * plan and append, 9 delta rule of packed requests, 10 short convolution, 11 append with
+ * rotation. reset != 0 clears the counts after reading. n_out: entries of out, at
  * least 12 (else VQ3_EINVAL); files whose two entries do not fit are left out. Synchronous on the device (waits for all
  * work); call it between, not during, launches.
  */
-#define VQ3_BOUNDS_FILES 9
+#define VQ3_BOUNDS_FILES 12
 VQ3_API int vq3_bounds_check(unsigned* out, int n_out, int reset);
 
 #ifdef __cplusplus

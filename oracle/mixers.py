@@ -1,0 +1,92 @@
+"""Float64 oracle of the delta rule over packed requests, the short convolution and the rotated append, with
+the error that each number format leaves (TEST INFRASTRUCTURE ONLY; shares no code with the library).
+
+The delta rule's recurrence is oracle/delta_rule.py's. For keys of at most unit length and strengths in [0, 1] a
+token's map of a state column, s -> a (I - b k k^T) s + b v k, does not lengthen, so an error made at one token
+reaches the end no larger than it was made; errors of different tokens are taken as independent (their sum grows
+with the root of their number).
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+WINDOW = 32  # tokens at most in one chunk
+
+
+def delta(q, k, v, beta, alpha, state, scale):
+    """One head: out [T, dv], the final state, and what the error bound needs.
+
+    q, k [T, dk]; v [T, dv]; beta, alpha [T]; state [dk, dv], all as float64."""
+    S = np.array(state, np.float64)
+    T, dv = q.shape[0], v.shape[1]
+    out = np.empty((T, dv))
+    top = np.linalg.norm(S, axis=0)          # largest length of each state column so far
+    reach = np.empty((T, dv))                # |q| times it
+    near = np.empty((T, dv))                 # sum over the last WINDOW tokens of |q . k_j| |b_j u_j|
+    us = np.zeros((T, dv))
+    for t in range(T):
+        u = beta[t] * (v[t] - alpha[t] * (S.T @ k[t]))
+        S = alpha[t] * S + np.outer(k[t], u)
+        us[t] = np.abs(u)
+        out[t] = scale * (S.T @ q[t])
+        top = np.maximum(top, np.linalg.norm(S, axis=0))
+        lo = max(0, t + 1 - WINDOW)
+        reach[t] = np.linalg.norm(q[t]) * top
+        near[t] = np.abs(k[lo : t + 1] @ q[t]) @ us[lo : t + 1]
+    return out, S, {"top": top, "reach": reach, "near": near}
+
+
+def delta_bound(out, info, v, scale, dtype, q):
+    """Tolerances (out [T, dv], state per column [dv]).
+
+    FP32 operands enter the products with 22 bits or more (half a step 2^-22), sums of FP32: each of a token's
+    four products leaves up to 2^-21 of the column's length and value. BF16 outputs take their products from
+    11-bit operands (half a step 2^-11), one with the state and two with the chunk's own tokens."""
+    T = max(1, out.shape[0])
+    size = info["top"] + np.abs(v).max(axis=0, initial=0)
+    tol_state = 4 * 2.0**-21 * (1 + np.sqrt(T)) * size
+    half, part = (2.0**-8, 2.0**-11) if dtype == "bf16" else (2.0**-11, 2.0**-21)
+    tiny = 2.0**-134 if dtype == "bf16" else 2.0**-25  # half a step of subnormals
+    made = part * (info["reach"] + 2 * info["near"]) + np.linalg.norm(q, axis=1, keepdims=True) * tol_state
+    return half * np.abs(out) + (1 + half) * abs(scale) * made + tiny, tol_state
+
+
+def conv(x, old, w, bias, silu, unit_heads, head_dim, eps):
+    """One request: x [T, C], old [W - 1, C], w [C, W]; out, new state, tolerance before the last rounding."""
+    T, W = x.shape[0], w.shape[1]
+    line = np.concatenate([old, x])
+    y, mag = np.zeros(x.shape), np.zeros(x.shape)
+    for j in range(W):
+        y += w[:, j] * line[j : j + T]
+        mag += np.abs(w[:, j] * line[j : j + T])
+    if bias is not None:
+        y, mag = y + bias, mag + np.abs(bias)
+    z, err = y, W * 2.0**-24 * mag           # W fused multiply-adds
+    if silu:
+        # exp is off by 2 + 1.173 |y| units of the last place, the quotient by 2, the sum by 1/2
+        z = y / (1 + np.exp(-y))
+        err = 1.1 * err + np.abs(z) * 2.0**-23 * (5 + 1.2 * np.abs(y))
+    n = unit_heads * head_dim
+    if n:
+        h = z[:, :n].reshape(T, unit_heads, head_dim)
+        e = err[:, :n].reshape(T, unit_heads, head_dim)
+        length = np.sqrt((h * h).sum(-1, keepdims=True) + eps)
+        # the length is off by what its entries are off, by its sums' roundings and those of the root
+        rel = np.sqrt((e * e).sum(-1, keepdims=True)) / length + 2.0**-23 * (2 + np.log2(head_dim))
+        err = np.concatenate([(e / length + np.abs(h) / length * rel).reshape(T, n), err[:, n:]], 1)
+        z = np.concatenate([(h / length).reshape(T, n), z[:, n:]], 1)
+    return z, line[T:], err
+
+
+def rotate(x, positions, freq, interleaved):
+    """x [T, H, D] turned; the tolerance before the last rounding is 2^-21 of the pair's length."""
+    half = len(freq)
+    angle = positions[:, None].astype(np.float64) * np.asarray(freq, np.float64)
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    y, size = np.array(x, np.float64), np.zeros(x.shape)
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., b] * c + x[..., a] * s
+    size[..., a] = size[..., b] = np.hypot(x[..., a], x[..., b])
+    return y, 2.0**-21 * size
