@@ -517,7 +517,7 @@ int vq3_bounds_check(unsigned* out, int n_out, int reset) {
   cudaError_t (*const rd[VQ3_BOUNDS_FILES])(unsigned*, bool) = {
       bounds_read_persistent,   bounds_read_lowrank, bounds_read_delta,     bounds_read_rotate, bounds_read_prefill,
       bounds_read_prefill_wide, bounds_read_attn,    bounds_read_attn_wide, bounds_read_kvcache,
-      bounds_read_delta_batch, bounds_read_conv,    bounds_read_rotary};
+      bounds_read_delta_batch,  bounds_read_delta_wide, bounds_read_conv,   bounds_read_rotary};
   for (int f = 0; f < VQ3_BOUNDS_FILES && 2 * f + 1 < n_out; ++f) {
     const cudaError_t e = rd[f](out + 2 * f, reset != 0);
     if (e != cudaSuccess) return report_error(VQ3_ECUDA, "bounds_check: %s", cudaGetErrorString(e));

@@ -12,54 +12,15 @@
 //
 // Two kernels, chosen on the host: delta_chunk_kernel for chunks of 8, 16 or 32 tokens on tensor
 // cores, delta_step_kernel for one or a few tokens, which streams the state once through registers.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "vq3_internal.h"
 
 namespace vq3 {
 VQ3_BOUNDS_RECORD(delta_batch)
+}
+#include "delta_common.cuh"
+
+namespace vq3 {
 namespace {
-
-// ---------------------------------------------------------------- requests
-
-struct Request {
-  int first, n;              // its rows, inside the batch whatever the starts are
-  const float* in;           // its state of this head, or null: zeros
-  float* out;                // or null: not written
-};
-
-__device__ __forceinline__ Request delta_request(const DeltaArgs& a, int r, int h) {
-  Request q;
-  int s = __ldg(a.q_start + r), e = __ldg(a.q_start + r + 1);
-  s = s < 0 ? 0 : (s > a.tokens ? a.tokens : s);
-  e = e < s ? s : (e > a.tokens ? a.tokens : e);
-  q.first = s;
-  q.n = e - s;
-  const int in = a.slot_in ? __ldg(a.slot_in + r) : -1, out = a.slot_out ? __ldg(a.slot_out + r) : -1;
-  const long long head = (long long)h * a.d_k * a.d_v;
-  q.in = in >= 0 && in < a.slots ? a.states + in * a.state_slot + head : nullptr;
-  q.out = out >= 0 && out < a.slots ? a.states + out * a.state_slot + head : nullptr;
-  return q;
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (!BF16) return pack_f16(lo, hi);
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // ---------------------------------------------------------------- chunks on tensor cores
 //
@@ -82,22 +43,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 constexpr int kConsumers = 4, kProducers = 2, kStages = 3;
 constexpr int kChunkThreads = 32 * (kConsumers + kProducers);
 constexpr int kWarpCols = 16, kCtaCols = kWarpCols * kConsumers;
-constexpr int kFullBar = 1, kEmptyBar = kFullBar + kStages;
-constexpr int kBarThreads = 32 * (kConsumers + 1);
+// Named barriers: per stage and consumer warp "filled" (the warps do not wait for one another), per stage "free".
+constexpr int kFullBar = 1, kEmptyBar = kFullBar + kStages * kConsumers;
+constexpr int kFullThreads = 64, kEmptyThreads = 32 * (kConsumers + 1);
+static_assert(kEmptyBar + kStages <= 16, "named barriers");
 
 template <int KS, int NN>
 struct Stage {
   static constexpr int DK = 16 * KS, C = 8 * NN;
   static constexpr int RS = DK + 8;                              // row of K and Q in halves: 16 bytes past 128
   static constexpr int TS = NN == 4 ? 40 : (NN == 2 ? 24 : 8);   // row of T and M: ldmatrix without conflicts
-  static constexpr int kK = 0, kQ = kK + C * RS * 2, kT = kQ + C * RS * 2;
-  static constexpr int kM = kT + 2 * C * TS * 2, kC = kM + 2 * C * TS * 2;  // hi, then lo
+  static constexpr int VS = kCtaCols + 8;                        // row of V
+  static constexpr int kK = 0, kQ = kK + C * RS * 2, kV = kQ + C * RS * 2, kT = kV + C * VS * 2;
+  static constexpr int NS = C + 4;                               // column of N in floats
+  // T: hi, then lo; before, in the same place, N
+  static constexpr int kM = kT + (2 * TS * 2 > NS * 4 ? 2 * TS * 2 : NS * 4) * C, kC = kM + 2 * C * TS * 2;  // M: hi, lo
   static constexpr int kBytes = (kC + (5 * C + 4) * 4 + 127) / 128 * 128;
   // factors per token: of V in R, of K S0 in R, of Q S0 and of M U in O, of U in the state; then g_C
   static constexpr int kFv = 0, kFk = C, kFq = 2 * C, kFm = 3 * C, kFw = 4 * C, kFg = 5 * C;
-  static constexpr int NS = C + 4;                               // row of N in floats
-  static constexpr int kScratch = C * NS * 4;                    // per producer: ratios, then N
-  static constexpr int kTotal = kStages * kBytes + kProducers * kScratch;
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -141,22 +104,6 @@ __device__ __forceinline__ uint32_t ldsm1(uint32_t at) {
   return r;
 }
 
-// The power of two that brings m >= 0 to [2^8, 2^9), and its inverse; exponents are kept inside FP32's
-// normal range (an infinite or NaN m gives finite factors: the values themselves carry it on).
-struct Scale {
-  float to, back;
-};
-__device__ __forceinline__ Scale scale_of(float m) {
-  int e = (int)(__float_as_uint(m) >> 23);
-  e = e < 9 ? 9 : e;
-  return Scale{__uint_as_float((uint32_t)(262 - e) << 23), __uint_as_float((uint32_t)(e - 8) << 23)};
-}
-// Two FP32 values as FP16 pairs: hi, and what hi leaves.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_f16(x, y);
-  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  lo = pack_f16(x - h.x, y - h.y);
-}
 // Rows g and g + 8 of NN accumulator tiles: the largest magnitude over the row (lanes of one g).
 template <int NT>
 __device__ __forceinline__ void row_max(const float (&x)[NT][4], float& m0, float& m1) {
@@ -174,52 +121,82 @@ __device__ __forceinline__ void row_max(const float (&x)[NT][4], float& m0, floa
 }
 
 // ---- producer: one chunk's K, Q, T, M and factors
+//
+// One warp, so everything is a chain of latencies: the copies land while the ratios are formed, the
+// ratios and N are kept by columns (lane j's 16-byte stores and loads do not conflict), and the
+// substitution goes column by column: once x_m is known every later row takes its part, 31 - m
+// independent products, where row by row each x_m waits for a sum (2,000 -> 700 cycles at C = 32).
 template <int KS, int NN, bool BF16>
-__device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, int h, int t0, unsigned char* st,
-                                        float* scratch, int lane) {
+__device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& rq, int h, int col0, int t0,
+                                        unsigned char* st, int lane) {
   using L = Stage<KS, NN>;
   constexpr int C = L::C, RS = L::RS, DK = L::DK, TS = L::TS, NS = L::NS;
   const int nt = rq.n - t0 < C ? rq.n - t0 : C;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t sk = smem_of(st + L::kK), sq = smem_of(st + L::kQ);
-  // rows of K and Q, tokens past the last zero
-  const int hq = h / a.group;
-  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + (long long)(rq.first + t0) * a.k_token + hq * a.k_head;
-  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (long long)(rq.first + t0) * a.q_token + hq * a.q_head;
-#pragma unroll 4
-  for (int i = lane; i < C * (DK / 8); i += 32) {
-    const int row = i / (DK / 8), c = i % (DK / 8);
-    const uint32_t off = (uint32_t)(row * RS + c * 8) * 2u;
-    if (row < nt && VQ3_IN(rq.first + t0 + row, a.tokens, 1)) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sk + off), "l"(kp + row * a.k_token + c * 8) : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sq + off), "l"(qp + row * a.q_token + c * 8) : "memory");
-    } else {
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sk + off), "r"(0u) : "memory");
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sq + off), "r"(0u) : "memory");
-    }
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  float al = 1.f, be = 0.f;  // lane = token
+  float* const ratio = reinterpret_cast<float*>(st + L::kT);  // [column j][row i], then N; T takes its place
+  // gates, lane = token
+  float al = 1.f, be = 0.f;
   if (lane < nt && VQ3_IN(rq.first + t0 + lane, a.tokens, 2)) {
     al = __ldg(a.alpha + (long long)(rq.first + t0 + lane) * a.alpha_token + h);
     be = __ldg(a.beta + (long long)(rq.first + t0 + lane) * a.beta_token + h);
   }
+  // rows of K and Q, tokens past the last zero: a lane takes one 16-byte column of every RPI-th row
+  {
+    constexpr int CPR = DK / 8, RPI = 32 / CPR > 0 ? 32 / CPR : 1;
+    const int hq = h / a.group, r0 = lane / CPR, c = lane % CPR;
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + (rq.first + t0 + r0) * a.k_token + hq * a.k_head + c * 8;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (rq.first + t0 + r0) * a.q_token + hq * a.q_head + c * 8;
+    const uint32_t off = (uint32_t)(r0 * RS + c * 8) * 2u;
+#pragma unroll 2
+    for (int i = 0; i < C / RPI; ++i) {
+      const uint32_t at = off + (uint32_t)(i * RPI * RS) * 2u;
+      const int row = i * RPI + r0;
+      // bytes read: 16, or none past the last token (zeros are written)
+      const int bytes = row < nt && VQ3_IN(rq.first + t0 + row, a.tokens, 1) ? 16 : 0;
+      const long long from = bytes ? i * RPI : -r0;  // an address inside the rows
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sk + at), "l"(kp + from * a.k_token), "r"(bytes) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + at), "l"(qp + from * a.q_token), "r"(bytes) : "memory");
+    }
+    // V: 8 lanes a row; columns behind the last are not used
+    const int rv = lane >> 3, cv = (lane & 7) * 8;
+    const bool some = col0 + cv < a.d_v;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.v) + (rq.first + t0) * a.v_token + h * a.v_head + (some ? col0 + cv : 0);
+    const uint32_t sv = smem_of(st + L::kV) + (uint32_t)(rv * L::VS + cv) * 2u;
+#pragma unroll 2
+    for (int i = 0; i < C / 4; ++i) {
+      const int row = 4 * i + rv;
+      const int bytes = some && row < nt && VQ3_IN(rq.first + t0 + row, a.tokens, 4) ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sv + (uint32_t)(4 * i * L::VS) * 2u),
+                   "l"(vp + (bytes ? row : 0) * a.v_token), "r"(bytes) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   // ratios D[i][j] = a_(j+1) ... a_i (lane = j), the running product g_i, and g_C / g_j
+  float* const f = reinterpret_cast<float*>(st + L::kC);
+  if (lane < C) f[L::kFv + lane] = al;
+  __syncwarp();
   float r = 1.f, gam = 1.f, gi = 1.f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const float ai = __shfl_sync(0xffffffffu, al, i);
-    gam *= ai;
-    if (i == lane) gi = gam;
-    if (i > lane) r *= ai;
-    if (lane < C) scratch[i * NS + lane] = r;
+  for (int i = 0; i < C; i += 4) {
+    const float4 a4 = *reinterpret_cast<const float4*>(f + L::kFv + i);
+    const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+    float d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gam *= av[e];
+      gi = i + e == lane ? gam : gi;
+      r *= i + e > lane ? av[e] : 1.f;
+      d[e] = r;
+    }
+    if (lane < C) *reinterpret_cast<float4*>(ratio + lane * NS + i) = make_float4(d[0], d[1], d[2], d[3]);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncwarp();
   // BF16 rows to FP16, each scaled by a power of two (lane = row: 16 bytes past 128 a row, no conflicts)
   float kb = 1.f, qb = 1.f;
   if constexpr (BF16) {
-#pragma unroll
+#pragma unroll 1
     for (int m = 0; m < 2; ++m) {
       if (lane < C) {
         uint4* row = reinterpret_cast<uint4*>(st + (m ? L::kQ : L::kK) + lane * RS * 2);
@@ -232,15 +209,15 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
           for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e])));
         }
         const Scale s = scale_of(fmaxf(__low2float(top), __high2float(top)));
-        const __nv_bfloat162 f = __float2bfloat162_rn(s.to);
+        const __nv_bfloat162 fs = __float2bfloat162_rn(s.to);
 #pragma unroll 4
         for (int c = 0; c < DK / 8; ++c) {
           const uint4 w = row[c];
           uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), f);
-            const float2 y = unpack2<true>(*reinterpret_cast<const uint32_t*>(&x));
+            const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), fs);
+            const float2 y = delta_unpack2<true>(*reinterpret_cast<const uint32_t*>(&x));
             ws[e] = pack_f16(y.x, y.y);
           }
           row[c] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
@@ -257,30 +234,29 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
   for (int i = 0; i < kTiles; ++i) kq[i][0] = kq[i][1] = kq[i][2] = kq[i][3] = 0.f;
 #pragma unroll 2
   for (int s = 0; s < KS; ++s) {
-    uint32_t kf[NN][2], qf[NN][2];
+    uint32_t kf[NN][4];
 #pragma unroll
-    for (int b = 0; b < NN; ++b) {
-      // matrices: K columns 0-7, 8-15 of the step, Q the same
-      uint32_t f[4];
-      ldsm4(f, (lane < 16 ? sk : sq) + (uint32_t)((8 * b + (lane & 7)) * RS + 16 * s + ((lane >> 3) & 1) * 8) * 2u);
-      kf[b][0] = f[0];
-      kf[b][1] = f[1];
-      qf[b][0] = f[2];
-      qf[b][1] = f[3];
-    }
+    for (int b = 0; b < NN; ++b)  // matrices: K columns 0-7, 8-15 of the step, Q the same
+      ldsm4(kf[b], (lane < 16 ? sk : sq) + (uint32_t)((8 * b + (lane & 7)) * RS + 16 * s + ((lane >> 3) & 1) * 8) * 2u);
     int i = 0;
 #pragma unroll
     for (int b = 0; b < NN; ++b) {
-      const uint32_t af[4] = {kf[b][0], qf[b][0], kf[b][1], qf[b][1]};
+      const uint32_t af[4] = {kf[b][0], kf[b][2], kf[b][1], kf[b][3]};
 #pragma unroll
       for (int n = 0; n <= b; ++n, ++i) mma16(kq[i], af, kf[n][0], kf[n][1]);
     }
   }
-  // N over the ratios in scratch (each thread where it read them); M, rows scaled, as FP16 parts
+  // N over the ratios (each thread where it read them); M, rows scaled, as FP16 parts
   uint16_t* mhi = reinterpret_cast<uint16_t*>(st + L::kM);
   uint16_t* mlo = mhi + C * TS;
   const float bk = be * kb;  // b_j and the factor of k_j
   float fm = 0.f;
+  float bj[NN][2];
+#pragma unroll
+  for (int n = 0; n < NN; ++n) {
+    bj[n][0] = __shfl_sync(0xffffffffu, bk, 8 * n + 2 * t);
+    bj[n][1] = __shfl_sync(0xffffffffu, bk, 8 * n + 2 * t + 1);
+  }
   int i = 0;
 #pragma unroll
   for (int b = 0; b < NN; ++b) {
@@ -290,11 +266,11 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
 #pragma unroll
     for (int n = 0; n <= b; ++n, ++i) {
       const int row = 8 * b + g, col = 8 * n + 2 * t;
-      const float b0 = __shfl_sync(0xffffffffu, bk, col), b1 = __shfl_sync(0xffffffffu, bk, col + 1);
-      float2* at = reinterpret_cast<float2*>(scratch + row * NS + col);
-      const float2 d = *at;
-      const float d0 = d.x * b0, d1 = d.y * b1;
-      *at = make_float2(col < row ? d0 * ki * kq[i][0] : 0.f, col + 1 < row ? d1 * ki * kq[i][1] : 0.f);
+      float* at0 = ratio + col * NS + row;
+      float* at1 = at0 + NS;
+      const float d0 = *at0 * bj[n][0], d1 = *at1 * bj[n][1];
+      *at0 = col < row ? -d0 * ki * kq[i][0] : 0.f;
+      *at1 = col + 1 < row ? -d1 * ki * kq[i][1] : 0.f;
       m[n][0] = col <= row ? d0 * kq[i][2] : 0.f;
       m[n][1] = col + 1 <= row ? d1 * kq[i][3] : 0.f;
       top = fmaxf(top, fmaxf(fabsf(m[n][0]), fabsf(m[n][1])));
@@ -315,26 +291,25 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
     if (lane >> 3 == b) fm = back;
   }
   __syncwarp();
-  // T = (I + N)^-1 by forward substitution, lane = column
-  float x[C];
+  // T = (I + N)^-1 by forward substitution, lane = column of T; -N is in `ratio` by columns. Rows in pairs.
+  float2 x[C / 2];
 #pragma unroll
-  for (int k = 0; k < C; ++k) x[k] = 0.f;
+  for (int k = 0; k < C / 2; ++k) x[k] = make_float2(2 * k == lane ? 1.f : 0.f, 2 * k + 1 == lane ? 1.f : 0.f);
+#pragma unroll
+  for (int m = 0; m < C - 1; ++m) {
+    const float xm = m & 1 ? x[m / 2].y : x[m / 2].x;
+#pragma unroll
+    for (int k = (m + 1) / 4 * 4; k < C; k += 4) {  // rows up to m hold zeros (the diagonal block's)
+      const float4 nv = *reinterpret_cast<const float4*>(ratio + m * NS + k);
+      if (k + 1 > m) x[k / 2] = fma_pair(make_float2(nv.x, nv.y), xm, x[k / 2]);
+      x[k / 2 + 1] = fma_pair(make_float2(nv.z, nv.w), xm, x[k / 2 + 1]);
+    }
+  }
   float top = 0.f;
 #pragma unroll
-  for (int k = 0; k < C; ++k) {
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-    for (int m = 0; m < k; m += 4) {
-      const float4 nv = *reinterpret_cast<const float4*>(scratch + k * NS + m);
-      s0 = fmaf(nv.x, x[m], s0);
-      s1 = fmaf(nv.y, x[m + 1], s1);
-      s2 = fmaf(nv.z, x[m + 2], s2);
-      s3 = fmaf(nv.w, x[m + 3], s3);
-    }
-    x[k] = (k == lane ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
-    top = fmaxf(top, fabsf(x[k]));
-  }
+  for (int k = 0; k < C / 2; ++k) top = fmaxf(top, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
   const Scale ts = scale_of(top);
+  __syncwarp();  // every lane has read N
   if (lane < C) {  // column j of T as row j
     uint4* thi = reinterpret_cast<uint4*>(st + L::kT + lane * TS * 2);
     uint4* tlo = reinterpret_cast<uint4*>(st + L::kT + (C + lane) * TS * 2);
@@ -342,11 +317,10 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
     for (int k = 0; k < C; k += 8) {
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split2(x[k + 2 * e] * ts.to, x[k + 2 * e + 1] * ts.to, hi[e], lo[e]);
+      for (int e = 0; e < 4; ++e) split2(x[k / 2 + e].x * ts.to, x[k / 2 + e].y * ts.to, hi[e], lo[e]);
       thi[k / 8] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       tlo[k / 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    float* f = reinterpret_cast<float*>(st + L::kC);
     f[L::kFv + lane] = ts.back;
     f[L::kFk + lane] = gi * kb * ts.back;
     f[L::kFq + lane] = a.scale * gi * qb;
@@ -359,12 +333,12 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const Request& rq, i
 
 // ---- consumer: one chunk against this warp's 16 columns; acc: S^T, row g column 2g, row g + 8 column 2g + 1
 template <int KS, int NN, bool BF16>
-__device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const uint32_t (&vw)[NN][2], const unsigned char* st,
-                                        float (&o)[NN][4], int lane) {
+__device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int warp,
+                                        int lane) {
   using L = Stage<KS, NN>;
   constexpr int C = L::C, RS = L::RS, TS = L::TS;
   constexpr int K2 = NN == 1 ? 1 : NN / 2;  // steps of 16 tokens (one of 8 for NN = 1)
-  const int t = lane & 3;
+  const int g = lane >> 2, t = lane & 3;
   const uint32_t sk = smem_of(st + L::kK), sq = smem_of(st + L::kQ), sT = smem_of(st + L::kT), sM = smem_of(st + L::kM);
   const float* f = reinterpret_cast<const float*>(st + L::kC);
 
@@ -412,16 +386,25 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const uint32_t 
       }
     }
   }
+#pragma unroll
+  for (int n = 0; n < NN; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      xk[n][e] *= e < 2 ? s0.back : s1.back;
+      xq[n][e] *= e < 2 ? s0.back : s1.back;
+    }
   // R^T = V^T - X_K, times the factor of T's column
+  const unsigned char* sv = st + L::kV + ((2 * t) * L::VS + warp * kWarpCols + 2 * g) * 2;
 #pragma unroll
   for (int n = 0; n < NN; ++n) {
     const float2 fv = *reinterpret_cast<const float2*>(f + L::kFv + 8 * n + 2 * t);
     const float2 fk = *reinterpret_cast<const float2*>(f + L::kFk + 8 * n + 2 * t);
-    const float2 va = unpack2<BF16>(vw[n][0]), vb = unpack2<BF16>(vw[n][1]);
-    xk[n][0] = va.x * fv.x - fk.x * (s0.back * xk[n][0]);
-    xk[n][1] = vb.x * fv.y - fk.y * (s0.back * xk[n][1]);
-    xk[n][2] = va.y * fv.x - fk.x * (s1.back * xk[n][2]);
-    xk[n][3] = vb.y * fv.y - fk.y * (s1.back * xk[n][3]);
+    const float2 va = delta_unpack2<BF16>(*reinterpret_cast<const uint32_t*>(sv + 8 * n * L::VS * 2));
+    const float2 vb = delta_unpack2<BF16>(*reinterpret_cast<const uint32_t*>(sv + (8 * n + 1) * L::VS * 2));
+    xk[n][0] = va.x * fv.x - fk.x * xk[n][0];
+    xk[n][1] = vb.x * fv.y - fk.y * xk[n][1];
+    xk[n][2] = va.y * fv.x - fk.x * xk[n][2];
+    xk[n][3] = vb.y * fv.y - fk.y * xk[n][3];
   }
   // U^T = R^T T^T
   row_max<NN>(xk, m0, m1);
@@ -562,10 +545,10 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const uint32_t 
   for (int n = 0; n < NN; ++n) {
     const float2 fq = *reinterpret_cast<const float2*>(f + L::kFq + 8 * n + 2 * t);
     const float2 fm = *reinterpret_cast<const float2*>(f + L::kFm + 8 * n + 2 * t);
-    o[n][0] = fq.x * (s0.back * xq[n][0]) + fm.x * (u0.back * o[n][0]);
-    o[n][1] = fq.y * (s0.back * xq[n][1]) + fm.y * (u0.back * o[n][1]);
-    o[n][2] = fq.x * (s1.back * xq[n][2]) + fm.x * (u1.back * o[n][2]);
-    o[n][3] = fq.y * (s1.back * xq[n][3]) + fm.y * (u1.back * o[n][3]);
+    o[n][0] = fq.x * xq[n][0] + fm.x * (u0.back * o[n][0]);
+    o[n][1] = fq.y * xq[n][1] + fm.y * (u0.back * o[n][1]);
+    o[n][2] = fq.x * xq[n][2] + fm.x * (u1.back * o[n][2]);
+    o[n][3] = fq.y * xq[n][3] + fm.y * (u1.back * o[n][3]);
   }
 }
 
@@ -576,17 +559,16 @@ __global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_ke
   extern __shared__ __align__(128) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y;
-  const Request rq = delta_request(a, blockIdx.z, h);
+  const DeltaRequest rq = delta_request(a, blockIdx.z, h);
   const int chunks = (rq.n + C - 1) / C;
 
   if (warp >= kConsumers) {
-    const int p = warp - kConsumers;
-    float* scratch = reinterpret_cast<float*>(sm + kStages * L::kBytes + p * L::kScratch);
-    for (int c = p; c < chunks; c += kProducers) {
+    for (int c = warp - kConsumers; c < chunks; c += kProducers) {
       const int s = c % kStages;
-      if (c >= kStages) bar_sync(kEmptyBar + s, kBarThreads);  // the consumers are done with chunk c - kStages
-      produce<KS, NN, BF16>(a, rq, h, c * C, sm + s * L::kBytes, scratch, lane);
-      bar_arrive(kFullBar + s, kBarThreads);
+      if (c >= kStages) bar_sync(kEmptyBar + s, kEmptyThreads);  // the consumers are done with chunk c - kStages
+      produce<KS, NN, BF16>(a, rq, h, blockIdx.x * kCtaCols, c * C, sm + s * L::kBytes, lane);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) bar_arrive(kFullBar + s * kConsumers + w, kFullThreads);
     }
     return;
   }
@@ -608,37 +590,23 @@ __global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_ke
       acc[n][2 + e] = s.y;
     }
   }
-  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + (long long)rq.first * a.v_token + h * a.v_head + col;
-  uint16_t* op = static_cast<uint16_t*>(a.out) + (long long)rq.first * a.o_token + h * a.o_head + col;
-  uint32_t vw[NN][2];
-  const auto load_v = [&](int t0) {
-#pragma unroll
-    for (int n = 0; n < NN; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = t0 + 8 * n + 2 * t + e;
-        vw[n][e] = on && tok < rq.n && VQ3_IN(rq.first + tok, a.tokens, 4)
-                       ? __ldg(reinterpret_cast<const uint32_t*>(vp + tok * a.v_token)) : 0u;
-      }
-  };
-  load_v(0);
+  uint16_t* op = static_cast<uint16_t*>(a.out) + rq.first * a.o_token + h * a.o_head + col;
   for (int c = 0; c < chunks; ++c) {
     const int s = c % kStages;
-    bar_sync(kFullBar + s, kBarThreads);
+    bar_sync(kFullBar + s * kConsumers + warp, kFullThreads);
+    float o[NN][4];
+    if (on) consume<KS, NN, BF16>(acc, sm + s * L::kBytes, o, warp, lane);
+    if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kEmptyThreads);
     if (on) {
-      float o[NN][4];
-      consume<KS, NN, BF16>(acc, vw, sm + s * L::kBytes, o, lane);
 #pragma unroll
       for (int n = 0; n < NN; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int tok = c * C + 8 * n + 2 * t + e;
           if (tok < rq.n && VQ3_IN(rq.first + tok, a.tokens, 5))
-            *reinterpret_cast<uint32_t*>(op + tok * a.o_token) = pack2<BF16>(o[n][e], o[n][2 + e]);
+            *reinterpret_cast<uint32_t*>(op + tok * a.o_token) = delta_pack2<BF16>(o[n][e], o[n][2 + e]);
         }
-      load_v((c + 1) * C);
     }
-    if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kBarThreads);
   }
   if (on && rq.out && (chunks || rq.out != rq.in)) {
 #pragma unroll
@@ -653,7 +621,7 @@ __global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_ke
 
 template <int KS, int NN, bool BF16>
 cudaError_t launch_chunk(const DeltaArgs& a, cudaStream_t st) {
-  constexpr int smem = Stage<KS, NN>::kTotal;
+  constexpr int smem = kStages * Stage<KS, NN>::kBytes;
   const cudaError_t e =
       cudaFuncSetAttribute(delta_chunk_kernel<KS, NN, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -665,117 +633,22 @@ template <int KS, bool BF16>
 cudaError_t launch_chunk_of(const DeltaArgs& a, cudaStream_t st) {
   if (a.max_new > 0 && a.max_new <= 8) return launch_chunk<KS, 1, BF16>(a, st);
   if (a.max_new > 0 && a.max_new <= 16) return launch_chunk<KS, 2, BF16>(a, st);
-  return launch_chunk<KS, 4, BF16>(a, st);
+  if constexpr (KS <= 8)
+    return launch_delta_wide(a, BF16, st);
+  else
+    return launch_chunk<KS, 4, BF16>(a, st);
 }
 
 // ---------------------------------------------------------------- single tokens
 //
-// A CTA takes one request, one value head and 64 columns: 8 groups of 16 lanes hold every eighth row of S,
-// 4 columns a lane, in registers. With x = S^T k and y = S^T q of the OLD state both products need one pass
-// over it and one exchange between the groups:
-//     u = b (v - a x),   S <- a S + k u^T,   o = scale (a y + (k . q) u).
-// All in FP32. Bound by the state's bytes, read once and written once.
+// A CTA takes one request, one value head and 64 columns.
 constexpr int kStepThreads = 128;
 constexpr int kGroups = kStepThreads / 16;
 
 template <int ROWS, bool BF16>  // d_k = 8 * ROWS
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const __grid_constant__ DeltaArgs a) {
-  constexpr int DK = kGroups * ROWS;
-  __shared__ float2 kqs[2][DK];                              // (k, q) of the token
-  __shared__ float4 part[2][2][kStepThreads / 32][16];       // x and y by warp
-  __shared__ float dots[2][kStepThreads / 32];               // k . q by warp
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid >> 4, cl = tid & 15;
-  const int h = blockIdx.y, hq = h / a.group;
-  const Request rq = delta_request(a, blockIdx.z, h);
-  const int col = blockIdx.x * 64 + cl * 4;
-  const bool on = col < a.d_v;
-  const size_t n_state = (size_t)a.d_k * a.d_v;
-  float4 S[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const size_t at = (size_t)(i * kGroups + grp) * a.d_v + col;
-    S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on && rq.in && VQ3_IN(at + 3, n_state, 7)) S[i] = __ldcs(reinterpret_cast<const float4*>(rq.in + at));
-  }
-  for (int t = 0; t < rq.n; ++t) {
-    const int b = t & 1;
-    const long long row = rq.first + t;
-    const bool in = VQ3_IN(row, a.tokens, 8);
-    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + row * a.k_token + hq * a.k_head;
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + row * a.q_token + hq * a.q_head;
-    float dot = 0.f;
-    for (int d = tid * 2; d < DK; d += 2 * kStepThreads) {
-      const float2 k2 = in ? unpack2<BF16>(__ldg(reinterpret_cast<const uint32_t*>(kp + d))) : make_float2(0.f, 0.f);
-      const float2 q2 = in ? unpack2<BF16>(__ldg(reinterpret_cast<const uint32_t*>(qp + d))) : make_float2(0.f, 0.f);
-      kqs[b][d] = make_float2(k2.x, q2.x);
-      kqs[b][d + 1] = make_float2(k2.y, q2.y);
-      dot += k2.x * q2.x + k2.y * q2.y;
-    }
-    const float al = in ? __ldg(a.alpha + row * a.alpha_token + h) : 1.f;
-    const float be = in ? __ldg(a.beta + row * a.beta_token + h) : 0.f;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (on && in) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + row * a.v_token + h * a.v_head + col));
-      const float2 v0 = unpack2<BF16>(w.x), v1 = unpack2<BF16>(w.y);
-      v[0] = v0.x;
-      v[1] = v0.y;
-      v[2] = v1.x;
-      v[3] = v1.y;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (lane == 0) dots[b][warp] = dot;
-    __syncthreads();
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float2 kq = kqs[b][i * kGroups + grp];
-      x.x = fmaf(kq.x, S[i].x, x.x);
-      x.y = fmaf(kq.x, S[i].y, x.y);
-      x.z = fmaf(kq.x, S[i].z, x.z);
-      x.w = fmaf(kq.x, S[i].w, x.w);
-      y.x = fmaf(kq.y, S[i].x, y.x);
-      y.y = fmaf(kq.y, S[i].y, y.y);
-      y.z = fmaf(kq.y, S[i].z, y.z);
-      y.w = fmaf(kq.y, S[i].w, y.w);
-    }
-    const auto both = [](float f) { return f + __shfl_xor_sync(0xffffffffu, f, 16); };
-    x = make_float4(both(x.x), both(x.y), both(x.z), both(x.w));
-    y = make_float4(both(y.x), both(y.y), both(y.z), both(y.w));
-    if (lane < 16) {
-      part[b][0][warp][cl] = x;
-      part[b][1][warp][cl] = y;
-    }
-    __syncthreads();
-    x = y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float kq = 0.f;
-#pragma unroll
-    for (int w = 0; w < kStepThreads / 32; ++w) {
-      const float4 px = part[b][0][w][cl], py = part[b][1][w][cl];
-      x = make_float4(x.x + px.x, x.y + px.y, x.z + px.z, x.w + px.w);
-      y = make_float4(y.x + py.x, y.y + py.y, y.z + py.z, y.w + py.w);
-      kq += dots[b][w];
-    }
-    const float4 u = make_float4(be * (v[0] - al * x.x), be * (v[1] - al * x.y), be * (v[2] - al * x.z), be * (v[3] - al * x.w));
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float k = kqs[b][i * kGroups + grp].x;
-      S[i] = make_float4(fmaf(k, u.x, al * S[i].x), fmaf(k, u.y, al * S[i].y), fmaf(k, u.z, al * S[i].z),
-                         fmaf(k, u.w, al * S[i].w));
-    }
-    if (grp == 0 && on && in) {
-      const uint2 w = make_uint2(pack2<BF16>(a.scale * fmaf(kq, u.x, al * y.x), a.scale * fmaf(kq, u.y, al * y.y)),
-                                 pack2<BF16>(a.scale * fmaf(kq, u.z, al * y.z), a.scale * fmaf(kq, u.w, al * y.w)));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.o_token + h * a.o_head + col) = w;
-    }
-  }
-  if (on && rq.out && (rq.n || rq.out != rq.in)) {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const size_t at = (size_t)(i * kGroups + grp) * a.d_v + col;
-      if (VQ3_IN(at + 3, n_state, 9)) __stcs(reinterpret_cast<float4*>(rq.out + at), S[i]);
-    }
-  }
+  __shared__ StepShared<ROWS, kGroups, 16> sm;
+  delta_steps<ROWS, kGroups, 16, BF16>(a, delta_request(a, blockIdx.z, blockIdx.y), blockIdx.y, blockIdx.x * 64, sm);
 }
 
 template <int ROWS, bool BF16>

@@ -131,6 +131,7 @@ cudaError_t bounds_read_attn(unsigned* host, bool reset);
 cudaError_t bounds_read_attn_wide(unsigned* host, bool reset);
 cudaError_t bounds_read_kvcache(unsigned* host, bool reset);
 cudaError_t bounds_read_delta_batch(unsigned* host, bool reset);
+cudaError_t bounds_read_delta_wide(unsigned* host, bool reset);
 cudaError_t bounds_read_conv(unsigned* host, bool reset);
 cudaError_t bounds_read_rotary(unsigned* host, bool reset);
 #else
@@ -338,11 +339,13 @@ struct DeltaArgs {
   const int* slot_in;
   const int* slot_out;
   long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head, alpha_token, beta_token, state_slot;
+  int* status;  // or null
   int tokens, requests, slots, v_heads, group, d_k, d_v, max_new;
   float scale;
 };
 constexpr int kDeltaStepTokens = 2;  // max_new up to which single tokens' kernel runs
 cudaError_t launch_delta_batch(const DeltaArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_delta_wide(const DeltaArgs& a, bool bf16, cudaStream_t st);  // d_k 64 or 128
 struct ConvArgs {
   const uint16_t* x;
   const uint16_t* weight;

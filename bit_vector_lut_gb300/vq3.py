@@ -183,7 +183,7 @@ def version() -> str:
 
 
 BOUNDS_FILES = ("decode", "lowrank", "delta", "rotate", "prefill", "prefill_wide", "attn", "attn_wide", "kvcache",
-                "delta_batch", "conv", "rotary")
+                "delta_batch", "delta_wide", "conv", "rotary")
 
 
 def bounds_check(reset: bool = True) -> dict[str, tuple[int, int]]:

@@ -711,12 +711,12 @@ VQ3_API const char* vq3_version(void);
  * number of the first one (0 if none), for f = 0 decode, 1 low-rank factors,
  * 2 delta rule, 3 rotation and residual, 4 prefill up to 128 rows, 5 prefill above,
  * 6 attention of few rows and the combining pass, 7 attention on tensor cores, 8 page
- * plan and append, 9 delta rule of packed requests, 10 short convolution, 11 append with
- * rotation. reset != 0 clears the counts after reading. n_out: entries of out, at
+ * plan and append, 9 delta rule of packed requests, 10 its prompts, 11 short convolution,
+ * 12 append with rotation. reset != 0 clears the counts after reading. n_out: entries of out, at
  * least 12 (else VQ3_EINVAL); files whose two entries do not fit are left out. Synchronous on the device (waits for all
  * work); call it between, not during, launches.
  */
-#define VQ3_BOUNDS_FILES 12
+#define VQ3_BOUNDS_FILES 13
 VQ3_API int vq3_bounds_check(unsigned* out, int n_out, int reset);
 
 #ifdef __cplusplus
