@@ -13,7 +13,7 @@
 //   warps 12-13  T = (I + N)^-1, one column a lane: the two 32 x 32 blocks by substitution, then
 //                T21 = -T22 N21 T11
 //   warp 14      issues the products of the state
-//   warp 15      copies K, Q and V by TMA
+//   warp 15      copies K, Q and V by TMA and issues [K; Q] K^T
 // The chain of a chunk is X_K, R, U, U w, dS, S; what is not on it (X_Q, O and its output of the chunk before, the
 // next chunks' rows and T) runs under it. FP32 operands enter as two FP16 parts as in delta_batch.cu. The scale of S
 // has to be known before dS is: it is made from a bound, |g_C| max |S| + sum |u w| max |k|, which is some 2^5 above
@@ -54,16 +54,19 @@ struct Wide {
   static constexpr int KB = DK / 64;             // 64-column blocks of K and Q
   static constexpr int SD = DK / 2;              // rows of S a thread
   static constexpr int NS = kC + 4;              // row of N in floats
-  // [K; Q] by 64-column blocks, T and M in the 128-byte swizzle; V; factors; N
+  // [K; Q] by 64-column blocks, T and M in the 128-byte swizzle; V; the output; factors
   static constexpr int kBlock = 2 * kC * 128, kTile = kC * 128;
-  static constexpr int kKQBytes = KB * kBlock, kTBytes = 2 * kTile, kMBytes = (BF16 ? 1 : 2) * kTile;
+  // (a place of T holds N first)
+  static constexpr int kKQBytes = KB * kBlock, kTBytes = kC * NS * 4, kMBytes = (BF16 ? 1 : 2) * kTile;
   static constexpr int kVBytes = kC * kCols * 2, kFBytes = 2048;
-  static constexpr int kKQ = 0, kT = kKQ + 3 * kKQBytes, kM = kT + 2 * kTBytes, kV = kM + 2 * kMBytes, kF = kV + 2 * kVBytes;
+  static_assert(kTBytes >= 2 * kTile && kTBytes % 1024 == 0, "N and T");
+  static constexpr int kKQ = 0, kT = kKQ + 3 * kKQBytes, kM = kT + 2 * kTBytes, kV = kM + 2 * kMBytes, kOut = kV + 2 * kVBytes;
+  static constexpr int kF = kOut + kVBytes;
   // factors per token: of V and of X_K in R, of X_Q and of U M in O, of U in dS, the largest |k|; then g_C
   static constexpr int kFv = 0, kFk = 64, kFq = 128, kFm = 192, kFw = 256, kKm = 320, kG = 384;
-  static constexpr int kN = kF + 3 * kFBytes;
-  // exchange of the column's halves: float2 [2][128], float4 [2][128]; rows: gates and factors; barriers
-  static constexpr int kX1 = kN + kC * NS * 4, kX2 = kX1 + 2048, kRow = kX2 + 4096, kMax = kRow + 1024, kBar = kMax + 256;
+  // exchange of the column's halves: float2 [2][128], float4 [2][128]; scales for the output: float2 [2][128]; rows: gates
+  // and factors; barriers
+  static constexpr int kX1 = kF + 3 * kFBytes, kX2 = kX1 + 2048, kXO = kX2 + 4096, kRow = kXO + 2048, kMax = kRow + 1024, kBar = kMax + 256;
   static constexpr int kSmem = kBar + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -79,17 +82,15 @@ enum {
   kbTFree = 15,   // [2]
   kbM = 17,       // [2]
   kbMFree = 19,   // [2]
-  kbFFree = 21,   // [3] factors
-  kbN = 24, kbNFree, kbKK,
-  kbS = 27,       // [4] S stored: half of d_k, half of that
-  kbXK = 31, kbR, kbU, kbXQ, kbW,
-  kbD = 36,       // [2]
-  kbO = 38, kbORead, kbDrain, kBars
+  kbN = 21, kbKK,
+  kbS = 23,       // [4] S stored: half of d_k, half of that
+  kbXK = 27, kbR, kbU, kbXQ, kbW,
+  kbD = 32,       // [2]
+  kbO = 34, kbORead, kbDrain, kBars
 };
 
 struct DeltaMaps {
-  CUtensorMap k, q, v;
-  int v_box;      // columns of a copy of V
+  CUtensorMap k, q, v, out;
 };
 
 __device__ __forceinline__ float2 bits2(const uint32_t* r, int i) {
@@ -110,12 +111,13 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
 // A wait tries so often, each try sleeping so long at most: a second in all.
 constexpr int kTries = 200000;
 constexpr uint32_t kTryNs = 5000;
-__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity) {
+constexpr int kPolls = 4000000;  // of the copying warp, with 100 ns between two
+__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns = kTryNs) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kTryNs)
+      : "r"(bar), "r"(parity), "r"(ns)
       : "memory");
   return ok != 0;
 }
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
 
   if (tid < kBars) {
     // arrivals: a copy, a product's completion or a warp each
-    constexpr int n[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 8, 8, 8, 2, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 8, 1};
+    constexpr int n[kBars] = {1, 1, 1, 4, 4, 4, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 4, 1};
     mbar_init(bar(tid), KB == 1 && tid >= kbS && tid < kbS + 4 ? 8 : n[tid]);
     if (tid == 0) *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -186,7 +188,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
     float2* const x1 = reinterpret_cast<float2*>(smem + L::kX1);
     float4* const x2 = reinterpret_cast<float4*>(smem + L::kX2);
     const auto pair_sync = [&] { sync_threads(1 + sub, 64); };
-    const auto factors = [&](int ch) { return reinterpret_cast<const float*>(smem + L::kF + (ch % 3) * L::kFBytes); };
     float2 S[SD / 2];
     float mS = 0.f;
 #pragma unroll
@@ -198,9 +199,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
     }
     x1[hf * 128 + c] = make_float2(mS, 0.f);
     pair_sync();
-    Scale ss = scale_of<14>(fmaxf(mS, x1[(hf ^ 1) * 128 + c].x)), ss_old = ss, ws{0.f, 0.f};
-    float gC = 1.f, ub = 1.f;
-    uint16_t* op = static_cast<uint16_t*>(a.out) + rq.first * a.o_token + h * a.o_head + col + (32 * hf) * a.o_token;
+    Scale ss = scale_of<14>(fmaxf(mS, x1[(hf ^ 1) * 128 + c].x)), ws{0.f, 0.f};
+    float gC = 1.f;
     for (int ch = 0;; ++ch) {
       // S <- g_C S + dS, and its parts for the products, half by half
       if (ch) {
@@ -231,150 +231,105 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         // behind the last chunk, too: U M goes where dS was, once everyone has read it
         arrive(kbS + (KB == 2 ? 2 * hf : 0) + i / 32);
       }
+      if (ch == chunks) break;
+      const float* f = reinterpret_cast<const float*>(smem + L::kF + (ch % 3) * L::kFBytes);
+      // R^T = V^T - X_K^T, times the factor of T's column
+      wait(kbVFull + (ch & 1), ch >> 1);
       uint32_t x[32];
       float2 r[16];
-      float top = 0.f, mS_all = 0.f;
-      Scale rs{1.f, 1.f};
-      const float* f = factors(ch);
-      if (ch < chunks) {
-        // R^T = V^T - X_K^T, times the factor of T's column
-        wait(kbVFull + (ch & 1), ch >> 1);
-        uint16_t vw[32];
-        {
-          const uint16_t* v = reinterpret_cast<const uint16_t*>(smem + L::kV + (ch & 1) * L::kVBytes) + 32 * hf * maps.v_box +
-                              (on ? c : 0);
+      float top = 0.f;
+      uint16_t vw[32];
+      {
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(smem + L::kV + (ch & 1) * L::kVBytes) + 32 * hf * kCols + c;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) vw[j] = v[j * maps.v_box];
-          const int left = rq.n - ch * kC - 32 * hf;  // rows behind the request's last are another's
-          if (left < 32)
+        for (int j = 0; j < 32; ++j) vw[j] = v[j * kCols];
+        const int left = rq.n - ch * kC - 32 * hf;  // rows behind the request's last are another's
+        if (left < 32)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j >= left) vw[j] = 0;
+          for (int j = 0; j < 32; ++j)
+            if (j >= left) vw[j] = 0;
+      }
+      arrive(kbVFree + (ch & 1));
+      wait(kbTM + (ch & 1), ch >> 1);
+      wait(kbXK, ch);
+      tc_after();
+      tmem_ld32(tm + kTmX + 32u * hf, x);
+      tc_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 fv = *reinterpret_cast<const float4*>(f + L::kFv + 32 * hf + j);
+        const float4 fk = *reinterpret_cast<const float4*>(f + L::kFk + 32 * hf + j);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float2 v2 = delta_unpack2<BF16>((uint32_t)vw[j + e] | (uint32_t)vw[j + e + 1] << 16);
+          float2& y = r[(j + e) / 2];
+          y = mul_pair(v2, e ? make_float2(fv.z, fv.w) : make_float2(fv.x, fv.y));
+          y = fma_pair(mul_pair(bits2(x, j + e), -ss.back), e ? make_float2(fk.z, fk.w) : make_float2(fk.x, fk.y), y);
+          top = max_pair(top, y);
         }
-        arrive(kbVFree + (ch & 1));
-        wait(kbTM + (ch & 1), ch >> 1);
-        wait(kbXK, ch);
+      }
+      x1[hf * 128 + c] = make_float2(top, mS);
+      pair_sync();
+      const float2 o1 = x1[(hf ^ 1) * 128 + c];
+      const Scale rs = scale_of(fmaxf(top, o1.x));
+      const float mS_all = fmaxf(mS, o1.y);
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], rs.to), hi[e], lo[e]);
+      if (ch) {  // U M of the chunk before has read U
+        wait(kbO, ch - 1);
         tc_after();
-        tmem_ld32(tm + kTmX + 32u * hf, x);
-        tc_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 fv = *reinterpret_cast<const float4*>(f + L::kFv + 32 * hf + j);
-          const float4 fk = *reinterpret_cast<const float4*>(f + L::kFk + 32 * hf + j);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 v2 = delta_unpack2<BF16>((uint32_t)vw[j + e] | (uint32_t)vw[j + e + 1] << 16);
-            float2& y = r[(j + e) / 2];
-            y = mul_pair(v2, e ? make_float2(fv.z, fv.w) : make_float2(fv.x, fv.y));
-            y = fma_pair(mul_pair(bits2(x, j + e), -ss.back), e ? make_float2(fk.z, fk.w) : make_float2(fk.x, fk.y), y);
-            top = max_pair(top, y);
-          }
-        }
-        x1[hf * 128 + c] = make_float2(top, mS);
-        pair_sync();
-        const float2 o1 = x1[(hf ^ 1) * 128 + c];
-        rs = scale_of(fmaxf(top, o1.x));
-        mS_all = fmaxf(mS, o1.y);
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], rs.to), hi[e], lo[e]);
-        if (ch) {  // U M of the chunk before has read U
-          wait(kbO, ch - 1);
-          tc_after();
-        }
-        tmem_st16(tm + kTmR + 16u * hf, hi);
-        tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
-        tc_wait_st();
-        arrive(kbR);
       }
-      // the output of the chunk before, up to its stores
-      uint32_t two[16];
-      if (ch) {
-        const float* f0 = factors(ch - 1);
-        if (ch == chunks) {
-          wait(kbO, ch - 1);
-          tc_after();
-        }
-        uint32_t um[32];
-        tmem_ld32(tm + kTmQ + 32u * hf, x);
-        tmem_ld32(tm + kTmD + 32u * hf, um);
-        tc_wait_ld();
-        arrive(kbORead);
+      tmem_st16(tm + kTmR + 16u * hf, hi);
+      tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
+      tc_wait_st();
+      arrive(kbR);
+      // U^T, as it is for the output and times w for dS
+      wait(kbU, ch);
+      tc_after();
+      tmem_ld32(tm + kTmX + 32u * hf, x);
+      tc_wait_ld();
+      float topu = 0.f, l1 = 0.f;
+      top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 fq = *reinterpret_cast<const float4*>(f0 + L::kFq + 32 * hf + j);
-          const float4 fm = *reinterpret_cast<const float4*>(f0 + L::kFm + 32 * hf + j);
+      for (int j = 0; j < 32; j += 4) {
+        const float4 fw = *reinterpret_cast<const float4*>(f + L::kFw + 32 * hf + j);
+        const float4 km = *reinterpret_cast<const float4*>(f + L::kKm + 32 * hf + j);
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 q = mul_pair(bits2(x, j + e), ss_old.back), u = mul_pair(bits2(um, j + e), ub);
-            const float2 y = fma_pair(e ? make_float2(fm.z, fm.w) : make_float2(fm.x, fm.y), u,
-                                      mul_pair(e ? make_float2(fq.z, fq.w) : make_float2(fq.x, fq.y), q));
-            two[(j + e) / 2] = delta_pack2<BF16>(y.x, y.y);
-          }
+        for (int e = 0; e < 4; e += 2) {
+          float2& u = r[(j + e) / 2];
+          u = mul_pair(bits2(x, j + e), rs.back);
+          const float2 w = mul_pair(u, e ? make_float2(fw.z, fw.w) : make_float2(fw.x, fw.y));
+          topu = max_pair(topu, u);
+          top = max_pair(top, w);
+          l1 = fmaf(fabsf(w.x), e ? km.z : km.x, fmaf(fabsf(w.y), e ? km.w : km.y, l1));
         }
-        arrive(kbFFree + (ch - 1) % 3);
       }
-      if (ch < chunks) {
-        // U^T, as it is for the output and times w for dS
-        wait(kbU, ch);
-        tc_after();
-        tmem_ld32(tm + kTmX + 32u * hf, x);
-        tc_wait_ld();
-        float topu = 0.f, l1 = 0.f;
-        top = 0.f;
+      x2[hf * 128 + c] = make_float4(topu, top, l1, 0.f);
+      pair_sync();
+      const float4 o2 = x2[(hf ^ 1) * 128 + c];
+      const Scale us = scale_of(fmaxf(topu, o2.x));
+      ws = scale_of(fmaxf(top, o2.y));
+      gC = f[L::kG];
+      if (hf == 0) reinterpret_cast<float2*>(smem + L::kXO)[(ch & 1) * 128 + c] = make_float2(ss.back, us.back);
+      ss = scale_of<14>(fabsf(gC) * mS_all + (l1 + o2.z));
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 fw = *reinterpret_cast<const float4*>(f + L::kFw + 32 * hf + j);
-          const float4 km = *reinterpret_cast<const float4*>(f + L::kKm + 32 * hf + j);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            float2& u = r[(j + e) / 2];
-            u = mul_pair(bits2(x, j + e), rs.back);
-            const float2 w = mul_pair(u, e ? make_float2(fw.z, fw.w) : make_float2(fw.x, fw.y));
-            topu = max_pair(topu, u);
-            top = max_pair(top, w);
-            l1 = fmaf(fabsf(w.x), e ? km.z : km.x, fmaf(fabsf(w.y), e ? km.w : km.y, l1));
-          }
-        }
-        x2[hf * 128 + c] = make_float4(topu, top, l1, 0.f);
-        pair_sync();
-        const float4 o2 = x2[(hf ^ 1) * 128 + c];
-        const Scale us = scale_of(fmaxf(topu, o2.x));
-        ws = scale_of(fmaxf(top, o2.y));
-        gC = f[L::kG];
-        ss_old = ss;
-        ub = us.back;
-        ss = scale_of<14>(fabsf(gC) * mS_all + (l1 + o2.z));
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float4 fw = *reinterpret_cast<const float4*>(f + L::kFw + 32 * hf + 2 * e);
-          split2(mul_pair(mul_pair(r[e], make_float2(fw.x, fw.y)), ws.to), hi[e], lo[e]);
-          split2(mul_pair(mul_pair(r[e + 1], make_float2(fw.z, fw.w)), ws.to), hi[e + 1], lo[e + 1]);
-        }
-        wait(kbXQ, ch);  // X_Q has read S, whose place this takes
-        tc_after();
-        tmem_st16(tm + kTmW + 16u * hf, hi);
-        tmem_st16(tm + kTmW + 32u + 16u * hf, lo);
-        tc_wait_st();
-        arrive(kbW);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], us.to), hi[e], lo[e]);
-        tmem_st16(tm + kTmR + 16u * hf, hi);  // (kbS comes behind these stores, and U M behind kbS)
-        if constexpr (!BF16) tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
-        tc_wait_st();
+      for (int e = 0; e < 16; e += 2) {
+        const float4 fw = *reinterpret_cast<const float4*>(f + L::kFw + 32 * hf + 2 * e);
+        split2(mul_pair(mul_pair(r[e], make_float2(fw.x, fw.y)), ws.to), hi[e], lo[e]);
+        split2(mul_pair(mul_pair(r[e + 1], make_float2(fw.z, fw.w)), ws.to), hi[e + 1], lo[e + 1]);
       }
-      if (ch) {  // the output's stores, while dS is multiplied
-        const int t0 = (ch - 1) * kC + 32 * hf, left = on && !dead ? rq.n - t0 : 0;
-        uint16_t* o = op;
+      wait(kbXQ, ch);  // X_Q has read S, whose place this takes
+      tc_after();
+      tmem_st16(tm + kTmW + 16u * hf, hi);
+      tmem_st16(tm + kTmW + 32u + 16u * hf, lo);
+      tc_wait_st();
+      arrive(kbW);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j < left && VQ3_IN(rq.first + t0 + j, a.tokens, 2)) *o = (uint16_t)(j & 1 ? two[j / 2] >> 16 : two[j / 2]);
-          o += a.o_token;
-        }
-        op += kC * a.o_token;
-      }
-      if (ch == chunks) break;
+      for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], us.to), hi[e], lo[e]);
+      tmem_st16(tm + kTmR + 16u * hf, hi);  // (kbS comes behind these stores, and U M behind kbS)
+      if constexpr (!BF16) tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
+      tc_wait_st();
     }
     if (on && rq.out && !dead) {
 #pragma unroll
@@ -393,7 +348,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
     const bool is_k = p < 64;
     float* const gate = reinterpret_cast<float*>(smem + L::kRow);  // a_(j + 1); b_j and the factor of k_j; g_C / g_j; a_0
     float *const bks = gate + 64, *const rest = bks + 64, *const gate0 = rest + 64;
-    float* const n_col = reinterpret_cast<float*>(smem + L::kN) + i;
     float al = 1.f, be = 0.f;  // of the next chunk
     const auto load_gates = [&](int t0) {
       al = 1.f;
@@ -403,11 +357,69 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         be = __ldg(a.beta + (long long)(rq.first + t0 + p) * a.beta_token + h);
       }
     };
+    // Output of a chunk, this warp's 32 columns (lane = column), through shared memory.
+    const int sub = warp - kRowWarp;
+    const int row_bytes = 2 * (a.d_v - col0 < kCols ? a.d_v - col0 : kCols);
+    const auto output = [&](int ch) {
+      const uint32_t tm = tmem + ((uint32_t)(sub * 32) << 16), tile = base + (uint32_t)L::kOut;
+      const float* f = reinterpret_cast<const float*>(smem + L::kF + (ch % 3) * L::kFBytes);
+      wait(kbO, ch);
+      tc_after();
+      const float2 back = reinterpret_cast<const float2*>(smem + L::kXO)[(ch & 1) * 128 + sub * 32 + lane];
+#pragma unroll 1
+      for (int j0 = 0; j0 < kC; j0 += 32) {
+        uint32_t xq[32], um[32];
+        tmem_ld32(tm + kTmQ + (uint32_t)j0, xq);
+        tmem_ld32(tm + kTmD + (uint32_t)j0, um);
+        tc_wait_ld();
+        if (j0) arrive(kbORead);
+        const uint32_t at = tile + (uint32_t)(j0 * kCols + sub * 32 + lane) * 2u;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 fq = *reinterpret_cast<const float4*>(f + L::kFq + j0 + j);
+          const float4 fm = *reinterpret_cast<const float4*>(f + L::kFm + j0 + j);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float2 q = mul_pair(bits2(xq, j + e), back.x), u = mul_pair(bits2(um, j + e), back.y);
+            const float2 y = fma_pair(e ? make_float2(fm.z, fm.w) : make_float2(fm.x, fm.y), u,
+                                      mul_pair(e ? make_float2(fq.z, fq.w) : make_float2(fq.x, fq.y), q));
+            const uint32_t two = delta_pack2<BF16>(y.x, y.y);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (uint32_t)((j + e) * kCols * 2)), "h"((uint16_t)two) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (uint32_t)((j + e + 1) * kCols * 2)), "h"((uint16_t)(two >> 16)) : "memory");
+          }
+        }
+      }
+      fence_async();
+      sync_threads(9, 128);  // whole rows
+      if (rq.n - ch * kC >= kC) {
+        if (p == 0 && !*abort && VQ3_IN(rq.first + ch * kC + kC - 1, a.tokens, 2))
+          asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                           reinterpret_cast<uint64_t>(&maps.out)),
+                       "r"(col0), "r"(h), "r"(rq.first + ch * kC), "r"(tile)
+                       : "memory");
+      } else {  // the rows behind the request's last are another's: row by row, up to 256 bytes
+        const int t = 16 * sub + lane;
+        if (lane < 16 && ch * kC + t < rq.n && !*abort && VQ3_IN(rq.first + ch * kC + t, a.tokens, 2)) {
+          const uint16_t* to = static_cast<const uint16_t*>(a.out) + (rq.first + ch * kC + t) * a.o_token + h * a.o_head + col0;
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(tile + (uint32_t)(t * kCols * 2)),
+                       "r"(row_bytes) : "memory");
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    };
+    const auto output_read = [&] { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); };
     load_gates(0);
-    for (int ch = 0; ch < chunks; ++ch) {
+    for (int ch = 0; ch < chunks + 3; ++ch) {
+      if (ch > 2) output(ch - 3);  // (chunk ch's factors go where those of ch - 3 were)
+      if (ch >= chunks) {
+        output_read();
+        sync_threads(9, 128);
+        continue;
+      }
       const int t0 = ch * kC, nt = rq.n - t0 < kC ? rq.n - t0 : kC, s3 = ch % 3;
       const uint32_t kq = base + (uint32_t)(L::kKQ + s3 * L::kKQBytes);
       float* const f = reinterpret_cast<float*>(smem + L::kF + s3 * L::kFBytes);
+      if (ch > 2) output_read();
       sync_threads(9, 128);  // the last chunk's gates have been read
       if (is_k) {
         if (p)
@@ -417,7 +429,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       }
       const float b_i = be;
       load_gates(t0 + kC);
-      if (ch >= 3) wait(kbFFree + s3, ch / 3 - 1);
       wait(kbKQFull + s3, ch / 3);
       // thread = row of [K; Q]: its largest entry; BF16 to FP16, scaled by a power of two; rows behind the last are zero
       float back = 1.f, largest = 512.f;
@@ -471,21 +482,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         f[L::kKm + p] = largest;
       }
       fence_async();
-      tc_before();
+      arrive(kbKQ + s3);  // (KK of the last chunk has been read)
       sync_threads(9, 128);
-      if (warp == kRowWarp) {
-        tc_after();
-        if (!dead) {
-#pragma unroll 1
-          for (int b = 0; b < KB; ++b) {
-            const uint64_t d = desc_sw128(kq + (uint32_t)(b * L::kBlock), 16);
-            mma_ss4(tmem + kTmKK, d, d, id_k, b > 0);
-          }
-        }
-        mma_commit(bar(kbKK));
-        if (lane == 0) mbar_arrive(bar(kbKQ + s3));
-        __syncwarp();
-      }
       // a_(j + 1) ... a_i for j < i, 1 from there on
       float r[kC], run = 1.f;
 #pragma unroll
@@ -504,7 +502,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         for (int j = 0; j < kC; j += 4) *reinterpret_cast<float4*>(rest + j) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
         f[L::kG] = gi;
       }
-      if (is_k && ch) wait(kbNFree, ch - 1);
+      if (is_k && ch >= 2) wait(kbTFree + (ch & 1), (ch >> 1) - 1);
       wait(kbKK, ch);
       tc_after();
       float top = 0.f;
@@ -530,6 +528,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         }
       }
       if (is_k) {
+        float* const n_col = reinterpret_cast<float*>(smem + L::kT + (ch & 1) * L::kTBytes) + i;
 #pragma unroll
         for (int j = 0; j < kC; ++j)
           if (j < 32 || i >= 32) n_col[j * L::NS] = r[j];
@@ -563,10 +562,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       // ---------------------------------------------------------- T, -N by columns
       const int w = warp - kInvWarp;
       float* const tops = reinterpret_cast<float*>(smem + L::kMax);
-      float* const n = reinterpret_cast<float*>(smem + L::kN);
       constexpr int NS = L::NS;
       for (int ch = 0; ch < chunks; ++ch) {
         wait(kbN, ch);
+        float* const n = reinterpret_cast<float*>(smem + L::kT + (ch & 1) * L::kTBytes);
         // a 32 x 32 block of the diagonal; rows in pairs
         float2 x[16];
 #pragma unroll
@@ -638,8 +637,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         tops[w * 32 + lane] = w == 0 ? fmaxf(top, topy) : topy;
         sync_threads(10, 64);
         const Scale s0 = scale_of(fmaxf(tops[lane], tops[32 + lane])), s1 = scale_of(top);  // column lane; 32 + lane
-        arrive(kbNFree);
-        if (ch >= 2) wait(kbTFree + (ch & 1), (ch >> 1) - 1);
         const uint32_t t = base + (uint32_t)(L::kT + (ch & 1) * L::kTBytes);
         const auto put = [&](int j, int q, const float2* v, float to) {
           uint32_t hi[4], lo[4];
@@ -755,36 +752,55 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       __syncwarp();
     } else {
       // ---------------------------------------------------------- copies; rows behind the request's last come along
-      if (lane < 3) {
+      if (lane < 4) {
         const CUtensorMap* const m = &maps.k + lane;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
       }
       const int hq = h / a.group;
-      int n_kq = 0, n_v = 0;  // copies begun
-      for (int ch = 0; ch < chunks; ++ch) {
-        const int s3 = ch % 3, s2 = ch & 1, row = rq.first + ch * kC;
-        const uint32_t kq = base + (uint32_t)(L::kKQ + s3 * L::kKQBytes);
-        if (ch >= 3) wait(kbKQFree + s3, ch / 3 - 1);
-        if (dead) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(kbKQFull + s3), (uint32_t)L::kKQBytes);
-#pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            tma_3d(kq + (uint32_t)(b * L::kBlock), &maps.k, 64 * b, hq, row, bar(kbKQFull + s3));
-            tma_3d(kq + (uint32_t)(b * L::kBlock) + kC * 128u, &maps.q, 64 * b, hq, row, bar(kbKQFull + s3));
+      int n_kq = 0, n_v = 0, n_kk = 0;  // begun
+      const auto done = [&](int i, int use) { return __all_sync(0xffffffffu, try_wait_for(bar(i), (uint32_t)(use & 1), 0)); };
+      // Each as soon as its place is free and its operands are there; the tries without any are bounded.
+      for (int tries = 0; (n_kq < chunks || n_v < chunks || n_kk < chunks) && tries < kPolls && !*abort; ++tries) {
+        if (n_kq < chunks && (n_kq < 3 || done(kbKQFree + n_kq % 3, n_kq / 3 - 1))) {
+          if (lane == 0) {
+            const int s = n_kq % 3;
+            const uint32_t kq = base + (uint32_t)(L::kKQ + s * L::kKQBytes);
+            mbar_expect_tx(bar(kbKQFull + s), (uint32_t)L::kKQBytes);
+#pragma unroll 1
+            for (int b = 0; b < KB; ++b) {
+              tma_3d(kq + (uint32_t)(b * L::kBlock), &maps.k, 64 * b, hq, rq.first + n_kq * kC, bar(kbKQFull + s));
+              tma_3d(kq + (uint32_t)(b * L::kBlock) + kC * 128u, &maps.q, 64 * b, hq, rq.first + n_kq * kC, bar(kbKQFull + s));
+            }
           }
+          __syncwarp();
+          ++n_kq;
+          tries = 0;
         }
-        __syncwarp();
-        ++n_kq;
-        if (ch >= 2) wait(kbVFree + s2, (ch >> 1) - 1);
-        if (dead) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(kbVFull + s2), (uint32_t)(kC * maps.v_box * 2));
-          tma_3d(base + (uint32_t)(L::kV + s2 * L::kVBytes), &maps.v, col0, h, row, bar(kbVFull + s2));
+        if (n_v < chunks && (n_v < 2 || done(kbVFree + (n_v & 1), (n_v >> 1) - 1))) {
+          if (lane == 0) {
+            const int s = n_v & 1;
+            mbar_expect_tx(bar(kbVFull + s), (uint32_t)L::kVBytes);
+            tma_3d(base + (uint32_t)(L::kV + s * L::kVBytes), &maps.v, col0, h, rq.first + n_v * kC, bar(kbVFull + s));
+          }
+          __syncwarp();
+          ++n_v;
+          tries = 0;
         }
-        __syncwarp();
-        ++n_v;
+        if (n_kk < chunks && done(kbKQ + n_kk % 3, n_kk / 3)) {  // [K; Q] K^T
+          tc_after();
+#pragma unroll 1
+          for (int b = 0; b < KB; ++b) {
+            const uint64_t d = desc_sw128(base + (uint32_t)(L::kKQ + (n_kk % 3) * L::kKQBytes + b * L::kBlock), 16);
+            mma_ss4(tmem + kTmKK, d, d, id_k, b > 0);
+          }
+          mma_commit(bar(kbKK));
+          ++n_kk;
+          tries = 0;
+        }
+        __nanosleep(100);
       }
+      if (n_kk < chunks || n_v < chunks) *abort = 1;
+      if (n_kk) mbar_drain(bar(kbKK), (uint32_t)((n_kk - 1) & 1));
       // no copy is in flight when the CTA ends (they have all been used unless a wait gave up)
       for (int i = n_kq > 3 ? n_kq - 3 : 0; i < n_kq; ++i) mbar_drain(bar(kbKQFull + i % 3), (uint32_t)((i / 3) & 1));
       for (int i = n_v > 2 ? n_v - 2 : 0; i < n_v; ++i) mbar_drain(bar(kbVFull + (i & 1)), (uint32_t)((i >> 1) & 1));
@@ -806,13 +822,12 @@ cudaError_t launch(const DeltaArgs& a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(delta_wide_kernel<DK, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   alignas(64) DeltaMaps maps;
-  maps.v_box = a.d_v < kCols ? a.d_v : kCols;
   const cuuint64_t qk[3] = {(cuuint64_t)DK, (cuuint64_t)(a.v_heads / a.group), (cuuint64_t)a.tokens};
   const cuuint64_t v[3] = {(cuuint64_t)a.d_v, (cuuint64_t)a.v_heads, (cuuint64_t)a.tokens};
-  const cuuint32_t box[3] = {64, 1, kC}, v_box[3] = {(cuuint32_t)maps.v_box, 1, kC};
-  const long long qs[2] = {a.q_head, a.q_token}, ks[2] = {a.k_head, a.k_token}, vs[2] = {a.v_head, a.v_token};
+  const cuuint32_t box[3] = {64, 1, kC}, v_box[3] = {kCols, 1, kC};
+  const long long qs[2] = {a.q_head, a.q_token}, ks[2] = {a.k_head, a.k_token}, vs[2] = {a.v_head, a.v_token}, os[2] = {a.o_head, a.o_token};
   if (!tensor_map(&maps.q, BF16, a.q, 3, qk, qs, box) || !tensor_map(&maps.k, BF16, a.k, 3, qk, ks, box) ||
-      !tensor_map(&maps.v, BF16, a.v, 3, v, vs, v_box, false))
+      !tensor_map(&maps.v, BF16, a.v, 3, v, vs, v_box, false) || !tensor_map(&maps.out, BF16, a.out, 3, v, os, v_box, false))
     return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((a.d_v + kCols - 1) / kCols), (unsigned)a.v_heads, (unsigned)a.requests);
   delta_wide_kernel<DK, BF16><<<grid, kWideThreads, smem, st>>>(a, maps);
