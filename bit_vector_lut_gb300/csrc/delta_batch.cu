@@ -553,10 +553,10 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
 }
 
 template <int KS, int NN, bool BF16>
-__global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
+__global__ void __launch_bounds__(kChunkThreads, KS > 8 ? 1 : (NN == 1 ? 3 : 2)) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
   using L = Stage<KS, NN>;
   constexpr int C = L::C;
-  extern __shared__ __align__(128) unsigned char sm[];
+  extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y;
   const DeltaRequest rq = delta_request(a, blockIdx.z, h);
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_ke
     for (int c = warp - kConsumers; c < chunks; c += kProducers) {
       const int s = c % kStages;
       if (c >= kStages) bar_sync(kEmptyBar + s, kEmptyThreads);  // the consumers are done with chunk c - kStages
-      produce<KS, NN, BF16>(a, rq, h, blockIdx.x * kCtaCols, c * C, sm + s * L::kBytes, lane);
+      produce<KS, NN, BF16>(a, rq, h, blockIdx.x * kCtaCols, c * C, smem + s * L::kBytes, lane);
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) bar_arrive(kFullBar + s * kConsumers + w, kFullThreads);
     }
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kChunkThreads, KS <= 8 ? 2 : 1) delta_chunk_ke
     const int s = c % kStages;
     bar_sync(kFullBar + s * kConsumers + warp, kFullThreads);
     float o[NN][4];
-    if (on) consume<KS, NN, BF16>(acc, sm + s * L::kBytes, o, warp, lane);
+    if (on) consume<KS, NN, BF16>(acc, smem + s * L::kBytes, o, warp, lane);
     if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kEmptyThreads);
     if (on) {
 #pragma unroll
@@ -629,14 +629,260 @@ cudaError_t launch_chunk(const DeltaArgs& a, cudaStream_t st) {
   delta_chunk_kernel<KS, NN, BF16><<<grid, kChunkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
+// ---------------------------------------------------------------- a few tokens
+//
+// Verify steps: blocks of 8 tokens, the mathematics and numbers of a chunk, but every warp by itself, with 16 columns of a
+// head's state in registers and no barrier: bound by the state's bytes, it lives from many warps that each wait for
+// their own loads. K and Q are loaded as the B operand of S^T [K; Q]^T, which is also both operands of [K; Q] K^T and,
+// transposed by movmatrix, K's part of the state's product. The order of d_k within a product is free: a lane loads 16
+// bytes of a row, two pairs of entries for each of two steps, and the state's rows follow (block_row). N goes through 64 floats of shared memory to lanes that
+// each solve for a column of T. (16 requests x 8 tokens, 48 heads of 128 x 128: 28.8 us as chunks of 8 whose T and M two
+// warps made for four; 41 us in FP32 on CUDA cores, bound by the reads of k and q from shared memory.)
+constexpr int kBlockTokens = 8, kBlockThreads = 128;
+
+template <bool BF16>
+__device__ __forceinline__ void row_to_f16(uint32_t* x, int n, float& back) {  // a row's entries in 4 lanes
+  if constexpr (BF16) {
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < n; ++i) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[i])));
+    float m = fmaxf(__low2float(top), __high2float(top));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const Scale s = scale_of(m);
+    const __nv_bfloat162 f = __float2bfloat162_rn(s.to);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]), f);
+      const float2 z = delta_unpack2<true>(*reinterpret_cast<const uint32_t*>(&y));
+      x[i] = pack_f16(z.x, z.y);
+    }
+    back = s.back;
+  }
+}
+// The row of the state at entry e of lane t in tile n: 8-entry tiles 4 i .. 4 i + 3 hold the 32 rows from 32 i on, 8 to a lane.
+__device__ __forceinline__ int block_row(int n, int t, int e) { return 32 * (n >> 2) + 8 * t + 2 * (n & 3) + e; }
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 template <int KS, bool BF16>
-cudaError_t launch_chunk_of(const DeltaArgs& a, cudaStream_t st) {
-  if (a.max_new > 0 && a.max_new <= 8) return launch_chunk<KS, 1, BF16>(a, st);
-  if (a.max_new > 0 && a.max_new <= 16) return launch_chunk<KS, 2, BF16>(a, st);
-  if constexpr (KS <= 8)
-    return launch_delta_wide(a, BF16, st);
-  else
-    return launch_chunk<KS, 4, BF16>(a, st);
+__global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_kernel(const __grid_constant__ DeltaArgs a) {
+  constexpr int B = kBlockTokens;
+  __shared__ float solve[kBlockThreads / 32][B][B];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, hq = h / a.group, c0 = blockIdx.x * kCtaCols + warp * kWarpCols;
+  if (c0 >= a.d_v) return;  // (no barrier of the block's follows)
+  const DeltaRequest rq = delta_request(a, blockIdx.z, h);
+  const int col = c0 + 2 * g;
+  const size_t n_state = (size_t)a.d_k * a.d_v;
+  float(*const sn)[B] = solve[warp];
+  float acc[2 * KS][4];
+#pragma unroll
+  for (int n = 0; n < 2 * KS; ++n) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const size_t at = (size_t)block_row(n, t, e) * a.d_v + col;
+      float2 s = make_float2(0.f, 0.f);
+      if (rq.in && VQ3_IN(at + 1, n_state, 10)) s = __ldcs(reinterpret_cast<const float2*>(rq.in + at));
+      acc[n][e] = s.x;
+      acc[n][2 + e] = s.y;
+    }
+  }
+  for (int t0 = 0; t0 < rq.n; t0 += B) {
+    const int nt = rq.n - t0 < B ? rq.n - t0 : B;
+    const long long row0 = rq.first + t0;
+    // K, Q of token g; tokens past the last: zeros, a gate of 1, a strength of 0
+    uint32_t kf[2 * KS], qf[2 * KS];
+    {
+      const bool in = g < nt && VQ3_IN(row0 + g, a.tokens, 11);
+      const uint16_t* kp = static_cast<const uint16_t*>(a.k) + (row0 + (in ? g : 0)) * a.k_token + hq * a.k_head + 8 * t;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (row0 + (in ? g : 0)) * a.q_token + hq * a.q_head + 8 * t;
+#pragma unroll
+      for (int i = 0; i < 2 * KS; i += 4) {
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), q = k;
+        if (in) {
+          k = __ldg(reinterpret_cast<const uint4*>(kp + 8 * i));
+          q = __ldg(reinterpret_cast<const uint4*>(qp + 8 * i));
+        }
+        kf[i] = k.x;
+        kf[i + 1] = k.y;
+        kf[i + 2] = k.z;
+        kf[i + 3] = k.w;
+        qf[i] = q.x;
+        qf[i + 1] = q.y;
+        qf[i + 2] = q.z;
+        qf[i + 3] = q.w;
+      }
+    }
+    uint32_t vw[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int tok = 2 * t + e;
+      vw[e] = tok < nt && VQ3_IN(row0 + tok, a.tokens, 12)
+                  ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.v) + (row0 + tok) * a.v_token + h * a.v_head + col))
+                  : 0u;
+    }
+    float al = 1.f, be = 0.f;
+    if (lane < nt && VQ3_IN(row0 + lane, a.tokens, 13)) {
+      al = __ldg(a.alpha + (row0 + lane) * a.alpha_token + h);
+      be = __ldg(a.beta + (row0 + lane) * a.beta_token + h);
+    }
+    // d0, d1: a_(j+1) ... a_g of j = 2 t, 2 t + 1; of those tokens: a_1 ... a_j and a_(j+1) ... a_8
+    float d0 = 1.f, d1 = 1.f, g0 = 1.f, g1 = 1.f, e0 = 1.f, e1 = 1.f, g8 = 1.f;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const float ai = __shfl_sync(0xffffffffu, al, i);
+      g8 *= ai;
+      (i <= 2 * t ? g0 : e0) *= ai;
+      (i <= 2 * t + 1 ? g1 : e1) *= ai;
+      if (i <= g) {
+        d0 *= i > 2 * t ? ai : 1.f;
+        d1 *= i > 2 * t + 1 ? ai : 1.f;
+      }
+    }
+    float kb = 1.f, qb = 1.f;  // of token g
+    row_to_f16<BF16>(kf, 2 * KS, kb);
+    row_to_f16<BF16>(qf, 2 * KS, qb);
+    const float bk = __shfl_sync(0xffffffffu, be, g) * kb;
+    const float bk0 = __shfl_sync(0xffffffffu, bk, 8 * t), bk1 = __shfl_sync(0xffffffffu, bk, 8 * t + 4);
+    const float kb0 = __shfl_sync(0xffffffffu, kb, 8 * t), kb1 = __shfl_sync(0xffffffffu, kb, 8 * t + 4);
+    const float qb0 = __shfl_sync(0xffffffffu, qb, 8 * t), qb1 = __shfl_sync(0xffffffffu, qb, 8 * t + 4);
+    float kq[4] = {0.f, 0.f, 0.f, 0.f};  // k_g . k_j, q_g . k_j of j = 2 t, 2 t + 1
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t af[4] = {kf[2 * s], qf[2 * s], kf[2 * s + 1], qf[2 * s + 1]};
+      mma16(kq, af, kf[2 * s], kf[2 * s + 1]);
+    }
+    sn[g][2 * t] = 2 * t < g ? d0 * bk0 * kb * kq[0] : 0.f;
+    sn[g][2 * t + 1] = 2 * t + 1 < g ? d1 * bk1 * kb * kq[1] : 0.f;
+    const float m0 = 2 * t <= g ? d0 * bk0 * kq[2] : 0.f, m1 = 2 * t + 1 <= g ? d1 * bk1 * kq[3] : 0.f;
+    __syncwarp();
+    // T by forward substitution, lane % 8 = column
+    float x[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      x[i] = i == (lane & 7) ? 1.f : 0.f;
+#pragma unroll
+      for (int m = 0; m < i; ++m) x[i] = fmaf(-sn[i][m], x[m], x[i]);
+    }
+    __syncwarp();
+    if (lane < B)
+#pragma unroll
+      for (int i = 0; i < B; ++i) sn[i][lane] = x[i];
+    __syncwarp();
+    const float2 tr = *reinterpret_cast<const float2*>(&sn[g][2 * t]);
+    __syncwarp();
+    const auto over_t = [](float m) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    const Scale ts = scale_of(over_t(fmaxf(fabsf(tr.x), fabsf(tr.y)))), ms = scale_of(over_t(fmaxf(fabsf(m0), fabsf(m1))));
+    uint32_t th, tl, mh, ml;
+    split2(tr.x * ts.to, tr.y * ts.to, th, tl);
+    split2(m0 * ms.to, m1 * ms.to, mh, ml);
+    const float tb0 = __shfl_sync(0xffffffffu, ts.back, 8 * t), tb1 = __shfl_sync(0xffffffffu, ts.back, 8 * t + 4);
+    const float mb0 = __shfl_sync(0xffffffffu, ms.back, 8 * t), mb1 = __shfl_sync(0xffffffffu, ms.back, 8 * t + 4);
+
+    // X^T = S^T [K; Q]^T
+    float top0, top1;
+    row_max<2 * KS>(acc, top0, top1);
+    const Scale s0 = scale_of(top0), s1 = scale_of(top1);
+    float xk[1][4] = {{0.f, 0.f, 0.f, 0.f}}, xq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        split2(acc[2 * s + p][0] * s0.to, acc[2 * s + p][1] * s0.to, hi[2 * p], lo[2 * p]);
+        split2(acc[2 * s + p][2] * s1.to, acc[2 * s + p][3] * s1.to, hi[2 * p + 1], lo[2 * p + 1]);
+      }
+      mma16(xk[0], hi, kf[2 * s], kf[2 * s + 1]);
+      mma16(xq, hi, qf[2 * s], qf[2 * s + 1]);
+      mma16(xk[0], lo, kf[2 * s], kf[2 * s + 1]);
+      if constexpr (!BF16) mma16(xq, lo, qf[2 * s], qf[2 * s + 1]);
+    }
+    // R^T, U^T
+    {
+      const float2 va = delta_unpack2<BF16>(vw[0]), vb = delta_unpack2<BF16>(vw[1]);
+      xk[0][0] = va.x - g0 * kb0 * (s0.back * xk[0][0]);
+      xk[0][1] = vb.x - g1 * kb1 * (s0.back * xk[0][1]);
+      xk[0][2] = va.y - g0 * kb0 * (s1.back * xk[0][2]);
+      xk[0][3] = vb.y - g1 * kb1 * (s1.back * xk[0][3]);
+    }
+    uint32_t hi[4], lo[4];
+    row_max<1>(xk, top0, top1);
+    const Scale r0 = scale_of(top0), r1 = scale_of(top1);
+    split2(xk[0][0] * r0.to, xk[0][1] * r0.to, hi[0], lo[0]);
+    split2(xk[0][2] * r1.to, xk[0][3] * r1.to, hi[1], lo[1]);
+    float u[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+    mma8(u[0], hi, th);
+    mma8(u[0], lo, th);
+    mma8(u[0], hi, tl);
+    u[0][0] *= r0.back * tb0;
+    u[0][1] *= r0.back * tb1;
+    u[0][2] *= r1.back * tb0;
+    u[0][3] *= r1.back * tb1;
+    // O^T = X_Q + U^T M^T
+    {
+      row_max<1>(u, top0, top1);
+      const Scale u0 = scale_of(top0), u1 = scale_of(top1);
+      split2(u[0][0] * u0.to, u[0][1] * u0.to, hi[0], lo[0]);
+      split2(u[0][2] * u1.to, u[0][3] * u1.to, hi[1], lo[1]);
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      mma8(o, hi, mh);
+      if constexpr (!BF16) {
+        mma8(o, lo, mh);
+        mma8(o, hi, ml);
+      }
+      const float f0 = a.scale * qb0, f1 = a.scale * qb1;
+      uint16_t* op = static_cast<uint16_t*>(a.out) + row0 * a.o_token + h * a.o_head + col;
+      if (2 * t < nt && VQ3_IN(row0 + 2 * t, a.tokens, 14))
+        *reinterpret_cast<uint32_t*>(op + 2 * t * a.o_token) =
+            delta_pack2<BF16>(f0 * (g0 * (s0.back * xq[0]) + mb0 * (u0.back * o[0])), f0 * (g0 * (s1.back * xq[2]) + mb0 * (u1.back * o[2])));
+      if (2 * t + 1 < nt && VQ3_IN(row0 + 2 * t + 1, a.tokens, 14))
+        *reinterpret_cast<uint32_t*>(op + (2 * t + 1) * a.o_token) =
+            delta_pack2<BF16>(f1 * (g1 * (s0.back * xq[1]) + mb1 * (u0.back * o[1])), f1 * (g1 * (s1.back * xq[3]) + mb1 * (u1.back * o[3])));
+    }
+    // S^T <- g_8 S^T + (U diag w)^T K
+    u[0][0] *= bk0 * e0;
+    u[0][1] *= bk1 * e1;
+    u[0][2] *= bk0 * e0;
+    u[0][3] *= bk1 * e1;
+    row_max<1>(u, top0, top1);
+    const Scale w0 = scale_of(top0), w1 = scale_of(top1);
+    split2(u[0][0] * w0.to, u[0][1] * w0.to, hi[0], lo[0]);
+    split2(u[0][2] * w1.to, u[0][3] * w1.to, hi[1], lo[1]);
+#pragma unroll
+    for (int n = 0; n < 2 * KS; ++n) {
+      const uint32_t kt = transposed(kf[n]);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma8(d, hi, kt);
+      mma8(d, lo, kt);
+      acc[n][0] = fmaf(w0.back, d[0], g8 * acc[n][0]);
+      acc[n][1] = fmaf(w0.back, d[1], g8 * acc[n][1]);
+      acc[n][2] = fmaf(w1.back, d[2], g8 * acc[n][2]);
+      acc[n][3] = fmaf(w1.back, d[3], g8 * acc[n][3]);
+    }
+  }
+  if (rq.out && (rq.n || rq.out != rq.in)) {
+#pragma unroll
+    for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const size_t at = (size_t)block_row(n, t, e) * a.d_v + col;
+        if (VQ3_IN(at + 1, n_state, 15)) __stcs(reinterpret_cast<float2*>(rq.out + at), make_float2(acc[n][e], acc[n][2 + e]));
+      }
+  }
+}
+
+template <int DK, bool BF16>
+cudaError_t launch_block(const DeltaArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.d_v + kCtaCols - 1) / kCtaCols), (unsigned)a.v_heads, (unsigned)a.requests);
+  delta_block_kernel<DK / 16, BF16><<<grid, kBlockThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- single tokens
@@ -658,14 +904,20 @@ cudaError_t launch_step(const DeltaArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int DK, bool BF16>
+cudaError_t launch_of(const DeltaArgs& a, cudaStream_t st) {
+  if (a.max_new > 0 && a.max_new <= kDeltaStepTokens) return launch_step<DK / kGroups, BF16>(a, st);
+  if (a.max_new > 0 && a.max_new <= kDeltaBlockTokens) return launch_block<DK, BF16>(a, st);
+  if constexpr (DK <= 128)
+    return launch_delta_wide(a, BF16, st);
+  else
+    return launch_chunk<DK / 16, 4, BF16>(a, st);
+}
 template <bool BF16>
 cudaError_t launch_delta_type(const DeltaArgs& a, cudaStream_t st) {
-  const bool step = a.max_new > 0 && a.max_new <= kDeltaStepTokens;
-  switch (a.d_k) {
-    case 64: return step ? launch_step<8, BF16>(a, st) : launch_chunk_of<4, BF16>(a, st);
-    case 128: return step ? launch_step<16, BF16>(a, st) : launch_chunk_of<8, BF16>(a, st);
-    default: return step ? launch_step<32, BF16>(a, st) : launch_chunk_of<16, BF16>(a, st);
-  }
+  if (a.d_k == 64) return launch_of<64, BF16>(a, st);
+  if (a.d_k == 128) return launch_of<128, BF16>(a, st);
+  return launch_of<256, BF16>(a, st);
 }
 
 }  // namespace

@@ -69,15 +69,19 @@ __device__ __forceinline__ float2 bits_pair(unsigned long long r) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(r));
   return y;
 }
-__device__ __forceinline__ float2 mul_pair(float2 x, float2 y) {
+__device__ __forceinline__ unsigned long long mul_bits(unsigned long long x, unsigned long long y) {
   unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(x)), "l"(pair_bits(y)));
-  return bits_pair(r);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
 }
-__device__ __forceinline__ float2 fma_pair(float2 x, float2 y, float2 a) {
+__device__ __forceinline__ unsigned long long fma_bits(unsigned long long x, unsigned long long y, unsigned long long a) {
   unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(x)), "l"(pair_bits(y)), "l"(pair_bits(a)));
-  return bits_pair(r);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul_pair(float2 x, float2 y) { return bits_pair(mul_bits(pair_bits(x), pair_bits(y))); }
+__device__ __forceinline__ float2 fma_pair(float2 x, float2 y, float2 a) {
+  return bits_pair(fma_bits(pair_bits(x), pair_bits(y), pair_bits(a)));
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 mul_pair(float2 x, float m) { return mul_pair(x, both(m)); }

@@ -343,7 +343,7 @@ struct DeltaArgs {
   int tokens, requests, slots, v_heads, group, d_k, d_v, max_new;
   float scale;
 };
-constexpr int kDeltaStepTokens = 2;  // max_new up to which single tokens' kernel runs
+constexpr int kDeltaStepTokens = 2, kDeltaBlockTokens = 16;  // max_new up to which the kernels of few tokens run
 cudaError_t launch_delta_batch(const DeltaArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_delta_wide(const DeltaArgs& a, bool bf16, cudaStream_t st);  // d_k 64 or 128
 struct ConvArgs {
