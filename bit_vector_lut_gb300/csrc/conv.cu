@@ -46,6 +46,35 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+__device__ __forceinline__ unsigned long long pair_of(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma_two(unsigned long long x, unsigned long long y, unsigned long long a) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(a));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul_two(unsigned long long x, unsigned long long y) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ void split_pair(unsigned long long v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ int start_of(const ConvArgs& a, int r) {
   const int s = __ldg(a.q_start + r);
   return s < 0 ? 0 : (s > a.tokens ? a.tokens : s);
@@ -54,9 +83,10 @@ __device__ __forceinline__ int start_of(const ConvArgs& a, int r) {
 // Tile i of the launch: request r's tiles begin at index first_r / L + r, which leaves room for all of them
 // (ceil(n / L) <= (first + n) / L - first / L + 1), whatever the lengths are.
 template <int W, bool BF16>
-__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_constant__ ConvArgs a, int shift) {
+__global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __grid_constant__ ConvArgs a, int shift,
+                                                                   int blocks) {
   __shared__ int counts[kConvThreads / 32];
-  const int tile = blockIdx.x, tid = threadIdx.x, L = 1 << shift;
+  const int tile = blockIdx.x / blocks, tid = threadIdx.x, L = 1 << shift;
   int before = 0;  // requests whose tiles begin at or before this one
   for (int i = tid; i < a.requests; i += kConvThreads) before += (start_of(a, i) >> shift) + i <= tile;
   before = __reduce_add_sync(0xffffffffu, before);
@@ -69,7 +99,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
   const int s = start_of(a, r), e = max(s, start_of(a, r + 1)), n = e - s;
   const int t0 = (tile - (s >> shift) - r) << shift;  // from the request's first token
   if (t0 < 0 || (t0 >= n && t0 > 0)) return;
-  const int c = (blockIdx.y * kConvThreads + tid) * 8;
+  const int c = ((blockIdx.x - tile * blocks) * kConvThreads + tid) * 8;
   // threads behind the last channel stay: the lanes of a head exchange sums
   const bool on = c < a.channels;
   const uint16_t* x = a.x + (long long)s * a.x_token + c;
@@ -108,7 +138,12 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
     for (int j = 0; j < W - 1; ++j) last[j] = row(t0 - (W - 1) + j);
   }
 
-  float w[W][8], bias[8];
+  const int end = min(t0 + L, n);
+  // the next kUnroll inputs are on their way while the last ones are worked on
+  uint4 next[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) next[u] = t0 + u < end ? row(t0 + u) : none;
+  unsigned long long w[W][4], bias[4];  // pairs of channels
   {
     uint4 ws[W];
 #pragma unroll
@@ -120,51 +155,82 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[j][i] = f[i * W + j];
-    unpack8<BF16>(on && a.bias ? __ldg(reinterpret_cast<const uint4*>(a.bias + c)) : none, bias);
+      for (int i = 0; i < 4; ++i) w[j][i] = pair_of(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+    float g[8];
+    unpack8<BF16>(on && a.bias ? __ldg(reinterpret_cast<const uint4*>(a.bias + c)) : none, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = pair_of(g[2 * i], g[2 * i + 1]);
   }
-  const int end = min(t0 + L, n);
   const bool unit = c < a.unit_channels;  // the same for all lanes of a head
-  uint16_t* o = a.out + (long long)s * a.o_token + c;
+  const bool units = __any_sync(0xffffffffu, unit);
+  uint16_t* o = a.out + (long long)(s + t0) * a.o_token + c;
+  const uint16_t* ahead = x + (t0 + kUnroll) * a.x_token;
   for (int t = t0; t < end; t += kUnroll) {
     uint4 line[W - 1 + kUnroll];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) line[j] = last[j];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) line[W - 1 + u] = t + u < end ? row(t + u) : none;
-    float y[kUnroll][8];
+    for (int u = 0; u < kUnroll; ++u) {
+      line[W - 1 + u] = next[u];
+      next[u] = on && t + kUnroll + u < end && VQ3_IN(s + t + kUnroll + u, a.tokens, 5) ? __ldg(reinterpret_cast<const uint4*>(ahead)) : none;
+      ahead += a.x_token;
+    }
+    unsigned long long y[kUnroll][4];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[u][i] = bias[i];
+      for (int i = 0; i < 4; ++i) y[u][i] = bias[i];
 #pragma unroll
     for (int j = 0; j < W - 1 + kUnroll; ++j) {
       float f[8];
       unpack8<BF16>(line[j], f);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (j - u >= 0 && j - u < W)
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long x2 = pair_of(f[2 * i], f[2 * i + 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[u][i] = fmaf(w[j - u < 0 || j - u >= W ? 0 : j - u][i], f[i], y[u][i]);
+        for (int u = 0; u < kUnroll; ++u)
+          if (j - u >= 0 && j - u < W) y[u][i] = fma_two(w[j - u < 0 || j - u >= W ? 0 : j - u][i], x2, y[u][i]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) last[j] = line[kUnroll + j];
+    if (a.silu)
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float e0, e1;
+          split_pair(mul_two(y[u][i], pair_of(-1.4426950408889634f, -1.4426950408889634f)), e0, e1);
+          y[u][i] = mul_two(y[u][i], pair_of(rcp(1.f + ex2(e0)), rcp(1.f + ex2(e1))));
+        }
+    if (units) {
+      float sum[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        unsigned long long two = mul_two(y[u][0], y[u][0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) two = fma_two(y[u][i], y[u][i], two);
+        float odd;
+        split_pair(two, sum[u], odd);
+        sum[u] += odd;
+      }
+      for (int d = 1; d < a.head_chunks; d <<= 1)
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const float f = unit ? rsqrtf(sum[u] + a.eps) : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[u][i] = mul_two(y[u][i], pair_of(f, f));
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (t + u >= end) break;
-      if (a.silu)
+      float z[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[u][i] = __fdividef(y[u][i], 1.f + __expf(-y[u][i]));
-      if (a.unit_channels) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(y[u][i], y[u][i], sum);
-        for (int d = 1; d < a.head_chunks; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float f = unit ? rsqrtf(sum + a.eps) : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[u][i] *= f;
-      }
-      if (on && VQ3_IN(s + t + u, a.tokens, 4)) *reinterpret_cast<uint4*>(o + (t + u) * a.o_token) = pack8<BF16>(y[u]);
+      for (int i = 0; i < 4; ++i) split_pair(y[u][i], z[2 * i], z[2 * i + 1]);
+      if (on && t + u < end && VQ3_IN(s + t + u, a.tokens, 4)) *reinterpret_cast<uint4*>(o) = pack8<BF16>(z);
+      o += a.o_token;
     }
   }
 }
@@ -175,11 +241,14 @@ cudaError_t launch_width(const ConvArgs& a, bool bf16, cudaStream_t st) {
   // tokens of a tile: 4 to 32, the longest that still gives every SM 16 CTAs
   int shift = 2;
   while (shift < 5 && (long long)blocks * (a.tokens >> (shift + 1)) >= 16LL * device_sm_count()) ++shift;
-  const dim3 grid((unsigned)((a.tokens >> shift) + a.requests), (unsigned)blocks);
+  // a tile's blocks of channels side by side: whole rows are read and written at about the same time
+  const long long tiles = (long long)((a.tokens >> shift) + a.requests) * blocks;
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)tiles;
   if (bf16)
-    short_conv_kernel<W, true><<<grid, kConvThreads, 0, st>>>(a, shift);
+    short_conv_kernel<W, true><<<grid, kConvThreads, 0, st>>>(a, shift, blocks);
   else
-    short_conv_kernel<W, false><<<grid, kConvThreads, 0, st>>>(a, shift);
+    short_conv_kernel<W, false><<<grid, kConvThreads, 0, st>>>(a, shift, blocks);
   return cudaGetLastError();
 }
 
