@@ -15,13 +15,17 @@ struct DeltaRequest {
   float* out;                // or null: not written
 };
 
-__device__ __forceinline__ DeltaRequest delta_request(const DeltaArgs& a, int r, int h) {
-  DeltaRequest q;
+__device__ __forceinline__ int2 delta_request_rows(const DeltaArgs& a, int r) {  // the first and how many
   int s = __ldg(a.q_start + r), e = __ldg(a.q_start + r + 1);
   s = s < 0 ? 0 : (s > a.tokens ? a.tokens : s);
   e = e < s ? s : (e > a.tokens ? a.tokens : e);
-  q.first = s;
-  q.n = e - s;
+  return make_int2(s, e - s);
+}
+__device__ __forceinline__ DeltaRequest delta_request(const DeltaArgs& a, int r, int h) {
+  DeltaRequest q;
+  const int2 rows = delta_request_rows(a, r);
+  q.first = rows.x;
+  q.n = rows.y;
   const int in = a.slot_in ? __ldg(a.slot_in + r) : -1, out = a.slot_out ? __ldg(a.slot_out + r) : -1;
   const long long head = (long long)h * a.d_k * a.d_v;
   q.in = in >= 0 && in < a.slots ? a.states + in * a.state_slot + head : nullptr;

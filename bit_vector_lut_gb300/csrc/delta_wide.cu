@@ -68,7 +68,7 @@ struct Wide {
   // and factors; barriers
   static constexpr int kX1 = kF + 3 * kFBytes, kX2 = kX1 + 2048, kXO = kX2 + 4096, kRow = kXO + 2048, kMax = kRow + 1024, kBar = kMax + 256;
   static constexpr int kSmem = kBar + 512;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static_assert(kSmem + 1024 <= 227 * 1024, "shared memory per CTA");
 };
 
 // Barriers, in order.
@@ -112,14 +112,58 @@ __device__ __forceinline__ uint4 ld_shared4(uint32_t at) {
 constexpr int kTries = 200000;
 constexpr uint32_t kTryNs = 5000;
 constexpr int kPolls = 4000000;  // of the copying warp, with 100 ns between two
-__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns = kTryNs) {
+__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
       : "memory");
   return ok != 0;
+}
+
+__device__ __forceinline__ bool is_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
+// The request whose turn it is: by classes of length, a power of two each, the longest first, and by their places in a
+// class. The CTAs that come last are short ones then, and the SMs end together. More requests than threads come as
+// they are.
+__device__ __forceinline__ int request_in_turn(const DeltaArgs& a, int turn, int* s) {
+  if (a.requests == 1 || a.requests > kWideThreads) return turn;
+  const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+  const bool is = r < a.requests;
+  const int cls = is ? 32 - __clz(delta_request_rows(a, r).y) : 0;  // 0 .. 31
+  const auto before = [&](int& v) {  // v of the lanes before this one, summed; v with them
+    const int own = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
+    }
+    return v - own;
+  };
+  if (r < 32) s[r] = 0;
+  __syncthreads();
+  if (is) atomicAdd(s + cls, 1);
+  __syncthreads();
+  int upto = s[31 - lane];
+  const int longer = before(upto);
+  const int at = __ffs(__ballot_sync(0xffffffffu, upto > turn)) - 1;
+  const int place = turn - __shfl_sync(0xffffffffu, longer, at);  // in class 31 - at
+  const uint32_t peers = __ballot_sync(0xffffffffu, is && cls == 31 - at);
+  if (lane == 0) s[32 + warp] = __popc(peers);
+  __syncthreads();
+  int in_warp = lane < kWideThreads / 32 ? s[32 + lane] : 0;
+  const int in_front = __shfl_sync(0xffffffffu, before(in_warp), warp) + __popc(peers & ((1u << lane) - 1u));
+  if (is && cls == 31 - at && in_front == place) s[48] = r;
+  __syncthreads();
+  return s[48];
 }
 
 template <int DK, bool BF16>
@@ -130,7 +174,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, col0 = blockIdx.x * kCols;
-  const DeltaRequest rq = delta_request(a, blockIdx.z, h);
+  __shared__ int turns[64];
+  const DeltaRequest rq = delta_request(a, request_in_turn(a, blockIdx.z, turns), h);
   if (rq.n <= kStepMost) {
     using Steps = StepShared<DK / 16, 16, 32>;
     static_assert(sizeof(Steps) <= L::kSmem, "shared memory of the steps");
@@ -758,7 +803,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       }
       const int hq = h / a.group;
       int n_kq = 0, n_v = 0, n_kk = 0;  // begun
-      const auto done = [&](int i, int use) { return __all_sync(0xffffffffu, try_wait_for(bar(i), (uint32_t)(use & 1), 0)); };
+      const auto done = [&](int i, int use) { return __all_sync(0xffffffffu, is_done(bar(i), (uint32_t)(use & 1))); };
       // Each as soon as its place is free and its operands are there; the tries without any are bounded.
       for (int tries = 0; (n_kq < chunks || n_v < chunks || n_kk < chunks) && tries < kPolls && !*abort; ++tries) {
         if (n_kq < chunks && (n_kq < 3 || done(kbKQFree + n_kq % 3, n_kq / 3 - 1))) {
