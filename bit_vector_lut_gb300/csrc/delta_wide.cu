@@ -33,7 +33,9 @@ namespace {
 
 constexpr int kC = 64;           // tokens of a chunk
 constexpr int kCols = 128;       // columns of a CTA
-constexpr int kStepMost = 4;     // tokens up to which a request is stepped through
+// Tokens up to which a request is stepped through instead (16 requests of 48 heads, one request: 5 tokens 71, 10.5 us
+// against 85, 14.2; 6 tokens 80, 12.1 against 85, 14.2; 8 tokens 97, 14.7 against 86, 14.2).
+constexpr int kStepMost = 6;
 constexpr int kWideThreads = 512;
 constexpr int kRowWarp = 8, kInvWarp = 12, kIssueWarp = 14;
 // Registers per thread: 128 at launch; the state's warps take what the others give up.
@@ -71,7 +73,8 @@ struct Wide {
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory per CTA");
 };
 
-// Barriers, in order.
+// Barriers, in order. Who arrives at one for a later use has waited for something that every waiter of the use before
+// did behind its wait, so that a phase is neither filled by the next one's arrivals nor missed.
 enum {
   kbKQFull = 0,   // [3] K and Q copied
   kbKQ = 3,       // [3] as FP16
@@ -82,11 +85,12 @@ enum {
   kbTFree = 15,   // [2]
   kbM = 17,       // [2]
   kbMFree = 19,   // [2]
-  kbN = 21, kbKK,
-  kbS = 23,       // [4] S stored: half of d_k, half of that
-  kbXK = 27, kbR, kbU, kbXQ, kbW,
-  kbD = 32,       // [2]
-  kbO = 34, kbORead, kbDrain, kBars
+  kbN = 21,       // [2]
+  kbKK = 23,
+  kbS = 24,       // [4] S stored: half of d_k, half of that
+  kbXK = 28, kbR, kbU, kbXQ, kbW,
+  kbD = 33,       // [2]
+  kbO = 35, kbORead, kbDrain, kBars
 };
 
 struct DeltaMaps {
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
 
   if (tid < kBars) {
     // arrivals: a copy, a product's completion or a warp each
-    constexpr int n[kBars] = {1, 1, 1, 4, 4, 4, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 4, 1};
+    constexpr int n[kBars] = {1, 1, 1, 4, 4, 4, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 2, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 4, 1};
     mbar_init(bar(tid), KB == 1 && tid >= kbS && tid < kbS + 4 ? 8 : n[tid]);
     if (tid == 0) *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -547,7 +551,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         for (int j = 0; j < kC; j += 4) *reinterpret_cast<float4*>(rest + j) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
         f[L::kG] = gi;
       }
-      if (is_k && ch >= 2) wait(kbTFree + (ch & 1), (ch >> 1) - 1);
+      // (all four: an arrival at kbTM for this chunk must not count for the chunk before the last)
+      if (ch >= 2) wait(kbTFree + (ch & 1), (ch >> 1) - 1);
       wait(kbKK, ch);
       tc_after();
       float top = 0.f;
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         f[L::kFk + p] = gi * back;
         sync_threads(11, 64);
         f[L::kFw + p] = bk * rest[p];
-        arrive(kbN);
+        arrive(kbN + (ch & 1));
         arrive(kbTM + (ch & 1));
       } else {
         const Scale sc = scale_of(top);
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       float* const tops = reinterpret_cast<float*>(smem + L::kMax);
       constexpr int NS = L::NS;
       for (int ch = 0; ch < chunks; ++ch) {
-        wait(kbN, ch);
+        wait(kbN + (ch & 1), ch >> 1);
         float* const n = reinterpret_cast<float*>(smem + L::kT + (ch & 1) * L::kTBytes);
         // a 32 x 32 block of the diagonal; rows in pairs
         float2 x[16];
