@@ -52,6 +52,7 @@ int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* s
     return report_error(VQ3_EUNSUPPORTED, "%s: d_v=%d must be a multiple of 16 up to 4096", who, d.d_v);
   if (d.max_new < 0) return report_error(VQ3_EINVAL, "%s: max_new=%d", who, d.max_new);
   if (!std::isfinite(d.scale)) return report_error(VQ3_EINVAL, "%s: scale=%g", who, (double)d.scale);
+  if (!on(d.status, 4)) return report_error(VQ3_EALIGN, "%s: status must be 4-byte aligned", who);
   if (done) return report_ok();
   const long long state = (long long)d.v_heads * d.d_k * d.d_v;
   if (b.slots) {
@@ -95,6 +96,7 @@ int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* s
   a.alpha = d.alpha;
   a.beta = d.beta;
   a.states = d.states;
+  a.status = d.status;
   a.q_start = b.q_start;
   a.slot_in = b.slot_in;
   a.slot_out = b.slot_out;

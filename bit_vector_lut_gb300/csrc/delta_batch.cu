@@ -10,8 +10,9 @@
 // The ratios g_i / g_j are products a_(j+1) ... a_i, not quotients: a gate of zero ends a memory
 // without a division by zero.
 //
-// Two kernels, chosen on the host: delta_chunk_kernel for chunks of 8, 16 or 32 tokens on tensor
-// cores, delta_step_kernel for one or a few tokens, which streams the state once through registers.
+// Three kernels here, chosen on the host by the most new tokens of a request: delta_step_kernel (up to 3) streams the
+// state once through registers, delta_block_kernel (up to 32, or 24 of d_k = 256) takes 8 tokens at a time,
+// delta_chunk_kernel chunks of 32 of prompts with d_k = 256; prompts of d_k 64 and 128 are delta_wide_kernel's.
 #include "vq3_internal.h"
 
 namespace vq3 {
@@ -22,13 +23,13 @@ VQ3_BOUNDS_RECORD(delta_batch)
 namespace vq3 {
 namespace {
 
-// ---------------------------------------------------------------- chunks on tensor cores
+// ---------------------------------------------------------------- chunks of 32 tokens, d_k = 256
 //
 // A CTA takes one request, one value head and 64 of its columns and walks the chunks in order. Each of
 // its four consumer warps owns 16 columns for the whole call: S^T [16][d_k] stays in registers as the
 // accumulators of m16n8k16 tiles, which is also the A operand's layout of the next product S^T [K; Q]^T,
 // and R^T, U^T follow in the same way, so no state and no intermediate passes through shared memory.
-// Two producer warps take turns with the chunks: they copy K and Q, form T and M, which do not depend on
+// Three producer warps take turns with the chunks: they copy K and Q, form T and M, which do not depend on
 // the state, and hand them over through a ring of three stages (named barriers, no spinning).
 //
 // Numbers: the tensor cores multiply FP16. K and Q enter exactly (BF16 rows are brought to a largest
@@ -37,10 +38,12 @@ namespace {
 // so that neither part leaves FP16's range: some 22 bits. Where only the 16-bit output depends on
 // a product (Q S0, M U) and the type is BF16, hi alone is used: 11 bits under an output of 8.
 //
-// mma.sync and not tcgen05: at 64 columns (N) the latter takes 48 cycles for 128 x 64 x 16, so a chunk
-// of 64 tokens would take 1,900 cycles of products and three trips through tensor and shared memory
-// where these four warps take 3,000 and none.
-constexpr int kConsumers = 4, kProducers = 2, kStages = 3;
+// mma.sync: a state of 256 x 128 with its two parts, the chunk's products and [K; Q] K^T would take 768 of the 512
+// columns of tensor memory. (d_k = 128, which the wide kernel takes: 16 ragged prompts 415 us here, 321 us there; one
+// prompt of 8,192 tokens 648 us at 96 CTAs here, 695 us at 48 there.) Three producers, as many as stages: one prompt of
+// 1,024 tokens, 48 heads of 256 x 128, 139 us, with two 148 us: a chunk's T and M take a warp as long as two chunks of
+// the consumers.
+constexpr int kConsumers = 4, kProducers = 3, kStages = 3;
 constexpr int kChunkThreads = 32 * (kConsumers + kProducers);
 constexpr int kWarpCols = 16, kCtaCols = kWarpCols * kConsumers;
 // Named barriers: per stage and consumer warp "filled" (the warps do not wait for one another), per stage "free".
@@ -48,11 +51,11 @@ constexpr int kFullBar = 1, kEmptyBar = kFullBar + kStages * kConsumers;
 constexpr int kFullThreads = 64, kEmptyThreads = 32 * (kConsumers + 1);
 static_assert(kEmptyBar + kStages <= 16, "named barriers");
 
-template <int KS, int NN>
+constexpr int KS = 16, NN = 4;  // steps of 16 of d_k, blocks of 8 tokens
 struct Stage {
   static constexpr int DK = 16 * KS, C = 8 * NN;
   static constexpr int RS = DK + 8;                              // row of K and Q in halves: 16 bytes past 128
-  static constexpr int TS = NN == 4 ? 40 : (NN == 2 ? 24 : 8);   // row of T and M: ldmatrix without conflicts
+  static constexpr int TS = 40;                                  // row of T and M: ldmatrix without conflicts
   static constexpr int VS = kCtaCols + 8;                        // row of V
   static constexpr int kK = 0, kQ = kK + C * RS * 2, kV = kQ + C * RS * 2, kT = kV + C * VS * 2;
   static constexpr int NS = C + 4;                               // column of N in floats
@@ -93,18 +96,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
                : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ uint32_t ldsm1t(uint32_t at) {
-  uint32_t r;
-  asm volatile("ldmatrix.sync.aligned.m8n8.x1.trans.shared.b16 {%0}, [%1];" : "=r"(r) : "r"(at) : "memory");
-  return r;
-}
-__device__ __forceinline__ uint32_t ldsm1(uint32_t at) {
-  uint32_t r;
-  asm volatile("ldmatrix.sync.aligned.m8n8.x1.shared.b16 {%0}, [%1];" : "=r"(r) : "r"(at) : "memory");
-  return r;
-}
-
-// Rows g and g + 8 of NN accumulator tiles: the largest magnitude over the row (lanes of one g).
+// Rows g and g + 8 of NT accumulator tiles: the largest magnitude over the row (lanes of one g).
 template <int NT>
 __device__ __forceinline__ void row_max(const float (&x)[NT][4], float& m0, float& m1) {
   m0 = m1 = 0.f;
@@ -126,10 +118,10 @@ __device__ __forceinline__ void row_max(const float (&x)[NT][4], float& m0, floa
 // ratios and N are kept by columns (lane j's 16-byte stores and loads do not conflict), and the
 // substitution goes column by column: once x_m is known every later row takes its part, 31 - m
 // independent products, where row by row each x_m waits for a sum (2,000 -> 700 cycles at C = 32).
-template <int KS, int NN, bool BF16>
+template <bool BF16>
 __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& rq, int h, int col0, int t0,
                                         unsigned char* st, int lane) {
-  using L = Stage<KS, NN>;
+  using L = Stage;
   constexpr int C = L::C, RS = L::RS, DK = L::DK, TS = L::TS, NS = L::NS;
   const int nt = rq.n - t0 < C ? rq.n - t0 : C;
   const int g = lane >> 2, t = lane & 3;
@@ -141,20 +133,19 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
     al = __ldg(a.alpha + (long long)(rq.first + t0 + lane) * a.alpha_token + h);
     be = __ldg(a.beta + (long long)(rq.first + t0 + lane) * a.beta_token + h);
   }
-  // rows of K and Q, tokens past the last zero: a lane takes one 16-byte column of every RPI-th row
+  // rows of K and Q, tokens past the last zero: a lane takes one 16-byte column
   {
-    constexpr int CPR = DK / 8, RPI = 32 / CPR > 0 ? 32 / CPR : 1;
-    const int hq = h / a.group, r0 = lane / CPR, c = lane % CPR;
-    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + (rq.first + t0 + r0) * a.k_token + hq * a.k_head + c * 8;
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (rq.first + t0 + r0) * a.q_token + hq * a.q_head + c * 8;
-    const uint32_t off = (uint32_t)(r0 * RS + c * 8) * 2u;
+    static_assert(DK / 8 == 32, "a lane per column");
+    const int hq = h / a.group, c = lane;
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + (rq.first + t0) * a.k_token + hq * a.k_head + c * 8;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (rq.first + t0) * a.q_token + hq * a.q_head + c * 8;
+    const uint32_t off = (uint32_t)(c * 8) * 2u;
 #pragma unroll 2
-    for (int i = 0; i < C / RPI; ++i) {
-      const uint32_t at = off + (uint32_t)(i * RPI * RS) * 2u;
-      const int row = i * RPI + r0;
+    for (int row = 0; row < C; ++row) {
+      const uint32_t at = off + (uint32_t)(row * RS) * 2u;
       // bytes read: 16, or none past the last token (zeros are written)
       const int bytes = row < nt && VQ3_IN(rq.first + t0 + row, a.tokens, 1) ? 16 : 0;
-      const long long from = bytes ? i * RPI : -r0;  // an address inside the rows
+      const long long from = bytes ? row : 0;  // an address inside the rows
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sk + at), "l"(kp + from * a.k_token), "r"(bytes) : "memory");
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + at), "l"(qp + from * a.q_token), "r"(bytes) : "memory");
     }
@@ -174,7 +165,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
   }
   // ratios D[i][j] = a_(j+1) ... a_i (lane = j), the running product g_i, and g_C / g_j
   float* const f = reinterpret_cast<float*>(st + L::kC);
-  if (lane < C) f[L::kFv + lane] = al;
+  f[L::kFv + lane] = al;
   __syncwarp();
   float r = 1.f, gam = 1.f, gi = 1.f;
 #pragma unroll
@@ -189,7 +180,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
       r *= i + e > lane ? av[e] : 1.f;
       d[e] = r;
     }
-    if (lane < C) *reinterpret_cast<float4*>(ratio + lane * NS + i) = make_float4(d[0], d[1], d[2], d[3]);
+    *reinterpret_cast<float4*>(ratio + lane * NS + i) = make_float4(d[0], d[1], d[2], d[3]);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncwarp();
@@ -198,7 +189,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
   if constexpr (BF16) {
 #pragma unroll 1
     for (int m = 0; m < 2; ++m) {
-      if (lane < C) {
+      {
         uint4* row = reinterpret_cast<uint4*>(st + (m ? L::kQ : L::kK) + lane * RS * 2);
         __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll 4
@@ -310,7 +301,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
   for (int k = 0; k < C / 2; ++k) top = fmaxf(top, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
   const Scale ts = scale_of(top);
   __syncwarp();  // every lane has read N
-  if (lane < C) {  // column j of T as row j
+  {  // column j of T as row j
     uint4* thi = reinterpret_cast<uint4*>(st + L::kT + lane * TS * 2);
     uint4* tlo = reinterpret_cast<uint4*>(st + L::kT + (C + lane) * TS * 2);
 #pragma unroll
@@ -332,12 +323,12 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
 }
 
 // ---- consumer: one chunk against this warp's 16 columns; acc: S^T, row g column 2g, row g + 8 column 2g + 1
-template <int KS, int NN, bool BF16>
+template <bool BF16>
 __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int warp,
                                         int lane) {
-  using L = Stage<KS, NN>;
+  using L = Stage;
   constexpr int C = L::C, RS = L::RS, TS = L::TS;
-  constexpr int K2 = NN == 1 ? 1 : NN / 2;  // steps of 16 tokens (one of 8 for NN = 1)
+  constexpr int K2 = NN / 2;  // steps of 16 tokens
   const int g = lane >> 2, t = lane & 3;
   const uint32_t sk = smem_of(st + L::kK), sq = smem_of(st + L::kQ), sT = smem_of(st + L::kT), sM = smem_of(st + L::kM);
   const float* f = reinterpret_cast<const float*>(st + L::kC);
@@ -358,31 +349,21 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
       split2(acc[2 * s + p][0] * s0.to, acc[2 * s + p][1] * s0.to, hi[2 * p], lo[2 * p]);
       split2(acc[2 * s + p][2] * s1.to, acc[2 * s + p][3] * s1.to, hi[2 * p + 1], lo[2 * p + 1]);
     }
-    if constexpr (NN == 1) {
-      // matrices: K columns 0-7, 8-15 of the step, Q the same
-      uint32_t b[4];
-      ldsm4(b, (lane < 16 ? sk : sq) + (uint32_t)((lane & 7) * RS + 16 * s + ((lane >> 3) & 1) * 8) * 2u);
-      mma16(xk[0], hi, b[0], b[1]);
-      mma16(xq[0], hi, b[2], b[3]);
-      mma16(xk[0], lo, b[0], b[1]);
-      if constexpr (!BF16) mma16(xq[0], lo, b[2], b[3]);
-    } else {
 #pragma unroll
-      for (int n = 0; n < NN; n += 2) {
-        const uint32_t off = (uint32_t)((8 * n + (lane & 7) + (lane >> 4) * 8) * RS + 16 * s + ((lane >> 3) & 1) * 8) * 2u;
-        uint32_t b[4];
-        ldsm4(b, sk + off);
-        mma16(xk[n], hi, b[0], b[1]);
-        mma16(xk[n + 1], hi, b[2], b[3]);
-        mma16(xk[n], lo, b[0], b[1]);
-        mma16(xk[n + 1], lo, b[2], b[3]);
-        ldsm4(b, sq + off);
-        mma16(xq[n], hi, b[0], b[1]);
-        mma16(xq[n + 1], hi, b[2], b[3]);
-        if constexpr (!BF16) {
-          mma16(xq[n], lo, b[0], b[1]);
-          mma16(xq[n + 1], lo, b[2], b[3]);
-        }
+    for (int n = 0; n < NN; n += 2) {
+      const uint32_t off = (uint32_t)((8 * n + (lane & 7) + (lane >> 4) * 8) * RS + 16 * s + ((lane >> 3) & 1) * 8) * 2u;
+      uint32_t b[4];
+      ldsm4(b, sk + off);
+      mma16(xk[n], hi, b[0], b[1]);
+      mma16(xk[n + 1], hi, b[2], b[3]);
+      mma16(xk[n], lo, b[0], b[1]);
+      mma16(xk[n + 1], lo, b[2], b[3]);
+      ldsm4(b, sq + off);
+      mma16(xq[n], hi, b[0], b[1]);
+      mma16(xq[n + 1], hi, b[2], b[3]);
+      if constexpr (!BF16) {
+        mma16(xq[n], lo, b[0], b[1]);
+        mma16(xq[n + 1], lo, b[2], b[3]);
       }
     }
   }
@@ -416,25 +397,18 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
   for (int ks = 0; ks < K2; ++ks) {
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int p = 0; p < (NN == 1 ? 1 : 2); ++p) {
+    for (int p = 0; p < 2; ++p) {
       split2(xk[2 * ks + p][0] * r0.to, xk[2 * ks + p][1] * r0.to, hi[2 * p], lo[2 * p]);
       split2(xk[2 * ks + p][2] * r1.to, xk[2 * ks + p][3] * r1.to, hi[2 * p + 1], lo[2 * p + 1]);
     }
-    if constexpr (NN == 1) {
-      const uint32_t bh = ldsm1t(sT + (lane & 7) * TS * 2), bl = ldsm1t(sT + (C + (lane & 7)) * TS * 2);
-      mma8(u[0], hi, bh);
-      mma8(u[0], lo, bh);
-      mma8(u[0], hi, bl);
-    } else {
 #pragma unroll
-      for (int n = 2 * ks; n < NN; ++n) {
-        // matrices: tokens 0-7, 8-15 of the step (rows) at block n (columns), hi, then lo
-        uint32_t b[4];
-        ldsm4t(b, sT + (uint32_t)(((lane >> 4) * C + 16 * ks + (lane & 15)) * TS + 8 * n) * 2u);
-        mma16(u[n], hi, b[0], b[1]);
-        mma16(u[n], lo, b[0], b[1]);
-        mma16(u[n], hi, b[2], b[3]);
-      }
+    for (int n = 2 * ks; n < NN; ++n) {
+      // matrices: tokens 0-7, 8-15 of the step (rows) at block n (columns), hi, then lo
+      uint32_t b[4];
+      ldsm4t(b, sT + (uint32_t)(((lane >> 4) * C + 16 * ks + (lane & 15)) * TS + 8 * n) * 2u);
+      mma16(u[n], hi, b[0], b[1]);
+      mma16(u[n], lo, b[0], b[1]);
+      mma16(u[n], hi, b[2], b[3]);
     }
   }
 #pragma unroll
@@ -461,49 +435,31 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
 #pragma unroll
     for (int ks = 0; ks < K2; ++ks)
 #pragma unroll
-      for (int p = 0; p < (NN == 1 ? 1 : 2); ++p) {
+      for (int p = 0; p < 2; ++p) {
         split2(w[2 * ks + p][0] * w0.to, w[2 * ks + p][1] * w0.to, hi[ks][2 * p], lo[ks][2 * p]);
         split2(w[2 * ks + p][2] * w1.to, w[2 * ks + p][3] * w1.to, hi[ks][2 * p + 1], lo[ks][2 * p + 1]);
       }
     const float gC = f[L::kFg];
-    if constexpr (NN == 1) {
 #pragma unroll
-      for (int n = 0; n < 2 * KS; n += 4) {
-        uint32_t b[4];  // matrices: 8 tokens (rows) at d_k 8n, 8(n + 1), ...
-        ldsm4t(b, sk + (uint32_t)((lane & 7) * RS + 8 * n + (lane >> 3) * 8) * 2u);
+    for (int n = 0; n < 2 * KS; n += 2) {
+      float d[2][4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma8(d, hi[0], b[p]);
-          mma8(d, lo[0], b[p]);
-          acc[n + p][0] = fmaf(w0.back, d[0], gC * acc[n + p][0]);
-          acc[n + p][1] = fmaf(w0.back, d[1], gC * acc[n + p][1]);
-          acc[n + p][2] = fmaf(w1.back, d[2], gC * acc[n + p][2]);
-          acc[n + p][3] = fmaf(w1.back, d[3], gC * acc[n + p][3]);
-        }
+      for (int p = 0; p < 2; ++p) d[p][0] = d[p][1] = d[p][2] = d[p][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < K2; ++ks) {
+        uint32_t b[4];  // matrices: tokens 0-7, 8-15 of the step (rows) at d_k 8n, then at 8(n + 1)
+        ldsm4t(b, sk + (uint32_t)((16 * ks + (lane & 15)) * RS + 8 * n + (lane >> 4) * 8) * 2u);
+        mma16(d[0], hi[ks], b[0], b[1]);
+        mma16(d[1], hi[ks], b[2], b[3]);
+        mma16(d[0], lo[ks], b[0], b[1]);
+        mma16(d[1], lo[ks], b[2], b[3]);
       }
-    } else {
 #pragma unroll
-      for (int n = 0; n < 2 * KS; n += 2) {
-        float d[2][4];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) d[p][0] = d[p][1] = d[p][2] = d[p][3] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < K2; ++ks) {
-          uint32_t b[4];  // matrices: tokens 0-7, 8-15 of the step (rows) at d_k 8n, then at 8(n + 1)
-          ldsm4t(b, sk + (uint32_t)((16 * ks + (lane & 15)) * RS + 8 * n + (lane >> 4) * 8) * 2u);
-          mma16(d[0], hi[ks], b[0], b[1]);
-          mma16(d[1], hi[ks], b[2], b[3]);
-          mma16(d[0], lo[ks], b[0], b[1]);
-          mma16(d[1], lo[ks], b[2], b[3]);
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          acc[n + p][0] = fmaf(w0.back, d[p][0], gC * acc[n + p][0]);
-          acc[n + p][1] = fmaf(w0.back, d[p][1], gC * acc[n + p][1]);
-          acc[n + p][2] = fmaf(w1.back, d[p][2], gC * acc[n + p][2]);
-          acc[n + p][3] = fmaf(w1.back, d[p][3], gC * acc[n + p][3]);
-        }
+      for (int p = 0; p < 2; ++p) {
+        acc[n + p][0] = fmaf(w0.back, d[p][0], gC * acc[n + p][0]);
+        acc[n + p][1] = fmaf(w0.back, d[p][1], gC * acc[n + p][1]);
+        acc[n + p][2] = fmaf(w1.back, d[p][2], gC * acc[n + p][2]);
+        acc[n + p][3] = fmaf(w1.back, d[p][3], gC * acc[n + p][3]);
       }
     }
   }
@@ -516,28 +472,19 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
   for (int ks = 0; ks < K2; ++ks) {
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int p = 0; p < (NN == 1 ? 1 : 2); ++p) {
+    for (int p = 0; p < 2; ++p) {
       split2(u[2 * ks + p][0] * u0.to, u[2 * ks + p][1] * u0.to, hi[2 * p], lo[2 * p]);
       split2(u[2 * ks + p][2] * u1.to, u[2 * ks + p][3] * u1.to, hi[2 * p + 1], lo[2 * p + 1]);
     }
-    if constexpr (NN == 1) {
-      const uint32_t bh = ldsm1(sM + (lane & 7) * TS * 2);
-      mma8(o[0], hi, bh);
-      if constexpr (!BF16) {
-        mma8(o[0], lo, bh);
-        mma8(o[0], hi, ldsm1(sM + (C + (lane & 7)) * TS * 2));
-      }
-    } else {
 #pragma unroll
-      for (int n = 2 * ks; n < NN; ++n) {
-        // matrices: block n (rows) at tokens 0-7, 8-15 of the step, hi, then lo
-        uint32_t b[4];
-        ldsm4(b, sM + (uint32_t)((((BF16 ? 0 : lane >> 4)) * C + 8 * n + (lane & 7)) * TS + 16 * ks + ((lane >> 3) & 1) * 8) * 2u);
-        mma16(o[n], hi, b[0], b[1]);
-        if constexpr (!BF16) {
-          mma16(o[n], lo, b[0], b[1]);
-          mma16(o[n], hi, b[2], b[3]);
-        }
+    for (int n = 2 * ks; n < NN; ++n) {
+      // matrices: block n (rows) at tokens 0-7, 8-15 of the step, hi, then lo
+      uint32_t b[4];
+      ldsm4(b, sM + (uint32_t)((((BF16 ? 0 : lane >> 4)) * C + 8 * n + (lane & 7)) * TS + 16 * ks + ((lane >> 3) & 1) * 8) * 2u);
+      mma16(o[n], hi, b[0], b[1]);
+      if constexpr (!BF16) {
+        mma16(o[n], lo, b[0], b[1]);
+        mma16(o[n], hi, b[2], b[3]);
       }
     }
   }
@@ -552,9 +499,9 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
   }
 }
 
-template <int KS, int NN, bool BF16>
-__global__ void __launch_bounds__(kChunkThreads, KS > 8 ? 1 : (NN == 1 ? 3 : 2)) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
-  using L = Stage<KS, NN>;
+template <bool BF16>
+__global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
+  using L = Stage;
   constexpr int C = L::C;
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -566,7 +513,7 @@ __global__ void __launch_bounds__(kChunkThreads, KS > 8 ? 1 : (NN == 1 ? 3 : 2))
     for (int c = warp - kConsumers; c < chunks; c += kProducers) {
       const int s = c % kStages;
       if (c >= kStages) bar_sync(kEmptyBar + s, kEmptyThreads);  // the consumers are done with chunk c - kStages
-      produce<KS, NN, BF16>(a, rq, h, blockIdx.x * kCtaCols, c * C, smem + s * L::kBytes, lane);
+      produce<BF16>(a, rq, h, blockIdx.x * kCtaCols, c * C, smem + s * L::kBytes, lane);
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) bar_arrive(kFullBar + s * kConsumers + w, kFullThreads);
     }
@@ -595,7 +542,7 @@ __global__ void __launch_bounds__(kChunkThreads, KS > 8 ? 1 : (NN == 1 ? 3 : 2))
     const int s = c % kStages;
     bar_sync(kFullBar + s * kConsumers + warp, kFullThreads);
     float o[NN][4];
-    if (on) consume<KS, NN, BF16>(acc, smem + s * L::kBytes, o, warp, lane);
+    if (on) consume<BF16>(acc, smem + s * L::kBytes, o, warp, lane);
     if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kEmptyThreads);
     if (on) {
 #pragma unroll
@@ -619,16 +566,17 @@ __global__ void __launch_bounds__(kChunkThreads, KS > 8 ? 1 : (NN == 1 ? 3 : 2))
   }
 }
 
-template <int KS, int NN, bool BF16>
+template <bool BF16>
 cudaError_t launch_chunk(const DeltaArgs& a, cudaStream_t st) {
-  constexpr int smem = kStages * Stage<KS, NN>::kBytes;
+  constexpr int smem = kStages * Stage::kBytes;
   const cudaError_t e =
-      cudaFuncSetAttribute(delta_chunk_kernel<KS, NN, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(delta_chunk_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.d_v + kCtaCols - 1) / kCtaCols), (unsigned)a.v_heads, (unsigned)a.requests);
-  delta_chunk_kernel<KS, NN, BF16><<<grid, kChunkThreads, smem, st>>>(a);
+  delta_chunk_kernel<BF16><<<grid, kChunkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
+
 // ---------------------------------------------------------------- a few tokens
 //
 // Verify steps: blocks of 8 tokens, the mathematics and numbers of a chunk, but every warp by itself, with 16 columns of a
@@ -907,11 +855,11 @@ cudaError_t launch_step(const DeltaArgs& a, cudaStream_t st) {
 template <int DK, bool BF16>
 cudaError_t launch_of(const DeltaArgs& a, cudaStream_t st) {
   if (a.max_new > 0 && a.max_new <= kDeltaStepTokens) return launch_step<DK / kGroups, BF16>(a, st);
-  if (a.max_new > 0 && a.max_new <= kDeltaBlockTokens) return launch_block<DK, BF16>(a, st);
+  if (a.max_new > 0 && a.max_new <= (DK == 256 ? kDeltaBlockTokens256 : kDeltaBlockTokens)) return launch_block<DK, BF16>(a, st);
   if constexpr (DK <= 128)
     return launch_delta_wide(a, BF16, st);
   else
-    return launch_chunk<DK / 16, 4, BF16>(a, st);
+    return launch_chunk<BF16>(a, st);
 }
 template <bool BF16>
 cudaError_t launch_delta_type(const DeltaArgs& a, cudaStream_t st) {

@@ -85,7 +85,7 @@ class vq3_delta(ctypes.Structure):
                 ("out", c_void_p), ("beta", c_void_p), ("alpha", c_void_p), ("states", c_void_p),
                 ("q_token", c_longlong), ("q_head", c_longlong), ("k_token", c_longlong), ("k_head", c_longlong),
                 ("v_token", c_longlong), ("v_head", c_longlong), ("out_token", c_longlong), ("out_head", c_longlong),
-                ("beta_token", c_longlong), ("alpha_token", c_longlong), ("state_slot", c_longlong)]
+                ("beta_token", c_longlong), ("alpha_token", c_longlong), ("state_slot", c_longlong), ("status", c_void_p)]
 
 
 class vq3_conv(ctypes.Structure):
@@ -793,12 +793,13 @@ def _batch(index: int, tokens: int, slots: int, q_start, slot_in, slot_out) -> v
 def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, alpha: torch.Tensor,
                      states: torch.Tensor, q_start: torch.Tensor, slot_in: torch.Tensor | None = None,
                      slot_out: torch.Tensor | None = None, max_new: int = 0, scale: float = 1.0,
-                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                     out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gated delta rule over packed requests (vq3_delta_rule_batch): q, k [tokens, qk_heads, d_k], v [tokens,
     v_heads, d_v] FP16 or BF16 (slices of one buffer, for instance), beta, alpha [tokens, v_heads] FP32, `states`
     [slots, v_heads, d_k, d_v] FP32. Request r has rows q_start[r] .. q_start[r + 1] - 1, goes on from slot
     slot_in[r] (negative, or slot_in None: from zeros) and leaves its state in slot_out[r] (negative, or None: nowhere).
-    max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it where it is known."""
+    max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it where it is known.
+    status: an int32 tensor [1] that becomes 3 if a wait inside the call gave up (its results are invalid then)."""
     index, dtype = v.get_device(), v.dtype
     qs, vs, ss = q.shape, v.shape, states.shape
     if dtype not in TYPES or len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or q.dtype is not dtype or \
@@ -813,11 +814,13 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
     if states.dtype is not _FLOAT or len(ss) != 4 or ss[1:] != (heads, d_k, d_v) or states.get_device() != index or \
             states.stride()[1:] != (d_k * d_v, d_v, 1):
         raise Vq3Error(-1, "states must be float32 [slots, v_heads, d_k, d_v], contiguous within a slot")
+    if status is not None and not (_ints_ok(index, status) and status.numel() == 1):
+        raise Vq3Error(-1, "status must be an int32 tensor [1] on the inputs' device")
     batch = _batch(index, tokens, ss[0], q_start, slot_in, slot_out)
     if out is None:
         if _elsewhere(index, stream):
             with _at(index, stream):
-                out = delta_rule_batch(q, k, v, beta, alpha, states, q_start, slot_in, slot_out, max_new, scale)
+                out = delta_rule_batch(q, k, v, beta, alpha, states, q_start, slot_in, slot_out, max_new, scale, status=status)
             _handed_out(index, stream, out)
             return out
         out = _empty(vs, dtype=dtype, device=v.device)
@@ -828,7 +831,7 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
         raise Vq3Error(-1, "the last axis of q, k, v and out must be contiguous")
     d = vq3_delta(TYPES[dtype], qs[1], heads, d_k, d_v, max_new, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                   out.data_ptr(), beta.data_ptr(), alpha.data_ptr(), states.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh,
-                  beta.stride(0), alpha.stride(0), states.stride(0))
+                  beta.stride(0), alpha.stride(0), states.stride(0), _ptr(status))
     _launch(index, stream, lib.vq3_delta_rule_batch, ctypes.byref(batch), ctypes.byref(d))
     return out
 

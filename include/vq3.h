@@ -505,9 +505,10 @@ typedef struct vq3_batch {
  * h / (v_heads / qk_heads),
  *   S <- alpha[t][h] S + beta[t][h] k_t (v_t - alpha[t][h] S^T k_t)^T,   out_t = scale S^T q_t.
  * States, sums and gates are FP32 (products with 22 bits of the state at least), out is rounded once. alpha may
- * be 0 (the state starts over). Rows outside the requests are neither read nor written. All lengths live in
- * device memory. max_new picks the kernel (1 or 2: one that streams the states; 8, 16: short chunks; above or
- * 0: chunks of 32 tokens); a wrong value costs time, not correctness. Deterministic, no workspace, one launch.
+ * be 0 (the state starts over). Rows outside the requests count for nothing and are left as they are. All lengths
+ * live in device memory. max_new picks the kernel (up to 3: one that streams the states token by token; up to 32, or 24
+ * of d_k = 256: blocks of 8 tokens; above or 0: prompts by chunks, the shortest requests token by token); a wrong value
+ * costs time, not correctness. Deterministic, no workspace, one launch.
  * d_k 64, 128 or 256; d_v a multiple of 16 up to 4096. Strides as in the attention calls; alpha and beta have
  * their heads side by side. out and states overlap no other buffer.
  * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
@@ -531,6 +532,7 @@ typedef struct vq3_delta {
   long long v_token, v_head, out_token, out_head;
   long long beta_token, alpha_token;
   long long state_slot;  /* a multiple of 4 */
+  int* status;           /* device word or NULL: 3 if a wait inside the call gave up, else left as it is */
 } vq3_delta;
 VQ3_API int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* stream);
 

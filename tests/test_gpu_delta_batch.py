@@ -1,5 +1,5 @@
 """The delta rule over packed requests on the GPU against the float64 recurrence, elementwise within the bound of
-oracle/mixers.py: every kernel and chunk length, states in slots, ragged and empty requests, strides, gates at
+oracle/mixers.py: every kernel, states in slots, ragged and empty requests, strides, gates at
 their limits."""
 
 import numpy as np
@@ -100,7 +100,7 @@ class Case:
         assert (got[: self.starts[0]] == 7).all() and (got[self.starts[-1]:] == 7).all()
 
 
-HINTS = [0, 1, 8, 16]  # chunks of 32, single tokens, chunks of 8, of 16
+HINTS = [0, 1, 8, 16]  # prompts, single tokens, blocks of 8 tokens (twice)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])

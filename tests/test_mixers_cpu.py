@@ -62,7 +62,8 @@ def test_batch_is_checked(bad, code):
     (dict(q=P + 8), ALIGN), (dict(v=P + 2), ALIGN), (dict(out=P + 4), ALIGN), (dict(states=P + 8), ALIGN), (dict(alpha=P + 2), ALIGN),
     (dict(q_token=32), INVALID), (dict(k_head=68), ALIGN), (dict(v_head=0), INVALID), (dict(out_token=-128), INVALID),
     (dict(out_token=40), INVALID), (dict(out=P), INVALID), (dict(out=3 * P), INVALID), (dict(alpha_token=3), INVALID),
-    (dict(beta_token=0), INVALID), (dict(state_slot=4 * 64 * 32 - 4), INVALID), (dict(state_slot=4 * 64 * 32 + 2), ALIGN)])
+    (dict(beta_token=0), INVALID), (dict(state_slot=4 * 64 * 32 - 4), INVALID), (dict(state_slot=4 * 64 * 32 + 2), ALIGN),
+    (dict(status=P + 2), ALIGN)])
 def test_delta_refuses(bad, code):
     assert delta(**bad) == code, vq3.lib.vq3_last_error()
 
@@ -127,6 +128,8 @@ def test_binding_refuses_before_the_library():
         lambda: vq3.delta_rule_batch(q, q, v, g, g, s, st, slot_in=st),           # slots of another batch
         lambda: vq3.delta_rule_batch(q, q, v, g, g, s, st, slot_out=sl.long()),
         lambda: vq3.delta_rule_batch(q, q, v, g, g, s, st, out=v[:2]),
+        lambda: vq3.delta_rule_batch(q, q, v, g, g, s, st, status=sl),
+        lambda: vq3.delta_rule_batch(q, q, v, g, g, s, st, status=st[:1].long()),
         lambda: vq3.delta_rule_batch(q.transpose(0, 2), q.transpose(0, 2), v, g, g, s, st),
         lambda: vq3.short_conv(x, w, cs, st),
         lambda: vq3.short_conv(x, w[:32], cs, st),
@@ -154,7 +157,7 @@ def test_binding_refuses_before_the_library():
     assert f is torch.float32
 
 
-@pytest.mark.parametrize("src", ["delta_batch.cu", "conv.cu", "rotary.cu"])
+@pytest.mark.parametrize("src", ["delta_batch.cu", "delta_wide.cu", "conv.cu", "rotary.cu"])
 def test_bounds_check_variant_compiles(tmp_path, src):
     from bit_vector_lut_gb300 import build as B
     r = subprocess.run([B.nvcc(), *B.ARCH, *B.NVCC_FLAGS, "-DVQ3_BOUNDS_CHECK", "-c", os.path.join(B.CSRC, src), "-o",
