@@ -5,7 +5,10 @@
 // A thread takes 8 channels and up to L tokens of one request, the last W - 1 inputs in registers. Tiles begin
 // at a request's first token, and L >= W - 1, so that only a request's first tile reads its slot; that tile's
 // threads write the new state, too, behind their own reads, and the slot read and the slot written may be the
-// same. Bound by HBM: an input is read by its own tile and, from L2, by the next one (3 rows of L).
+// same. Bound by HBM: an input is read by its own tile and, from L2, by the next one (3 rows of L). What it took: the
+// next inputs on their way while four tokens are worked on (104 -> 86 us for 8,921 tokens x 10,240 channels of 4, FP16),
+// SiLU by ex2 and rcp of some 2^-22 under an output of 2^-11 (80), whole rows of channels at about the same time (79.6),
+// the sums of four tokens exchanged together and two channels an instruction (66: 5.5 TB/s, 82% of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -16,7 +19,6 @@ VQ3_BOUNDS_RECORD(conv)
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kUnroll = 4;  // tokens whose loads are in flight together
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
@@ -82,11 +84,23 @@ __device__ __forceinline__ int start_of(const ConvArgs& a, int r) {
 
 // Tile i of the launch: request r's tiles begin at index first_r / L + r, which leaves room for all of them
 // (ceil(n / L) <= (first + n) / L - first / L + 1), whatever the lengths are.
-template <int W, bool BF16>
-__global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __grid_constant__ ConvArgs a, int shift,
+// U: tokens worked on, and fetched, together.
+template <int W, int U, bool BF16>
+__global__ void __launch_bounds__(kConvThreads, U == 1 ? 6 : 4) short_conv_kernel(const __grid_constant__ ConvArgs a, int shift,
                                                                    int blocks) {
   __shared__ int counts[kConvThreads / 32];
   const int tile = blockIdx.x / blocks, tid = threadIdx.x, L = 1 << shift;
+  const int c = ((blockIdx.x - tile * blocks) * kConvThreads + tid) * 8;
+  // threads behind the last channel stay: the lanes of a head exchange sums
+  const bool on = c < a.channels;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 ws[W], bs = none;
+  const auto weights = [&] {
+#pragma unroll
+    for (int j = 0; j < W; ++j) ws[j] = on ? __ldg(reinterpret_cast<const uint4*>(a.weight + (long long)c * W) + j) : none;
+    if (on && a.bias) bs = __ldg(reinterpret_cast<const uint4*>(a.bias + c));
+  };
+  if constexpr (U == 1) weights();  // under the search for the request
   int before = 0;  // requests whose tiles begin at or before this one
   for (int i = tid; i < a.requests; i += kConvThreads) before += (start_of(a, i) >> shift) + i <= tile;
   before = __reduce_add_sync(0xffffffffu, before);
@@ -99,56 +113,45 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
   const int s = start_of(a, r), e = max(s, start_of(a, r + 1)), n = e - s;
   const int t0 = (tile - (s >> shift) - r) << shift;  // from the request's first token
   if (t0 < 0 || (t0 >= n && t0 > 0)) return;
-  const int c = ((blockIdx.x - tile * blocks) * kConvThreads + tid) * 8;
-  // threads behind the last channel stay: the lanes of a head exchange sums
-  const bool on = c < a.channels;
   const uint16_t* x = a.x + (long long)s * a.x_token + c;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
   const auto row = [&](int t) {
     return on && VQ3_IN(s + t, a.tokens, 1) ? __ldg(reinterpret_cast<const uint4*>(x + t * a.x_token)) : none;
   };
 
+  const int in = t0 == 0 && a.slot_in ? __ldg(a.slot_in + r) : -1, out = t0 == 0 && a.slot_out ? __ldg(a.slot_out + r) : -1;
+  const int end = min(t0 + L, n);
+  // the next inputs are on their way while the last ones are worked on
+  uint4 next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next[u] = t0 + u < end ? row(t0 + u) : none;
   uint4 last[W - 1];  // the inputs before t0
-  if (t0 == 0) {
-    const int in = a.slot_in ? __ldg(a.slot_in + r) : -1, out = a.slot_out ? __ldg(a.slot_out + r) : -1;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    last[j] = none;
+    if (t0)
+      last[j] = row(t0 - (W - 1) + j);
+    else if (on && in >= 0 && in < a.slots && VQ3_IN(c + 7, a.channels, 2))
+      last[j] = *reinterpret_cast<const uint4*>(a.states + in * a.state_slot + j * a.state_row + c);
+  }
+  if (on && out >= 0 && out < a.slots && (n || out != in)) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      last[j] = none;
-      if (on && in >= 0 && in < a.slots && VQ3_IN(c + 7, a.channels, 2))
-        last[j] = *reinterpret_cast<const uint4*>(a.states + in * a.state_slot + j * a.state_row + c);
-    }
-    if (on && out >= 0 && out < a.slots && (n || out != in)) {
+      // input n + j of the line (old state, new tokens)
+      uint4 w = none;
+      if (n + j >= W - 1) {
+        w = row(n + j - (W - 1));
+      } else {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        // input n + j of the line (old state, new tokens)
-        uint4 w = none;
-        if (n + j >= W - 1) {
-          w = row(n + j - (W - 1));
-        } else {
-#pragma unroll
-          for (int i = j; i < W - 1; ++i)
-            if (n + j == i) w = last[i];
-        }
-        if (VQ3_IN(c + 7, a.channels, 3)) *reinterpret_cast<uint4*>(a.states + out * a.state_slot + j * a.state_row + c) = w;
+        for (int i = j; i < W - 1; ++i)
+          if (n + j == i) w = last[i];
       }
+      if (VQ3_IN(c + 7, a.channels, 3)) *reinterpret_cast<uint4*>(a.states + out * a.state_slot + j * a.state_row + c) = w;
     }
-    if (n == 0) return;
-  } else {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) last[j] = row(t0 - (W - 1) + j);
   }
-
-  const int end = min(t0 + L, n);
-  // the next kUnroll inputs are on their way while the last ones are worked on
-  uint4 next[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) next[u] = t0 + u < end ? row(t0 + u) : none;
+  if (n == 0) return;
+  if constexpr (U > 1) weights();
   unsigned long long w[W][4], bias[4];  // pairs of channels
   {
-    uint4 ws[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      ws[j] = on ? __ldg(reinterpret_cast<const uint4*>(a.weight + (long long)c * W) + j) : none;
     float f[W * 8];
 #pragma unroll
     for (int j = 0; j < W; ++j) unpack8<BF16>(ws[j], reinterpret_cast<float(&)[8]>(f[8 * j]));
@@ -157,46 +160,46 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[j][i] = pair_of(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
     float g[8];
-    unpack8<BF16>(on && a.bias ? __ldg(reinterpret_cast<const uint4*>(a.bias + c)) : none, g);
+    unpack8<BF16>(bs, g);
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = pair_of(g[2 * i], g[2 * i + 1]);
   }
   const bool unit = c < a.unit_channels;  // the same for all lanes of a head
   const bool units = __any_sync(0xffffffffu, unit);
   uint16_t* o = a.out + (long long)(s + t0) * a.o_token + c;
-  const uint16_t* ahead = x + (t0 + kUnroll) * a.x_token;
-  for (int t = t0; t < end; t += kUnroll) {
-    uint4 line[W - 1 + kUnroll];
+  const uint16_t* ahead = x + (t0 + U) * a.x_token;
+  for (int t = t0; t < end; t += U) {
+    uint4 line[W - 1 + U];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) line[j] = last[j];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       line[W - 1 + u] = next[u];
-      next[u] = on && t + kUnroll + u < end && VQ3_IN(s + t + kUnroll + u, a.tokens, 5) ? __ldg(reinterpret_cast<const uint4*>(ahead)) : none;
+      next[u] = on && t + U + u < end && VQ3_IN(s + t + U + u, a.tokens, 5) ? __ldg(reinterpret_cast<const uint4*>(ahead)) : none;
       ahead += a.x_token;
     }
-    unsigned long long y[kUnroll][4];
+    unsigned long long y[U][4];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[u][i] = bias[i];
 #pragma unroll
-    for (int j = 0; j < W - 1 + kUnroll; ++j) {
+    for (int j = 0; j < W - 1 + U; ++j) {
       float f[8];
       unpack8<BF16>(line[j], f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const unsigned long long x2 = pair_of(f[2 * i], f[2 * i + 1]);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < U; ++u)
           if (j - u >= 0 && j - u < W) y[u][i] = fma_two(w[j - u < 0 || j - u >= W ? 0 : j - u][i], x2, y[u][i]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) last[j] = line[kUnroll + j];
+    for (int j = 0; j < W - 1; ++j) last[j] = line[U + j];
     if (a.silu)
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float e0, e1;
@@ -204,9 +207,9 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
           y[u][i] = mul_two(y[u][i], pair_of(rcp(1.f + ex2(e0)), rcp(1.f + ex2(e1))));
         }
     if (units) {
-      float sum[kUnroll];
+      float sum[U];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         unsigned long long two = mul_two(y[u][0], y[u][0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) two = fma_two(y[u][i], y[u][i], two);
@@ -216,16 +219,16 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
       }
       for (int d = 1; d < a.head_chunks; d <<= 1)
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+        for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         const float f = unit ? rsqrtf(sum[u] + a.eps) : 1.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[u][i] = mul_two(y[u][i], pair_of(f, f));
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       float z[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) split_pair(y[u][i], z[2 * i], z[2 * i + 1]);
@@ -238,17 +241,21 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
 template <int W>
 cudaError_t launch_width(const ConvArgs& a, bool bf16, cudaStream_t st) {
   const int blocks = (a.channels / 8 + kConvThreads - 1) / kConvThreads;
-  // tokens of a tile: 4 to 32, the longest that still gives every SM 16 CTAs
+  // Tokens of a tile: 4 to 32, the most that still give every SM 4 CTAs, 32 where they give it 8. Tiles of 4 | 8 | 16 |
+  // 32 tokens at 10,240 channels, us: 512 tokens 7.4 | 6.7 | 7.2 | 9.8, 1,024 tokens 14.0 | 11.5 | 11.3 | 14.9, 2,048
+  // tokens 25.3 | 20.5 | 19.1 | 20.5, 8,960 tokens 100 | 77 | 69 | 67.
   int shift = 2;
-  while (shift < 5 && (long long)blocks * (a.tokens >> (shift + 1)) >= 16LL * device_sm_count()) ++shift;
+  while (shift < 5 && (long long)blocks * (a.tokens >> (shift + 1)) >= (shift < 4 ? 4LL : 8LL) * device_sm_count()) ++shift;
   // a tile's blocks of channels side by side: whole rows are read and written at about the same time
   const long long tiles = (long long)((a.tokens >> shift) + a.requests) * blocks;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)tiles;
-  if (bf16)
-    short_conv_kernel<W, true><<<grid, kConvThreads, 0, st>>>(a, shift, blocks);
+  // One token at a time where there is hardly more than one a request: 64 users' tokens of 10,240 channels 5.9 -> 4.1 us.
+  const auto run = [&](auto* kernel) { kernel<<<grid, kConvThreads, 0, st>>>(a, shift, blocks); };
+  if (a.tokens <= a.requests)
+    run(bf16 ? short_conv_kernel<W, 1, true> : short_conv_kernel<W, 1, false>);
   else
-    short_conv_kernel<W, false><<<grid, kConvThreads, 0, st>>>(a, shift, blocks);
+    run(bf16 ? short_conv_kernel<W, 4, true> : short_conv_kernel<W, 4, false>);
   return cudaGetLastError();
 }
 

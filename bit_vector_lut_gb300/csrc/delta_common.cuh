@@ -104,7 +104,8 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // GROUPS groups of LANES lanes; a lane holds 4 columns of every GROUPS-th row of S in registers. With x = S^T k and
 // y = S^T q of the OLD state both products need one pass over it and one exchange between the groups:
 //     u = b (v - a x),   S <- a S + k u^T,   o = scale (a y + (k . q) u).
-// All in FP32. Bound by the state's bytes, read once and written once.
+// All in FP32. Bound by the state's bytes, read once and written once: 64 users' single tokens, 48 heads of 128 x 128,
+// 60.5 us (99% of a copy's rate).
 template <int ROWS, int GROUPS, int LANES>
 struct StepShared {
   static constexpr int kWarps = GROUPS * LANES / 32;

@@ -8,7 +8,7 @@
 //
 // A CTA takes kTile tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
 // the heads' items: 2 x 16 bytes a thread, both partners of 8 pairs, so that a row may be turned in place. Bound by
-// HBM.
+// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 66 us (88% of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(kRotThreads) kv_append_rotary_kernel(const __g
 template <bool BF16>
 cudaError_t launch_type(const RotaryArgs& a, cudaStream_t st) {
   const int n = a.kv.tokens;
-  if (n < 16 * device_sm_count())
+  // a token | 4 tokens a CTA, 32 + 8 heads of 128, us: 64 tokens 3.2 | 5.2, 1,200 tokens 7.6 | 8.4, 2,400 tokens 14.4 |
+  // 13.6
+  if (n < 12 * device_sm_count())
     kv_append_rotary_kernel<1, BF16><<<n, kRotThreads, 0, st>>>(a);
   else
     kv_append_rotary_kernel<4, BF16><<<(n + 3) / 4, kRotThreads, 0, st>>>(a);
