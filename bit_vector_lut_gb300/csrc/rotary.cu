@@ -6,9 +6,9 @@
 // Angles: freq / (2 pi) as a 64-bit fraction of a turn (from FP64), times the position modulo one turn in integers:
 // exact for any position, where an FP32 product is off by whole radians from some 10^7 on (by 2^-8 radians at 10^5).
 //
-// A CTA takes kTile tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
+// A CTA takes 4 tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
 // the heads' items: 2 x 16 bytes a thread, both partners of 8 pairs, so that a row may be turned in place. Bound by
-// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 66 us (88% of a copy's rate).
+// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 67 us (87% of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -70,45 +70,50 @@ __global__ void __launch_bounds__(kRotThreads) kv_append_rotary_kernel(const __g
     table[t][f] = make_float2(c, s);
   }
   __syncthreads();
-  const int item_shift = kv.chunk_shift - 1;  // items of a head: pairs of 16-byte chunks
-  const int per_token = (a.heads + 2 * kv.kv_heads) << item_shift;
-  const int pairs = a.half >> 3;
-#pragma unroll 2
-  for (int i = tid; i < TILE * per_token; i += kRotThreads) {
-    const int t = TILE == 1 ? 0 : i / per_token;
-    const int u = i - t * per_token, unit = u >> item_shift, p = u - (unit << item_shift);
-    if (pos[t] < 0) continue;
-    const int tok = t0 + t;
+  // An item is both chunks of 8 pairs of a head; a thread takes the same one of many heads, so that it reads the table
+  // once. Items of a head side by side, then heads.
+  const int item_shift = kv.chunk_shift - 1, items = tid >> item_shift;
+  const int p = tid & ((1 << item_shift) - 1), step = (kRotThreads / TILE) >> item_shift, t = items / step;
+  const int units = a.heads + 2 * kv.kv_heads, tok = t0 + t;
+  if (pos[t] < 0 || !VQ3_IN(tok, kv.tokens, 1)) return;
+  const bool turns_here = p < a.half >> 3, apart = turns_here && !a.interleaved;
+  float4 cs[4];  // (c0, s0, c1, s1), ...
+  if (turns_here)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[e] = reinterpret_cast<const float4*>(&table[t][8 * p])[e];
+  const long long sl = slot[t], page = sl >> kv.page_shift, in = sl & ((1 << kv.page_shift) - 1);
+  const bool kept = sl >= 0 && sl < limit && VQ3_IN(page, kv.n_pages, 2);
+  // both chunks: halves half apart where the rotation pairs them so, neighbours otherwise (values are never turned)
+  const int d0 = apart ? 8 * p : 16 * p, d1 = apart ? a.half + 8 * p : 16 * p + 8;
+  struct Item {
+    uint4 x, y;
+    uint16_t *to, *to2;
+  };
+  const auto fetch = [&](int unit, Item& it) {
+    it.to = nullptr;
     const uint16_t* src;
-    uint16_t* dst;
-    bool ok = VQ3_IN(tok, kv.tokens, 1), turn = p < pairs;
+    bool value = false;
     if (unit < a.heads) {
       src = a.q + tok * a.q_token + unit * a.q_head;
-      dst = a.q_out + tok * a.o_token + unit * a.o_head;
-    } else {
-      const long long sl = slot[t];
-      if (sl < 0 || sl >= limit) continue;
-      const long long page = sl >> kv.page_shift, in = sl & ((1 << kv.page_shift) - 1);
-      ok = ok && VQ3_IN(page, kv.n_pages, 2);
-      const int h = unit - a.heads;
-      if (h < kv.kv_heads) {
-        src = kv.k_rows + tok * kv.k_row + h * kv.k_row_head;
-        dst = kv.k_pages + page * kv.k_page + in * kv.k_token + h * kv.k_head;
-      } else {
-        const int hv = h - kv.kv_heads;
-        src = kv.v_rows + tok * kv.v_row + hv * kv.v_row_head;
-        dst = kv.v_pages + page * kv.v_page + in * kv.v_token + hv * kv.v_head;
-        turn = false;
-      }
+      it.to = a.q_out + tok * a.o_token + unit * a.o_head;
+    } else if (kept && unit < units) {
+      const int h = unit - a.heads, hv = h - kv.kv_heads;
+      value = hv >= 0;
+      src = value ? kv.v_rows + tok * kv.v_row + hv * kv.v_row_head : kv.k_rows + tok * kv.k_row + h * kv.k_row_head;
+      it.to = value ? kv.v_pages + page * kv.v_page + in * kv.v_token + hv * kv.v_head
+                    : kv.k_pages + page * kv.k_page + in * kv.k_token + h * kv.k_head;
     }
-    if (!ok) continue;
-    // both chunks: halves half apart where the rotation pairs them so, neighbours otherwise
-    const bool apart = turn && !a.interleaved;
-    const int d0 = apart ? 8 * p : 16 * p, d1 = apart ? a.half + 8 * p : 16 * p + 8;
-    uint4 x = ldg_once(src + d0), y = ldg_once(src + d1);
-    if (turn) {
-      const float4* cs = reinterpret_cast<const float4*>(&table[t][8 * p]);  // (c0, s0, c1, s1), ...
-      uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    if (!it.to) return;
+    const int a0 = value ? 16 * p : d0, a1 = value ? 16 * p + 8 : d1;
+    it.x = ldg_once(src + a0);
+    it.y = ldg_once(src + a1);
+    it.to2 = it.to + a1;
+    it.to += a0;
+  };
+  const auto finish = [&](int unit, Item& it) {
+    if (!it.to) return;
+    if (turns_here && unit < a.heads + kv.kv_heads) {
+      uint32_t xs[4] = {it.x.x, it.x.y, it.x.z, it.x.w}, ys[4] = {it.y.x, it.y.y, it.y.z, it.y.w};
       if (a.interleaved) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -127,20 +132,28 @@ __global__ void __launch_bounds__(kRotThreads) kv_append_rotary_kernel(const __g
           ys[e] = pack2<BF16>(w.x * c.x + v.x * c.y, w.y * c.z + v.y * c.w);
         }
       }
-      x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-      y = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+      it.x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+      it.y = make_uint4(ys[0], ys[1], ys[2], ys[3]);
     }
-    *reinterpret_cast<uint4*>(dst + d0) = x;
-    *reinterpret_cast<uint4*>(dst + d1) = y;
+    *reinterpret_cast<uint4*>(it.to) = it.x;
+    *reinterpret_cast<uint4*>(it.to2) = it.y;
+  };
+  constexpr int kInFlight = 2;
+  for (int unit = items - t * step; unit < units; unit += kInFlight * step) {
+    Item it[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) fetch(unit + u * step, it[u]);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) finish(unit + u * step, it[u]);
   }
 }
 
 template <bool BF16>
 cudaError_t launch_type(const RotaryArgs& a, cudaStream_t st) {
   const int n = a.kv.tokens;
-  // a token | 4 tokens a CTA, 32 + 8 heads of 128, us: 64 tokens 3.2 | 5.2, 1,200 tokens 7.6 | 8.4, 2,400 tokens 14.4 |
-  // 13.6
-  if (n < 12 * device_sm_count())
+  // a token | 4 tokens a CTA, 32 + 8 heads of 128, us: 64 tokens 2.8 | 4.0, 256 tokens 3.3 | 4.0, 600 tokens 4.6 | 4.4,
+  // 1,200 tokens 8.1 | 6.3, some 16,000 tokens 86 | 67
+  if (n < 3 * device_sm_count())
     kv_append_rotary_kernel<1, BF16><<<n, kRotThreads, 0, st>>>(a);
   else
     kv_append_rotary_kernel<4, BF16><<<(n + 3) / 4, kRotThreads, 0, st>>>(a);
