@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint8, c_void_p
 from typing import NamedTuple
 
@@ -95,6 +96,23 @@ class vq3_conv(ctypes.Structure):
                 ("state_slot", c_longlong), ("state_row", c_longlong)]
 
 
+def _packer(cls):
+    """Makes the bytes of a structure, in half the time of the structure itself."""
+    letters = {c_int: "i", c_float: "f", c_void_p: "P", c_longlong: "q"}
+    form = struct.Struct("@" + "".join(letters[t] for _, t in cls._fields_))
+    assert form.size == ctypes.sizeof(cls)
+
+    def pack(*values):
+        try:
+            return form.pack(*values)
+        except struct.error as e:  # a number that its field does not hold
+            raise Vq3Error(-1, f"{cls.__name__}: {e}") from None
+
+    return pack
+
+
+_pack_batch, _pack_delta, _pack_conv, _pack_rotary = (_packer(c) for c in (vq3_batch, vq3_delta, vq3_conv, vq3_rotary))
+
 # VQ3_TYPE_* in vq3.h
 TYPES = {torch.float16: 0, torch.bfloat16: 1}
 
@@ -143,10 +161,10 @@ def _load() -> ctypes.CDLL:
         "vq3_paged_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_cache), c_void_p, c_int, c_void_p, c_void_p,
                                         c_size_t, c_void_p]),
         "vq3_prompt_attention": (c_int, [POINTER(vq3_attn), POINTER(vq3_kv_rows), c_void_p, c_size_t, c_void_p]),
-        "vq3_kv_append_rotary": (c_int, [POINTER(vq3_rotary), POINTER(vq3_kv_rows), c_void_p, POINTER(vq3_kv_cache),
-                                         c_void_p]),
-        "vq3_delta_rule_batch": (c_int, [POINTER(vq3_batch), POINTER(vq3_delta), c_void_p]),
-        "vq3_short_conv": (c_int, [POINTER(vq3_batch), POINTER(vq3_conv), c_void_p]),
+        # vq3_rotary, vq3_batch, vq3_delta and vq3_conv come as their bytes or by reference
+        "vq3_kv_append_rotary": (c_int, [c_void_p, POINTER(vq3_kv_rows), c_void_p, POINTER(vq3_kv_cache), c_void_p]),
+        "vq3_delta_rule_batch": (c_int, [c_void_p, c_void_p, c_void_p]),
+        "vq3_short_conv": (c_int, [c_void_p, c_void_p, c_void_p]),
         "vq3_last_error": (ctypes.c_char_p, []),
         "vq3_version": (ctypes.c_char_p, []),
         "vq3_bounds_check": (c_int, [POINTER(ctypes.c_uint), c_int, c_int]),
@@ -670,7 +688,7 @@ def kv_append_rotary(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, p
         raise Vq3Error(-1, "slots (int64) and positions (int32) must be contiguous with an entry per row")
     if freq.dtype is not _FLOAT or not freq.is_contiguous() or freq.get_device() != index:
         raise Vq3Error(-1, "freq must be a contiguous float32 tensor on the rows' device")
-    rot = vq3_rotary(TYPES[dtype], 0, 2 * freq.numel(), bool(interleaved), freq.data_ptr(), positions.data_ptr())
+    heads = qp = op = q_token = q_head = out_token = out_head = 0
     if q is None:
         if q_out is not None:
             raise Vq3Error(-1, "q_out without q")
@@ -688,13 +706,14 @@ def kv_append_rotary(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, p
             q_out = _empty(shape, dtype=dtype, device=q.device)
         elif q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != index:
             raise Vq3Error(-1, "q_out must be like q")
-        rot.heads, rot.q, rot.q_out = shape[1], q.data_ptr(), q_out.data_ptr()
-        rot.q_token, rot.q_head, qd = q.stride()
-        rot.out_token, rot.out_head, od = q_out.stride()
+        heads, qp, op = shape[1], q.data_ptr(), q_out.data_ptr()
+        q_token, q_head, qd = q.stride()
+        out_token, out_head, od = q_out.stride()
         if qd != 1 or od != 1:
             raise Vq3Error(-1, "the head_dim axis of q and q_out must be contiguous")
-    _launch(index, stream, lib.vq3_kv_append_rotary, ctypes.byref(rot), ctypes.byref(rows), slots.data_ptr(),
-            ctypes.byref(cache))
+    rot = _pack_rotary(TYPES[dtype], heads, 2 * freq.numel(), bool(interleaved), freq.data_ptr(), positions.data_ptr(), qp,
+                       op, q_token, q_head, out_token, out_head)
+    _launch(index, stream, lib.vq3_kv_append_rotary, rot, ctypes.byref(rows), slots.data_ptr(), ctypes.byref(cache))
     return q_out
 
 
@@ -780,14 +799,15 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start:
 
 # ---------------------------------------------------------------- the delta rule for packed requests
 
-def _batch(index: int, tokens: int, slots: int, q_start, slot_in, slot_out) -> vq3_batch:
+def _batch(index: int, tokens: int, slots: int, q_start, slot_in, slot_out) -> bytes:
     if not _ints_ok(index, q_start) or q_start.numel() < 1:
         raise Vq3Error(-1, "q_start must be a contiguous int32 tensor [requests + 1] on the inputs' device")
     requests = q_start.numel() - 1
-    for s in (slot_in, slot_out):
+    for s in (slot_in,) if slot_in is slot_out else (slot_in, slot_out):
         if s is not None and not (_ints_ok(index, s) and s.numel() == requests):
             raise Vq3Error(-1, "slot_in and slot_out must be contiguous int32 tensors [requests] on the inputs' device")
-    return vq3_batch(tokens, requests, slots, q_start.data_ptr(), _ptr(slot_in), _ptr(slot_out))
+    return _pack_batch(tokens, requests, slots, q_start.data_ptr(), 0 if slot_in is None else slot_in.data_ptr(),
+                       0 if slot_out is None else slot_out.data_ptr())
 
 
 def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, alpha: torch.Tensor,
@@ -801,18 +821,19 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
     max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it where it is known.
     status: an int32 tensor [1] that becomes 3 if a wait inside the call gave up (its results are invalid then)."""
     index, dtype = v.get_device(), v.dtype
-    qs, vs, ss = q.shape, v.shape, states.shape
+    qs, vs = q.shape, v.shape
     if dtype not in TYPES or len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or q.dtype is not dtype or \
             k.dtype is not dtype or q.get_device() != index or k.get_device() != index:
         raise Vq3Error(-1, "q and k [tokens, qk_heads, d_k] and v [tokens, v_heads, d_v] must be FP16 or BF16 tensors of "
                            "one type and device")
     tokens, heads, d_v = vs
-    d_k = qs[2]
+    qk_heads, d_k = qs[1], qs[2]
     for g in (beta, alpha):
-        if g.shape != vs[:2] or g.dtype is not _FLOAT or g.get_device() != index or (heads > 1 and g.stride(1) != 1):
+        if g.shape != (tokens, heads) or g.dtype is not _FLOAT or g.get_device() != index or (heads > 1 and g.stride(1) != 1):
             raise Vq3Error(-1, "beta and alpha must be float32 [tokens, v_heads], the heads side by side")
-    if states.dtype is not _FLOAT or len(ss) != 4 or ss[1:] != (heads, d_k, d_v) or states.get_device() != index or \
-            states.stride()[1:] != (d_k * d_v, d_v, 1):
+    ss, st = states.shape, states.stride()
+    if states.dtype is not _FLOAT or len(ss) != 4 or ss[1] != heads or ss[2] != d_k or ss[3] != d_v or \
+            states.get_device() != index or st[1] != d_k * d_v or st[2] != d_v or st[3] != 1:
         raise Vq3Error(-1, "states must be float32 [slots, v_heads, d_k, d_v], contiguous within a slot")
     if status is not None and not (_ints_ok(index, status) and status.numel() == 1):
         raise Vq3Error(-1, "status must be an int32 tensor [1] on the inputs' device")
@@ -829,10 +850,10 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
     (qt, qh, qd), (kt, kh, kd), (vt, vh, vd), (ot, oh, od) = q.stride(), k.stride(), v.stride(), out.stride()
     if qd != 1 or kd != 1 or vd != 1 or od != 1:
         raise Vq3Error(-1, "the last axis of q, k, v and out must be contiguous")
-    d = vq3_delta(TYPES[dtype], qs[1], heads, d_k, d_v, max_new, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                  out.data_ptr(), beta.data_ptr(), alpha.data_ptr(), states.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh,
-                  beta.stride(0), alpha.stride(0), states.stride(0), _ptr(status))
-    _launch(index, stream, lib.vq3_delta_rule_batch, ctypes.byref(batch), ctypes.byref(d))
+    d = _pack_delta(TYPES[dtype], qk_heads, heads, d_k, d_v, max_new, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    out.data_ptr(), beta.data_ptr(), alpha.data_ptr(), states.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh,
+                    beta.stride(0), alpha.stride(0), st[0], 0 if status is None else status.data_ptr())
+    _launch(index, stream, lib.vq3_delta_rule_batch, batch, d)
     return out
 
 
@@ -844,19 +865,21 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, states: torch.Tensor, q_st
     width], bias [channels] or None, `states` [slots, width - 1, channels] (the last inputs), all of one type; slots as
     in delta_rule_batch. The first unit_heads heads of head_dim channels come out with unit length."""
     index, dtype, xs = x.get_device(), x.dtype, x.shape
-    if dtype not in TYPES or len(xs) != 2 or weight.dim() != 2 or weight.shape[0] != xs[1] or weight.dtype is not dtype \
+    ws, ss = weight.shape, states.shape
+    if dtype not in TYPES or len(xs) != 2 or len(ws) != 2 or ws[0] != xs[1] or weight.dtype is not dtype \
             or not weight.is_contiguous() or weight.get_device() != index:
         raise Vq3Error(-1, "x [tokens, channels] and weight [channels, width] must be FP16 or BF16 tensors of one type and "
                            "device, weight contiguous")
     tokens, channels = xs
-    width = weight.shape[1]
+    width = ws[1]
     if bias is not None and (bias.shape != (channels,) or bias.dtype is not dtype or not bias.is_contiguous()
                              or bias.get_device() != index):
         raise Vq3Error(-1, "bias must be a contiguous tensor [channels] of x's type and device")
-    if states.dim() != 3 or states.shape[1:] != (width - 1, channels) or states.dtype is not dtype or \
-            states.get_device() != index or states.stride(2) != 1:
+    st = states.stride()
+    if len(ss) != 3 or ss[1] != width - 1 or ss[2] != channels or states.dtype is not dtype or \
+            states.get_device() != index or st[2] != 1:
         raise Vq3Error(-1, "states must be [slots, width - 1, channels] of x's type and device")
-    batch = _batch(index, tokens, states.shape[0], q_start, slot_in, slot_out)
+    batch = _batch(index, tokens, ss[0], q_start, slot_in, slot_out)
     if out is None:
         if _elsewhere(index, stream):
             with _at(index, stream):
@@ -870,7 +893,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, states: torch.Tensor, q_st
     ot, oc = out.stride()
     if xc != 1 or oc != 1:
         raise Vq3Error(-1, "the channels of x and out must be contiguous")
-    c = vq3_conv(TYPES[dtype], channels, width, bool(silu), unit_heads, head_dim, eps, x.data_ptr(), weight.data_ptr(),
-                 _ptr(bias), states.data_ptr(), out.data_ptr(), xt, ot, states.stride(0), states.stride(1))
-    _launch(index, stream, lib.vq3_short_conv, ctypes.byref(batch), ctypes.byref(c))
+    c = _pack_conv(TYPES[dtype], channels, width, bool(silu), unit_heads, head_dim, eps, x.data_ptr(), weight.data_ptr(),
+                   0 if bias is None else bias.data_ptr(), states.data_ptr(), out.data_ptr(), xt, ot, st[0], st[1])
+    _launch(index, stream, lib.vq3_short_conv, batch, c)
     return out

@@ -157,6 +157,15 @@ def test_binding_refuses_before_the_library():
     assert f is torch.float32
 
 
+def test_packed_structures_are_the_structures():
+    for cls, pack in ((vq3.vq3_batch, vq3._pack_batch), (vq3.vq3_delta, vq3._pack_delta), (vq3.vq3_conv, vq3._pack_conv),
+                      (vq3.vq3_rotary, vq3._pack_rotary)):
+        values = [1.5 if t is ctypes.c_float else 3 + i for i, (_, t) in enumerate(cls._fields_)]
+        assert pack(*values) == bytes(cls(*values))
+        with pytest.raises(vq3.Vq3Error):
+            pack(1 << 40, *values[1:])
+
+
 @pytest.mark.parametrize("src", ["delta_batch.cu", "delta_wide.cu", "conv.cu", "rotary.cu"])
 def test_bounds_check_variant_compiles(tmp_path, src):
     from bit_vector_lut_gb300 import build as B
