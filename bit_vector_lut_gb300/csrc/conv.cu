@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kConvThreads, U == 1 ? 6 : 4) short_conv_kerne
     for (int j = 0; j < W; ++j) ws[j] = on ? __ldg(reinterpret_cast<const uint4*>(a.weight + (long long)c * W) + j) : none;
     if (on && a.bias) bs = __ldg(reinterpret_cast<const uint4*>(a.bias + c));
   };
-  if constexpr (U == 1) weights();  // under the search for the request
+  if constexpr (U == 1)
+    if (a.tokens) weights();  // under the search for the request; without rows there may be none
   int before = 0;  // requests whose tiles begin at or before this one
   for (int i = tid; i < a.requests; i += kConvThreads) before += (start_of(a, i) >> shift) + i <= tile;
   before = __reduce_add_sync(0xffffffffu, before);

@@ -856,7 +856,8 @@ cudaError_t launch_step(const DeltaArgs& a, cudaStream_t st) {
 
 template <int DK, bool BF16>
 cudaError_t launch_of(const DeltaArgs& a, cudaStream_t st) {
-  if (a.max_new > 0 && a.max_new <= kDeltaStepTokens) return launch_step<DK / kGroups, BF16>(a, st);
+  // (without rows states are copied at most, and there is nothing for a tensor map to describe)
+  if (!a.tokens || (a.max_new > 0 && a.max_new <= kDeltaStepTokens)) return launch_step<DK / kGroups, BF16>(a, st);
   if (a.max_new > 0 && a.max_new <= (DK == 256 ? kDeltaBlockTokens256 : kDeltaBlockTokens)) return launch_block<DK, BF16>(a, st);
   if constexpr (DK <= 128)
     return launch_delta_wide(a, BF16, st);

@@ -12,6 +12,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests.mixers_workloads import odd_starts  # noqa: E402
+from tests.test_gpu_conv_rotary import Conv  # noqa: E402
 from tests.test_gpu_delta_batch import DEV, DT, Case, f64, ints, vq3  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +131,28 @@ def test_status_word_stays(vq3, hint):  # noqa: F811
         out, states = c.run(vq3, hint, status=status)
         c.check(out, states)
         assert status.item() == was
+
+
+@pytest.mark.parametrize("dk", [64, 128, 256])
+@pytest.mark.parametrize("hint", [0, 1, 8])
+def test_requests_without_any_row(vq3, dk, hint):  # noqa: F811
+    # states go from slot to slot, or become zeros
+    c = Case(51, [0, 0, 0], 1, 2, dk, 32, behind=0)
+    ins = [c.slot_in[0], -1, c.slot_in[2]]
+    out, states = c.run(vq3, hint, ins)
+    c.check(out, states, slot_in=ins)
+
+
+def test_conv_without_any_row(vq3):  # noqa: F811
+    import ctypes
+    c = Conv(52, [0, 0], 64, 4, behind=0)
+    ins = [c.slot_in[0], -1]
+    out, states = c.run(vq3, ins)
+    c.check(out, states, slot_in=ins)
+    # and with null inputs, which the header allows without rows
+    states, starts, slots = c.states.to(DEV).clone(), ints([0, 0, 0]), (ints(ins), ints(c.slot_out))
+    b = vq3.vq3_batch(0, 2, len(states), starts.data_ptr(), slots[0].data_ptr(), slots[1].data_ptr())
+    d = vq3.vq3_conv(0, 64, 4, 1, 0, 0, 1e-6, None, None, None, states.data_ptr(), None, 64, 64, 192, 64)
+    assert vq3.lib.vq3_short_conv(ctypes.byref(b), ctypes.byref(d), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    c.check(out, states, slot_in=ins)
