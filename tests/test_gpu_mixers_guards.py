@@ -12,7 +12,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests.mixers_workloads import odd_starts  # noqa: E402
-from tests.test_gpu_conv_rotary import Conv  # noqa: E402
+from tests.test_gpu_conv_rotary import Conv, Rotary  # noqa: E402
 from tests.test_gpu_delta_batch import DEV, DT, Case, f64, ints, vq3  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +156,58 @@ def test_conv_without_any_row(vq3):  # noqa: F811
     assert vq3.lib.vq3_short_conv(ctypes.byref(b), ctypes.byref(d), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     c.check(out, states, slot_in=ins)
+
+
+@pytest.mark.parametrize("hint", [0, 1, 8])
+def test_states_past_32_bits(vq3, hint):  # noqa: F811
+    # slots 2^31 floats into the pool, 9 GB
+    c = Case(53, [70, 3], 1, 2, 128, 128, "bf16")
+    pool = torch.empty(70000, 2, 128, 128, device=DEV)
+    ins, outs = [69999, 66000], [65999, 69990]
+    for r in range(2):
+        pool[ins[r]] = c.states[c.slot_in[r]].to(DEV)
+    out = torch.full(c.v.shape, 7.0, dtype=DT["bf16"], device=DEV)
+    vq3.delta_rule_batch(*(x.to(DEV) for x in (c.q, c.k, c.v, c.beta, c.alpha)), pool, c.q_start, ints(ins), ints(outs),
+                         max_new=hint, scale=c.scale, out=out)
+    torch.cuda.synchronize()
+    states = c.states.to(DEV).clone()
+    for r in range(2):
+        states[c.slot_out[r]] = pool[outs[r]]
+    c.check(out, states)
+
+
+def test_rows_past_32_bits(vq3):  # noqa: F811
+    # rows of a buffer whose tokens lie 2^26 entries apart, the last ones 2^32 into it
+    c = Case(54, [70], 1, 1, 64, 64, "f16", behind=0)
+    far = torch.empty(70 << 26, dtype=torch.float16, device=DEV)
+    view = [far.as_strided((70, 1, 64), (1 << 26, 64, 1), 64 * i) for i in range(4)]
+    for x, y in zip(view, (c.q, c.k, c.v)):
+        x.copy_(y.to(DEV))
+    view[3].fill_(7.0)
+    for hint in (0, 1, 8):
+        states = c.states.to(DEV).clone()
+        vq3.delta_rule_batch(*view[:3], c.beta.to(DEV), c.alpha.to(DEV), states, c.q_start, ints(c.slot_in), ints(c.slot_out),
+                             max_new=hint, scale=c.scale, out=view[3])
+        torch.cuda.synchronize()
+        c.check(view[3], states)
+    w = Conv(55, [70], 64, 4, behind=0)
+    view[0].copy_(w.x.to(DEV).unflatten(1, (1, 64)))
+    states = w.states.to(DEV).clone()
+    vq3.short_conv(view[0][:, 0], w.w.to(DEV), states, ints(w.starts), ints(w.slot_in), ints(w.slot_out), out=view[1][:, 0])
+    torch.cuda.synchronize()
+    w.check(view[1][:, 0], states)
+
+
+def test_cache_past_32_bits(vq3):  # noqa: F811
+    # pages 2^32 entries into the cache, 9 GB a side
+    c = Rotary(56, [5, 77, 4095], 3, 2, 128, 64, 16, "bf16")
+    pools = [torch.empty(1 << 20, 16, 2, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    small, slots = c.pages, c.slots
+    far = [(1 << 20) * 16 - 1 - s for s in slots]
+    c.pages, c.slots = pools, far
+    got = c.run(vq3)
+    for s, p in zip(small, pools):
+        for a, b in zip(slots, far):
+            s[a // 16, a % 16] = p[b // 16, b % 16]
+    c.pages, c.slots = small, slots
+    c.check(got)
