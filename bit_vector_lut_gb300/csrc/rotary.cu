@@ -8,7 +8,7 @@
 //
 // A CTA takes 4 tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
 // the heads' items: 2 x 16 bytes a thread, both partners of 8 pairs, so that a row may be turned in place. Bound by
-// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 67 us (87% of a copy's rate).
+// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 64 us (91% of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 ldg_once(const uint16_t* p) {
 }
 
 template <int TILE, bool BF16>
-__global__ void __launch_bounds__(kRotThreads) kv_append_rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 4) kv_append_rotary_kernel(const __grid_constant__ RotaryArgs a) {
   __shared__ unsigned long long turns[128];
   __shared__ float2 table[TILE][128];  // (cos, sin)
   __shared__ int pos[TILE];
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kRotThreads) kv_append_rotary_kernel(const __g
 template <bool BF16>
 cudaError_t launch_type(const RotaryArgs& a, cudaStream_t st) {
   const int n = a.kv.tokens;
-  // a token | 4 tokens a CTA, 32 + 8 heads of 128, us: 64 tokens 2.8 | 4.0, 256 tokens 3.3 | 4.0, 600 tokens 4.6 | 4.4,
-  // 1,200 tokens 8.1 | 6.3, some 16,000 tokens 86 | 67
-  if (n < 3 * device_sm_count())
+  // a token | 4 tokens a CTA, 32 + 8 heads of 128, us: 64 tokens 2.8 | 4.0, 256 tokens 3.3 | 4.0, 600 tokens 4.6 | 4.7,
+  // 1,200 tokens 8.1 | 6.6, some 16,000 tokens 86 | 64 (with three CTAs an SM instead of four 67, with five 73)
+  if (n < 5 * device_sm_count())
     kv_append_rotary_kernel<1, BF16><<<n, kRotThreads, 0, st>>>(a);
   else
     kv_append_rotary_kernel<4, BF16><<<(n + 3) / 4, kRotThreads, 0, st>>>(a);

@@ -222,7 +222,7 @@ def test_rotary_forms(vq3, dtype, interleaved, dim, rotated):  # noqa: F811
 @pytest.mark.parametrize("heads,kv_heads", [(1, 1), (5, 1), (24, 4), (7, 7), (2, 3)])
 @pytest.mark.parametrize("T", [1, 3, 100, 2500])
 def test_rotary_heads_and_tokens(vq3, heads, kv_heads, T):  # noqa: F811
-    # 2,500 tokens are above what a CTA a token takes (3 per SM)
+    # 2,500 tokens are above what a CTA a token takes (5 per SM)
     c = Rotary(2, [(i * 37) % 5000 if i % 10 else -1 for i in range(T)], heads, kv_heads, 64, 32, 32, "bf16", layout="hnd")
     got, live = c.check(c.run(vq3))
     assert (got[~live] == 7).all()
