@@ -579,15 +579,16 @@ cudaError_t launch_chunk(const DeltaArgs& a, cudaStream_t st) {
 
 // ---------------------------------------------------------------- a few tokens
 //
-// Verify steps: blocks of 8 tokens, the mathematics and numbers of a chunk, but every warp by itself, with 16 columns of a
-// head's state in registers and no barrier: bound by the state's bytes, it lives from many warps that each wait for
+// Verify steps: blocks of 8 tokens, the mathematics and numbers of a chunk, but every warp by itself, with 16 columns of
+// a head's state in registers and no barrier: bound by the state's bytes, it lives from many warps that each wait for
 // their own loads. K and Q are loaded as the B operand of S^T [K; Q]^T, which is also both operands of [K; Q] K^T and,
 // transposed by movmatrix, K's part of the state's product. The order of d_k within a product is free: a lane loads 16
-// bytes of a row, two pairs of entries for each of two steps, and the state's rows follow (block_row). N goes through 64 floats of shared memory to lanes that
-// each solve for a column of T. 16 requests x 8 tokens, 48 heads of 128 x 128: 27.3 us (57% of a copy's rate), some 1,800 instructions a warp at three
-// warps a scheduler; 28.8 us as chunks of 8 whose T and M two warps made for four; 29.0 us with four warps a scheduler,
-// which spill; 27.0 us, but 5.0 instead of 4.6 for one request, with the next task's state on its way into shared
-// memory; 41 us in FP32 on CUDA cores, bound by the reads of k and q from shared memory.
+// bytes of a row, two pairs of entries for each of two steps, and the state's rows follow (block_row). N goes through
+// 64 floats of shared memory to lanes that each solve for a column of T. 16 requests x 8 tokens, 48 heads of 128 x 128:
+// 27.2 us (57% of a copy's rate), some 1,500 instructions a warp at three warps a scheduler; 28.8 us as chunks of 8 whose
+// T and M two warps made for four; 29.0 us with four warps a scheduler, which spill; 27.0 us, but 5.0 instead of 4.6 for
+// one request, with the next task's state on its way into shared memory; 41 us in FP32 on CUDA cores, bound by the reads
+// of k and q from shared memory.
 constexpr int kBlockTokens = 8, kBlockThreads = 128;
 
 template <bool BF16>
