@@ -35,8 +35,8 @@ namespace {
 // Numbers: the tensor cores multiply FP16. K and Q enter exactly (BF16 rows are brought to a largest
 // entry of 2^8 by a power of two, which the factors of the token take back). Every FP32 operand (S, R, U,
 // T, M) enters as two FP16 parts, hi and what hi leaves, scaled by a power of two per row of the product
-// so that neither part leaves FP16's range: some 22 bits. Where only the 16-bit output depends on
-// a product (Q S0, M U) and the type is BF16, hi alone is used: 11 bits under an output of 8.
+// so that neither part leaves FP16's range: some 22 bits, for either type: a BF16 output made from hi
+// alone (11 bits) may be rounded the other way (one prompt of 8,192 tokens: 670 us instead of 720).
 //
 // mma.sync: a state of 256 x 128 with its two parts, the chunk's products and [K; Q] K^T would take 768 of the 512
 // columns of tensor memory. (d_k = 128, which the wide kernel takes: 16 ragged prompts 415 us here, 321 us there; one
@@ -276,7 +276,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
       uint32_t hi = 0u, lo = 0u;
       if (n <= b) split2(m[n][0] * s.to, m[n][1] * s.to, hi, lo);
       *reinterpret_cast<uint32_t*>(mhi + (8 * b + g) * TS + 8 * n + 2 * t) = hi;
-      if constexpr (!BF16) *reinterpret_cast<uint32_t*>(mlo + (8 * b + g) * TS + 8 * n + 2 * t) = lo;
+      *reinterpret_cast<uint32_t*>(mlo + (8 * b + g) * TS + 8 * n + 2 * t) = lo;
     }
     const float back = __shfl_sync(0xffffffffu, s.back, (lane & 7) * 4);  // of row 8 b + lane % 8
     if (lane >> 3 == b) fm = back;
@@ -361,10 +361,8 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
       ldsm4(b, sq + off);
       mma16(xq[n], hi, b[0], b[1]);
       mma16(xq[n + 1], hi, b[2], b[3]);
-      if constexpr (!BF16) {
-        mma16(xq[n], lo, b[0], b[1]);
-        mma16(xq[n + 1], lo, b[2], b[3]);
-      }
+      mma16(xq[n], lo, b[0], b[1]);
+      mma16(xq[n + 1], lo, b[2], b[3]);
     }
   }
 #pragma unroll
@@ -480,12 +478,10 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     for (int n = 2 * ks; n < NN; ++n) {
       // matrices: block n (rows) at tokens 0-7, 8-15 of the step, hi, then lo
       uint32_t b[4];
-      ldsm4(b, sM + (uint32_t)((((BF16 ? 0 : lane >> 4)) * C + 8 * n + (lane & 7)) * TS + 16 * ks + ((lane >> 3) & 1) * 8) * 2u);
+      ldsm4(b, sM + (uint32_t)(((lane >> 4) * C + 8 * n + (lane & 7)) * TS + 16 * ks + ((lane >> 3) & 1) * 8) * 2u);
       mma16(o[n], hi, b[0], b[1]);
-      if constexpr (!BF16) {
-        mma16(o[n], lo, b[0], b[1]);
-        mma16(o[n], hi, b[2], b[3]);
-      }
+      mma16(o[n], lo, b[0], b[1]);
+      mma16(o[n], hi, b[2], b[3]);
     }
   }
 #pragma unroll
@@ -753,7 +749,7 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
       mma16(xk[0], hi, kf[2 * s], kf[2 * s + 1]);
       mma16(xq, hi, qf[2 * s], qf[2 * s + 1]);
       mma16(xk[0], lo, kf[2 * s], kf[2 * s + 1]);
-      if constexpr (!BF16) mma16(xq, lo, qf[2 * s], qf[2 * s + 1]);
+      mma16(xq, lo, qf[2 * s], qf[2 * s + 1]);
     }
     // R^T, U^T
     {
@@ -784,10 +780,8 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
       split2(u[0][2] * u1.to, u[0][3] * u1.to, hi[1], lo[1]);
       float o[4] = {0.f, 0.f, 0.f, 0.f};
       mma8(o, hi, mh);
-      if constexpr (!BF16) {
-        mma8(o, lo, mh);
-        mma8(o, hi, ml);
-      }
+      mma8(o, lo, mh);
+      mma8(o, hi, ml);
       const float f0 = a.scale * qb0, f1 = a.scale * qb1;
       uint16_t* op = static_cast<uint16_t*>(a.out) + row0 * a.o_token + h * a.o_head + col;
       if (2 * t < nt && VQ3_IN(row0 + 2 * t, a.tokens, 14))

@@ -20,7 +20,7 @@
 // what comes out and leaves 17 bits of FP16's range below it.
 // Bound by that chain and by the row warps, which are both busy some 10,400 cycles a chunk, a third of them waiting for
 // products of 50 to 70 cycles for 128 x 64 x 16 (32 where they have the SM to themselves): 5.3 us a chunk of 64 tokens,
-// 0.67 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.32 ms for 16 of 1 to 1,100 tokens.
+// 0.72 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.32 ms for 16 of 1 to 1,100 tokens.
 // (Without the copying warp, with code of 165 KB: 1,622 and 611 us. The output by the state's warps while U is made:
 // the same for one prompt, 336 us for 16. The output's copies by the copying warp: 728 us.)
 // All waits are bounded: one that runs out ends the CTA's work and sets the status word.
@@ -64,7 +64,7 @@ struct Wide {
   // [K; Q] by 64-column blocks, T and M in the 128-byte swizzle; V; the output; factors
   static constexpr int kBlock = 2 * kC * 128, kTile = kC * 128;
   // (a place of T holds N first)
-  static constexpr int kKQBytes = KB * kBlock, kTBytes = kC * NS * 4, kMBytes = (BF16 ? 1 : 2) * kTile;
+  static constexpr int kKQBytes = KB * kBlock, kTBytes = kC * NS * 4, kMBytes = 2 * kTile;
   static constexpr int kVBytes = kC * kCols * 2, kFBytes = 2048;
   static_assert(kTBytes >= 2 * kTile && kTBytes % 1024 == 0, "N and T");
   static constexpr int kKQ = 0, kT = kKQ + 3 * kKQBytes, kM = kT + 2 * kTBytes, kV = kM + 2 * kMBytes, kOut = kV + 2 * kVBytes;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], us.to), hi[e], lo[e]);
       tmem_st16(tm + kTmR + 16u * hf, hi);  // (kbS comes behind these stores, and U M behind kbS)
-      if constexpr (!BF16) tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
+      tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
       tc_wait_st();
     }
     if (on && rq.out && !dead) {
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
 #pragma unroll
           for (int e = 0; e < 4; ++e) split2(r[8 * q + 2 * e] * sc.to, r[8 * q + 2 * e + 1] * sc.to, hi[e], lo[e]);
           st_shared4(m + swz(i, q), hi);
-          if constexpr (!BF16) st_shared4(m + L::kTile + swz(i, q), lo);
+          st_shared4(m + L::kTile + swz(i, q), lo);
         }
         fence_async();
         arrive(kbM + (ch & 1));
@@ -752,9 +752,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           wait(kbM + (was & 1), was >> 1);
           if (!dead) {
             const uint64_t m = desc_sw128(base + (uint32_t)(L::kM + (was & 1) * L::kMBytes), 16);
-            // U hi by M hi; FP16 also U lo by M hi, U hi by M lo
+            // U hi by M hi, U lo by M hi, U hi by M lo
 #pragma unroll 1
-            for (uint32_t part = 0; part < (BF16 ? 1u : 3u); ++part)
+            for (uint32_t part = 0; part < 3; ++part)
               mma_ts4<2>(tmem + kTmD, tmem + kTmR + (part == 1 ? 32u : 0u), m + (part == 2 ? (uint64_t)(L::kTile >> 4) : 0u), id_k,
                          part > 0);
             mma_commit(bar(kbO));
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           for (int b = 0; b < KB; ++b) {
             const uint64_t q = desc_sw128(kq_at(ch, b) + kC * 128u, 16);
 #pragma unroll 1
-            for (uint32_t part = 0; part < (BF16 ? 1u : 2u); ++part)
+            for (uint32_t part = 0; part < 2; ++part)
               mma_ts4<2>(tmem + kTmQ, tmem + (part ? kTmSlo : kTmShi) + 32u * b, q, id_k, b + part > 0);
           }
           mma_commit(bar(kbXQ));

@@ -11,7 +11,8 @@ from __future__ import annotations
 
 import numpy as np
 
-WINDOW = 32  # tokens at most in one chunk
+WINDOW = 32  # tokens that `near` looks back over
+ETA = 2.0**-17  # of delta_causal
 
 
 def delta(q, k, v, beta, alpha, state, scale):
@@ -50,6 +51,29 @@ def delta_bound(out, info, v, scale, dtype, q):
     tiny = 2.0**-134 if dtype == "bf16" else 2.0**-25  # half a step of subnormals
     made = part * (info["reach"] + 2 * info["near"]) + np.linalg.norm(q, axis=1, keepdims=True) * tol_state
     return half * np.abs(out) + (1 + half) * abs(scale) * made + tiny, tol_state
+
+
+def delta_causal(q, k, v, beta, alpha, state, scale, dtype):
+    """One head as `delta`, with tolerances that only what a token can see enters: out, state, tolerances of both.
+
+    A column's size at token t is the largest it has had, as the gates since then leave it: the values', the state
+    column's length. Each token adds an error of ETA of that size, earlier ones are shortened by the gates, and
+    different tokens' are independent. ETA: four products of operands with 22 bits (2^-21 each), and two sets of
+    values that share a power of two with others up to 2^20 larger (2^-39 of the largest, 2^-19 each):
+    1.5 * 2^-18 < 2^-17. Both types alike: a 16-bit output adds half a step of its own, no more."""
+    S = np.array(state, np.float64)
+    T, dv = v.shape
+    out, tol = np.empty((T, dv)), np.empty((T, dv))
+    size, err = np.linalg.norm(S, axis=0), np.zeros(dv)
+    half, tiny = (2.0**-8, 2.0**-134) if dtype == "bf16" else (2.0**-11, 2.0**-25)
+    for t in range(T):
+        S = alpha[t] * S
+        S = S + np.outer(k[t], beta[t] * (v[t] - S.T @ k[t]))
+        out[t] = scale * (S.T @ q[t])
+        size = np.maximum(alpha[t] * size, np.maximum(np.abs(v[t]), np.linalg.norm(S, axis=0)))
+        err = np.hypot(alpha[t] * err, ETA * size)
+        tol[t] = half * np.abs(out[t]) + (1 + half) * abs(scale) * np.linalg.norm(q[t]) * err + tiny
+    return out, S, tol, err
 
 
 def conv(x, old, w, bias, silu, unit_heads, head_dim, eps):
