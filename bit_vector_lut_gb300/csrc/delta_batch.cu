@@ -33,7 +33,7 @@ namespace {
 // the state, and hand them over through a ring of three stages (named barriers, no spinning).
 //
 // Numbers: the tensor cores multiply FP16. K and Q enter exactly (BF16 rows are brought to a largest
-// entry of 2^8 by a power of two, which the factors of the token take back). Every FP32 operand (S, R, U,
+// entry of 2^14 by a power of two, which the factors of the token take back). Every FP32 operand (S, R, U,
 // T, M) enters as two FP16 parts, hi and what hi leaves, scaled by a power of two per row of the product
 // so that neither part leaves FP16's range: some 22 bits, for either type: a BF16 output made from hi
 // alone (11 bits) may be rounded the other way (one prompt of 8,192 tokens: 670 us instead of 720).
@@ -61,9 +61,10 @@ struct Stage {
   static constexpr int NS = C + 4;                               // column of N in floats
   // T: hi, then lo; before, in the same place, N
   static constexpr int kM = kT + (2 * TS * 2 > NS * 4 ? 2 * TS * 2 : NS * 4) * C, kC = kM + 2 * C * TS * 2;  // M: hi, lo
-  static constexpr int kBytes = (kC + (5 * C + 4) * 4 + 127) / 128 * 128;
-  // factors per token: of V in R, of K S0 in R, of Q S0 and of M U in O, of U in the state; then g_C
-  static constexpr int kFv = 0, kFk = C, kFq = 2 * C, kFm = 3 * C, kFw = 4 * C, kFg = 5 * C;
+  static constexpr int kBytes = (kC + (6 * C + 4) * 4 + 127) / 128 * 128;
+  // factors per token: of V in R, of K S0 in R, of Q S0 and of M U in O, of U in the state; then g_C, and whether T has
+  // grown too large; gates
+  static constexpr int kFv = 0, kFk = C, kFq = 2 * C, kFm = 3 * C, kFw = 4 * C, kFg = 5 * C, kFt = kFg + 1, kFa = 5 * C + 4;
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -166,6 +167,7 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
   // ratios D[i][j] = a_(j+1) ... a_i (lane = j), the running product g_i, and g_C / g_j
   float* const f = reinterpret_cast<float*>(st + L::kC);
   f[L::kFv + lane] = al;
+  f[L::kFa + lane] = al;
   __syncwarp();
   float r = 1.f, gam = 1.f, gi = 1.f;
 #pragma unroll
@@ -317,14 +319,86 @@ __device__ __forceinline__ void produce(const DeltaArgs& a, const DeltaRequest& 
     f[L::kFq + lane] = a.scale * gi * qb;
     f[L::kFm + lane] = a.scale * qb * fm;
     f[L::kFw + lane] = bk * r;
-    if (lane == 0) f[L::kFg] = gam;
+    const bool grown = __any_sync(0xffffffffu, !(top < kGrown));
+    if (lane == 0) {
+      f[L::kFg] = gam;
+      f[L::kFt] = grown ? 1.f : 0.f;
+    }
   }
   __syncwarp();
 }
 
-// ---- consumer: one chunk against this warp's 16 columns; acc: S^T, row g column 2g, row g + 8 column 2g + 1
+// ---- tokens one at a time, by a warp with 16 columns of S in its accumulators (row(n, e) of S: entry e of tile n)
+template <int NT, bool BF16, class Row>
+__device__ __forceinline__ void warp_steps(const DeltaArgs& a, int h, long long row0, int nt, int col, float (&acc)[NT][4],
+                                           Row row) {
+  const int hq = h / a.group, t = threadIdx.x & 3;
+  for (int j = 0; j < nt && VQ3_IN(row0 + j, a.tokens, 16); ++j) {
+    const long long at = row0 + j;
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + at * a.k_token + hq * a.k_head;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + at * a.q_token + hq * a.q_head;
+    float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};  // k . S of two columns, q . S of them, k . q
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 k = delta_unpack2<BF16>(__ldg(reinterpret_cast<const uint32_t*>(kp + row(n, 0))));
+      const float2 q = delta_unpack2<BF16>(__ldg(reinterpret_cast<const uint32_t*>(qp + row(n, 0))));
+      s[0] = fmaf(k.x, acc[n][0], fmaf(k.y, acc[n][1], s[0]));
+      s[1] = fmaf(k.x, acc[n][2], fmaf(k.y, acc[n][3], s[1]));
+      s[2] = fmaf(q.x, acc[n][0], fmaf(q.y, acc[n][1], s[2]));
+      s[3] = fmaf(q.x, acc[n][2], fmaf(q.y, acc[n][3], s[3]));
+      s[4] = fmaf(k.x, q.x, fmaf(k.y, q.y, s[4]));
+    }
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
+      s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
+    }
+    const float al = __ldg(a.alpha + at * a.alpha_token + h), be = __ldg(a.beta + at * a.beta_token + h);
+    const float2 v = delta_unpack2<BF16>(__ldg(
+        reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.v) + at * a.v_token + h * a.v_head + col)));
+    const float u0 = be * (v.x - al * s[0]), u1 = be * (v.y - al * s[1]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 k = delta_unpack2<BF16>(__ldg(reinterpret_cast<const uint32_t*>(kp + row(n, 0))));
+      acc[n][0] = fmaf(k.x, u0, al * acc[n][0]);
+      acc[n][1] = fmaf(k.y, u0, al * acc[n][1]);
+      acc[n][2] = fmaf(k.x, u1, al * acc[n][2]);
+      acc[n][3] = fmaf(k.y, u1, al * acc[n][3]);
+    }
+    if (t == 0)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * a.o_token + h * a.o_head + col) =
+          delta_pack2<BF16>(a.scale * fmaf(s[4], u0, al * s[2]), a.scale * fmaf(s[4], u1, al * s[3]));
+  }
+}
+// Least of a column's sizes over the lanes that share it.
+__device__ __forceinline__ unsigned seen_least(unsigned m) {
+  m = min(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return min(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+// The least that a token's R finds in its two columns, from `size` on and with earlier tokens' as the gates leave them:
+// for the few chunks that the least value alone would have gone through again (a small one behind large ones).
+template <int NB, class Gate>
+__device__ __forceinline__ float2 least_found(const float (&r)[NB][4], float2 size, Gate gate) {
+  const int quad = threadIdx.x & 28;
+  float2 least = both(INFINITY);
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y0 = fabsf(__shfl_sync(0xffffffffu, r[n][i & 1], quad + i / 2));
+      const float y1 = fabsf(__shfl_sync(0xffffffffu, r[n][2 + (i & 1)], quad + i / 2));
+      const float a = fabsf(gate(8 * n + i));
+      size = make_float2(fmaxf(a * size.x, y0), fmaxf(a * size.y, y1));
+      if (y0 != 0.f) least.x = fminf(least.x, size.x);
+      if (y1 != 0.f) least.y = fminf(least.y, size.y);
+    }
+  return least;
+}
+
+// ---- consumer: one chunk against this warp's 16 columns; acc: S^T, row g column 2g, row g + 8 column 2g + 1.
+// False, with S as it was: the chunk has to be gone through token by token.
 template <bool BF16>
-__device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int warp,
+__device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int warp,
                                         int lane) {
   using L = Stage;
   constexpr int C = L::C, RS = L::RS, TS = L::TS;
@@ -374,6 +448,7 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     }
   // R^T = V^T - X_K, times the factor of T's column
   const unsigned char* sv = st + L::kV + ((2 * t) * L::VS + warp * kWarpCols + 2 * g) * 2;
+  unsigned seen0 = ~0u, seen1 = ~0u;
 #pragma unroll
   for (int n = 0; n < NN; ++n) {
     const float2 fv = *reinterpret_cast<const float2*>(f + L::kFv + 8 * n + 2 * t);
@@ -384,10 +459,15 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     xk[n][1] = vb.x * fv.y - fk.y * xk[n][1];
     xk[n][2] = va.y * fv.x - fk.x * xk[n][2];
     xk[n][3] = vb.y * fv.y - fk.y * xk[n][3];
+    seen0 = min(seen0, min(seen_of(fmaxf(fabsf(va.x * fv.x), fabsf(xk[n][0]))), seen_of(fmaxf(fabsf(vb.x * fv.y), fabsf(xk[n][1])))));
+    seen1 = min(seen1, min(seen_of(fmaxf(fabsf(va.y * fv.x), fabsf(xk[n][2]))), seen_of(fmaxf(fabsf(vb.y * fv.y), fabsf(xk[n][3])))));
   }
+  seen0 = seen_least(seen0);
+  seen1 = seen_least(seen1);
   // U^T = R^T T^T
-  row_max<NN>(xk, m0, m1);
-  const Scale r0 = scale_of(m0), r1 = scale_of(m1);
+  float top0, top1;
+  row_max<NN>(xk, top0, top1);
+  const Scale r0 = scale_of(top0), r1 = scale_of(top1);
   float u[NN][4];
 #pragma unroll
   for (int n = 0; n < NN; ++n) u[n][0] = u[n][1] = u[n][2] = u[n][3] = 0.f;
@@ -415,6 +495,22 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     u[n][1] *= r0.back;
     u[n][2] *= r1.back;
     u[n][3] *= r1.back;
+  }
+  float um0, um1;
+  row_max<NN>(u, um0, um1);
+  {
+    float all = 0.f;
+#pragma unroll
+    for (int n = 0; n < NN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) all += fabsf(u[n][e]);
+    // (R and what it comes from have T's factor of 2^-14)
+    if (__any_sync(0xffffffffu, !(all < INFINITY)) || f[L::kFt] != 0.f) return false;
+    const float need0 = fmaxf(top0, 0x1p-14f * um0) * kRange, need1 = fmaxf(top1, 0x1p-14f * um1) * kRange;
+    if (__any_sync(0xffffffffu, need0 > seen_back(seen0) || need1 > seen_back(seen1))) {
+      const float2 least = least_found<NN>(xk, make_float2(0x1p-17f * m0, 0x1p-17f * m1), [f](int i) { return f[L::kFa + i]; });
+      if (__any_sync(0xffffffffu, need0 > least.x || need1 > least.y)) return false;
+    }
   }
   // S^T <- g_C S^T + (U diag(w))^T K
   {
@@ -462,8 +558,7 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     }
   }
   // O^T = X_Q + U^T M^T
-  row_max<NN>(u, m0, m1);
-  const Scale u0 = scale_of(m0), u1 = scale_of(m1);
+  const Scale u0 = scale_of(um0), u1 = scale_of(um1);
 #pragma unroll
   for (int n = 0; n < NN; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
@@ -493,6 +588,7 @@ __device__ __forceinline__ void consume(float (&acc)[2 * KS][4], const unsigned 
     o[n][2] = fq.x * xq[n][2] + fm.x * (u1.back * o[n][2]);
     o[n][3] = fq.y * xq[n][3] + fm.y * (u1.back * o[n][3]);
   }
+  return true;
 }
 
 template <bool BF16>
@@ -538,9 +634,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     const int s = c % kStages;
     bar_sync(kFullBar + s * kConsumers + warp, kFullThreads);
     float o[NN][4];
-    if (on) consume<BF16>(acc, smem + s * L::kBytes, o, warp, lane);
+    const bool done = on && consume<BF16>(acc, smem + s * L::kBytes, o, warp, lane);
     if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kEmptyThreads);
-    if (on) {
+    if (on && !done) {
+      warp_steps<2 * KS, BF16>(a, h, rq.first + c * C, min(rq.n - c * C, C), col, acc, [t](int n, int e) { return 8 * n + 2 * t + e; });
+    } else if (on) {
 #pragma unroll
       for (int n = 0; n < NN; ++n)
 #pragma unroll
@@ -736,6 +834,7 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
     // X^T = S^T [K; Q]^T
     float top0, top1;
     row_max<2 * KS>(acc, top0, top1);
+    const float2 size = make_float2(0.125f * top0, 0.125f * top1);
     const Scale s0 = scale_of(top0), s1 = scale_of(top1);
     float xk[1][4] = {{0.f, 0.f, 0.f, 0.f}}, xq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -760,6 +859,12 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
       xk[0][3] = vb.y - g1 * kb1 * (s1.back * xk[0][3]);
     }
     uint32_t hi[4], lo[4];
+    unsigned seen0, seen1;
+    {
+      const float2 va = delta_unpack2<BF16>(vw[0]), vb = delta_unpack2<BF16>(vw[1]);
+      seen0 = seen_least(min(seen_of(fmaxf(fabsf(va.x), fabsf(xk[0][0]))), seen_of(fmaxf(fabsf(vb.x), fabsf(xk[0][1])))));
+      seen1 = seen_least(min(seen_of(fmaxf(fabsf(va.y), fabsf(xk[0][2]))), seen_of(fmaxf(fabsf(vb.y), fabsf(xk[0][3])))));
+    }
     row_max<1>(xk, top0, top1);
     const Scale r0 = scale_of(top0), r1 = scale_of(top1);
     split2(xk[0][0] * r0.to, xk[0][1] * r0.to, hi[0], lo[0]);
@@ -772,9 +877,24 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
     u[0][1] *= r0.back * tb1;
     u[0][2] *= r1.back * tb0;
     u[0][3] *= r1.back * tb1;
+    {
+      float um0, um1;
+      row_max<1>(u, um0, um1);
+      const float need0 = fmaxf(top0, um0) * kRange, need1 = fmaxf(top1, um1) * kRange;
+      bool lost = __any_sync(0xffffffffu, !(fabsf(u[0][0]) + fabsf(u[0][1]) + fabsf(u[0][2]) + fabsf(u[0][3]) < INFINITY));
+      if (__any_sync(0xffffffffu, need0 > seen_back(seen0) || need1 > seen_back(seen1))) {
+        const float2 least = least_found<1>(xk, size, [al](int i) { return __shfl_sync(0xffffffffu, al, i); });
+        lost |= __any_sync(0xffffffffu, need0 > least.x || need1 > least.y) != 0;
+      }
+      if (lost) {
+        warp_steps<2 * KS, BF16>(a, h, row0, nt, col, acc, [t](int n, int e) { return block_row(n, t, e); });
+        continue;
+      }
+      top0 = um0;
+      top1 = um1;
+    }
     // O^T = X_Q + U^T M^T
     {
-      row_max<1>(u, top0, top1);
       const Scale u0 = scale_of(top0), u1 = scale_of(top1);
       split2(u[0][0] * u0.to, u[0][1] * u0.to, hi[0], lo[0]);
       split2(u[0][2] * u1.to, u[0][3] * u1.to, hi[1], lo[1]);

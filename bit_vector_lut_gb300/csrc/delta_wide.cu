@@ -17,10 +17,12 @@
 // The chain of a chunk is X_K, R, U, U w, dS, S; what is not on it (X_Q, O and its output of the chunk before, the
 // next chunks' rows and T) runs under it. FP32 operands enter as two FP16 parts as in delta_batch.cu. The scale of S
 // has to be known before dS is: it is made from a bound, |g_C| max |S| + sum |u w| max |k|, which is some 2^5 above
-// what comes out and leaves 17 bits of FP16's range below it.
+// what comes out and leaves 17 bits of FP16's range below it. A chunk with values that cannot share a power of two
+// (kRange, kGrown) goes on as it is, but its dS and its output are not used: the state's warps, whose S is still the
+// chunk's first, step through its tokens in FP32.
 // Bound by that chain and by the row warps, which are both busy some 10,400 cycles a chunk, a third of them waiting for
 // products of 50 to 70 cycles for 128 x 64 x 16 (32 where they have the SM to themselves): 5.3 us a chunk of 64 tokens,
-// 0.72 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.32 ms for 16 of 1 to 1,100 tokens.
+// 0.75 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.34 ms for 16 of 1 to 1,100 tokens.
 // (Without the copying warp, with code of 165 KB: 1,622 and 611 us. The output by the state's warps while U is made:
 // the same for one prompt, 336 us for 16. The output's copies by the copying warp: 728 us.)
 // All waits are bounded: one that runs out ends the CTA's work and sets the status word.
@@ -69,8 +71,8 @@ struct Wide {
   static_assert(kTBytes >= 2 * kTile && kTBytes % 1024 == 0, "N and T");
   static constexpr int kKQ = 0, kT = kKQ + 3 * kKQBytes, kM = kT + 2 * kTBytes, kV = kM + 2 * kMBytes, kOut = kV + 2 * kVBytes;
   static constexpr int kF = kOut + kVBytes;
-  // factors per token: of V and of X_K in R, of X_Q and of U M in O, of U in dS, the largest |k|; then g_C
-  static constexpr int kFv = 0, kFk = 64, kFq = 128, kFm = 192, kFw = 256, kKm = 320, kG = 384;
+  // factors per token: of V and of X_K in R, of X_Q and of U M in O, of U in dS, the largest |k|, its gate; then g_C
+  static constexpr int kFv = 0, kFk = 64, kFq = 128, kFm = 192, kFw = 256, kKm = 320, kFa = 384, kG = 448;
   // exchange of the column's halves: float2 [2][128], float4 [2][128]; scales for the output: float2 [2][128]; rows: gates
   // and factors; barriers
   static constexpr int kX1 = kF + 3 * kFBytes, kX2 = kX1 + 2048, kXO = kX2 + 4096, kRow = kXO + 2048, kMax = kRow + 1024, kBar = kMax + 256;
@@ -95,7 +97,9 @@ enum {
   kbS = 24,       // [4] S stored: half of d_k, half of that
   kbXK = 28, kbR, kbU, kbXQ, kbW,
   kbD = 33,       // [2]
-  kbO = 35, kbORead, kbDrain, kBars
+  kbO = 35, kbORead, kbDrain,
+  kbPair,         // [4] the two warps of 32 columns, while they step
+  kBars = kbPair + 4
 };
 
 struct DeltaMaps {
@@ -196,13 +200,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
   const auto bar = [&](int i) { return bar0 + 8u * i; };
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(smem + L::kBar + 8 * kBars);
   volatile int* const abort = reinterpret_cast<volatile int*>(smem + L::kBar + 8 * kBars + 4);
-  static_assert(8 * kBars + 8 <= 512, "barriers");
+  // of the last four chunks: its number + 1 if it has to be gone through token by token
+  volatile int* const again = abort + 1;
+  static_assert(8 * kBars + 24 <= 512, "barriers");
 
   if (tid < kBars) {
     // arrivals: a copy, a product's completion or a warp each
-    constexpr int n[kBars] = {1, 1, 1, 4, 4, 4, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 2, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 4, 1};
+    constexpr int n[kBars] = {1, 1, 1, 4, 4, 4, 1, 1, 1, 1, 1, 8, 8, 6, 6, 1, 1, 2, 2, 1, 1, 2, 2, 1, 4, 4, 4, 4, 1, 8, 1, 1, 8, 1, 1, 1, 4, 1, 2, 2, 2, 2};
     mbar_init(bar(tid), KB == 1 && tid >= kbS && tid < kbS + 4 ? 8 : n[tid]);
     if (tid == 0) *abort = 0;
+    if (tid < 4) again[tid] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -253,8 +260,101 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
     }
     x1[hf * 128 + c] = make_float2(mS, 0.f);
     pair_sync();
-    Scale ss = scale_of<14>(fmaxf(mS, x1[(hf ^ 1) * 128 + c].x)), ws{0.f, 0.f};
+    Scale ss = scale_of(fmaxf(mS, x1[(hf ^ 1) * 128 + c].x)), ws{0.f, 0.f};
     float gC = 1.f;
+    // S over a chunk token by token, with its output: delta_steps with two threads a column. S goes through tensor memory,
+    // where its parts are otherwise, a slice at a time: in registers it cost the loop around it some 100 spilled ones.
+    int n_met = 0;
+    const auto met = [&] {
+      arrive(kbPair + sub);
+      wait(kbPair + sub, n_met++);
+    };
+    const auto steps = [&](int ch) {
+      const int nt = rq.n - ch * kC < kC ? rq.n - ch * kC : kC, hq = h / a.group;
+      const uint32_t at = tm + kTmShi + (uint32_t)(hf * SD);
+#pragma unroll
+      for (int i = 0; i < SD; i += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(e & 1 ? S[(i + e) / 2].y : S[(i + e) / 2].x);
+        tmem_st16(at + (uint32_t)i, w);
+      }
+      tc_wait_st();
+#pragma unroll 1
+      for (int j = 0; j < nt; ++j) {
+        const long long row = rq.first + ch * kC + j;
+        if (!VQ3_IN(row, a.tokens, 5)) break;
+        const uint4* kp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * a.k_token + hq * a.k_head + hf * SD);
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * a.q_token + hq * a.q_head + hf * SD);
+        float2 x = both(0.f), y = x, kq = x;
+#pragma unroll 1
+        for (int i = 0; i < SD; i += 32) {
+          uint32_t s[32];
+          tmem_ld32(at + (uint32_t)i, s);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 kw = __ldg(kp + i / 8 + e), qw = __ldg(qp + i / 8 + e);
+            const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w}, q4[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+              const float2 k2 = delta_unpack2<BF16>(k4[l]), q2 = delta_unpack2<BF16>(q4[l]), s2 = bits2(s, 8 * e + 2 * l);
+              x = fma_pair(k2, s2, x);
+              y = fma_pair(q2, s2, y);
+              kq = fma_pair(k2, q2, kq);
+            }
+          }
+        }
+        const float4 own = make_float4(x.x + x.y, y.x + y.y, kq.x + kq.y, 0.f);
+        x2[hf * 128 + c] = own;
+        met();
+        const float4 other = x2[(hf ^ 1) * 128 + c];
+        met();
+        const float al = __ldg(a.alpha + row * a.alpha_token + h), be = __ldg(a.beta + row * a.beta_token + h);
+        const float v = on ? delta_unpack2<BF16>(__ldg(static_cast<const uint16_t*>(a.v) + row * a.v_token + h * a.v_head + col)).x : 0.f;
+        const float u = be * (v - al * (own.x + other.x));
+#pragma unroll 1
+        for (int i = 0; i < SD; i += 32) {
+          uint32_t s[32], w[16];
+          tmem_ld32(at + (uint32_t)i, s);
+          tc_wait_ld();
+#pragma unroll
+          for (int n = 0; n < 32; n += 16) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 kw = __ldg(kp + (i + n) / 8 + e);
+              const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+              for (int l = 0; l < 4; ++l) {
+                const float2 s2 = fma_pair(delta_unpack2<BF16>(k4[l]), u, mul_pair(bits2(s, n + 8 * e + 2 * l), al));
+                w[8 * e + 2 * l] = __float_as_uint(s2.x);
+                w[8 * e + 2 * l + 1] = __float_as_uint(s2.y);
+              }
+            }
+            tmem_st16(at + (uint32_t)(i + n), w);
+          }
+        }
+        tc_wait_st();
+        if (on && hf == 0)
+          static_cast<uint16_t*>(a.out)[row * a.o_token + h * a.o_head + col] =
+              (uint16_t)delta_pack2<BF16>(a.scale * fmaf(own.z + other.z, u, al * (own.y + other.y)), 0.f);
+      }
+      mS = 0.f;
+#pragma unroll
+      for (int i = 0; i < SD; i += 32) {
+        uint32_t s[32];
+        tmem_ld32(at + (uint32_t)i, s);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          S[(i + e) / 2] = bits2(s, e);
+          mS = max_pair(mS, S[(i + e) / 2]);
+        }
+      }
+      x1[hf * 128 + c] = make_float2(mS, 0.f);
+      met();
+      ss = scale_of(fmaxf(mS, x1[(hf ^ 1) * 128 + c].x));
+    };
     for (int ch = 0;; ++ch) {
       // S <- g_C S + dS, and its parts for the products, half by half
       if (ch) {
@@ -263,9 +363,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         tc_after();
         mS = 0.f;
       }
+      // every warp's word on it came before its arrival for U w; only where a wait gave up the two warps of a column may
+      // see different ones, and so steps() has no barrier that is not bounded
+      const bool stepped = ch && again[(ch - 1) & 3] == ch;
+      if (stepped) steps(ch - 1);
 #pragma unroll
       for (int i = 0; i < SD; i += 32) {
-        if (ch) {
+        if (ch && !stepped) {
           uint32_t x[32];
           tmem_ld32(tm + kTmD + (uint32_t)(hf * SD + i), x);
           tc_wait_ld();
@@ -322,11 +426,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           top = max_pair(top, y);
         }
       }
-      x1[hf * 128 + c] = make_float2(top, mS);
+      // with S's largest entry, rounded up to 16 bits, what the half's last tokens leave to the next one
+      const float last = fmaxf(fabsf(r[15].y), fabsf(f[L::kFa + 32 * hf + 31] * r[15].x));
+      const uint32_t mS16 = (__float_as_uint(mS) + 0xffffu) & 0xffff0000u;
+      x1[hf * 128 + c] = make_float2(top, __uint_as_float(mS16 | __float_as_uint(last) >> 16));
       pair_sync();
       const float2 o1 = x1[(hf ^ 1) * 128 + c];
-      const Scale rs = scale_of(fmaxf(top, o1.x));
-      const float mS_all = fmaxf(mS, o1.y);
+      const float topr = fmaxf(top, o1.x);
+      const Scale rs = scale_of(topr);
+      const float mS_all = __uint_as_float(max(mS16, __float_as_uint(o1.y) & 0xffff0000u));
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], rs.to), hi[e], lo[e]);
@@ -338,6 +446,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
       tc_wait_st();
       arrive(kbR);
+      // (under U) the least that a token's R finds in its column, from the state on; with T's factor, as R
+      float least = INFINITY;
+      {
+        // (BF16: k's factor is 2^-14 of its largest entry); the second half also goes on from the last tokens of the first
+        float size = mS_all * fabsf(f[L::kFk + 32 * hf]) * (BF16 ? 0x1p11f : 0x1p-3f);
+        if (hf) size = fmaxf(size, __uint_as_float(__float_as_uint(o1.y) << 16));
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 fa = *reinterpret_cast<const float4*>(f + L::kFa + 32 * hf + j);
+          const float av[4] = {fa.x, fa.y, fa.z, fa.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = e & 1 ? r[(j + e) / 2].y : r[(j + e) / 2].x;
+            size = fmaxf(fabsf(av[e] * size), fabsf(y));
+            if (y != 0.f) least = fminf(least, size);
+          }
+        }
+      }
       // U^T, as it is for the output and times w for dS
       wait(kbU, ch);
       tc_after();
@@ -359,14 +485,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           l1 = fmaf(fabsf(w.x), e ? km.z : km.x, fmaf(fabsf(w.y), e ? km.w : km.y, l1));
         }
       }
-      x2[hf * 128 + c] = make_float4(topu, top, l1, 0.f);
+      x2[hf * 128 + c] = make_float4(topu, top, l1, least);
       pair_sync();
       const float4 o2 = x2[(hf ^ 1) * 128 + c];
       const Scale us = scale_of(fmaxf(topu, o2.x));
       ws = scale_of(fmaxf(top, o2.y));
       gC = f[L::kG];
       if (hf == 0) reinterpret_cast<float2*>(smem + L::kXO)[(ch & 1) * 128 + c] = make_float2(ss.back, us.back);
-      ss = scale_of<14>(fabsf(gC) * mS_all + (l1 + o2.z));
+      ss = scale_of(fabsf(gC) * mS_all + (l1 + o2.z));
+      {
+        // (l1 is not finite if a U is not)
+        const bool lost = !(l1 + o2.z < INFINITY) || fmaxf(topr, 0x1p-14f * fmaxf(topu, o2.x)) * kRange > fminf(least, o2.w);
+        if (__any_sync(0xffffffffu, lost) && lane == 0) again[ch & 3] = ch + 1;
+      }
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
         const float4 fw = *reinterpret_cast<const float4*>(f + L::kFw + 32 * hf + 2 * e);
@@ -443,17 +574,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           }
         }
       }
+      const bool skip = *abort || again[ch & 3] == ch + 1;  // written by the state's warps in that case
       fence_async();
       sync_threads(9, 128);  // whole rows
       if (rq.n - ch * kC >= kC) {
-        if (p == 0 && !*abort && VQ3_IN(rq.first + ch * kC + kC - 1, a.tokens, 2))
+        if (p == 0 && !skip && VQ3_IN(rq.first + ch * kC + kC - 1, a.tokens, 2))
           asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                            reinterpret_cast<uint64_t>(&maps.out)),
                        "r"(col0), "r"(h), "r"(rq.first + ch * kC), "r"(tile)
                        : "memory");
       } else {  // the rows behind the request's last are another's: row by row, up to 256 bytes
         const int t = 16 * sub + lane;
-        if (lane < 16 && ch * kC + t < rq.n && !*abort && VQ3_IN(rq.first + ch * kC + t, a.tokens, 2)) {
+        if (lane < 16 && ch * kC + t < rq.n && !skip && VQ3_IN(rq.first + ch * kC + t, a.tokens, 2)) {
           const uint16_t* to = static_cast<const uint16_t*>(a.out) + (rq.first + ch * kC + t) * a.o_token + h * a.o_head + col0;
           asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(tile + (uint32_t)(t * kCols * 2)),
                        "r"(row_bytes) : "memory");
@@ -476,6 +608,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       if (ch > 2) output_read();
       sync_threads(9, 128);  // the last chunk's gates have been read
       if (is_k) {
+        f[L::kFa + p] = al;
         if (p)
           gate[p - 1] = al;
         else
@@ -485,7 +618,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       load_gates(t0 + kC);
       wait(kbKQFull + s3, ch / 3);
       // thread = row of [K; Q]: its largest entry; BF16 to FP16, scaled by a power of two; rows behind the last are zero
-      float back = 1.f, largest = 512.f;
+      float back = 1.f, largest = 0x1p15f;
       {
         const uint32_t row = kq + (is_k ? 0u : kC * 128u);
         const auto at = [&](int q) { return row + (uint32_t)((q >> 3) * L::kBlock) + swz(i, q & 7); };
@@ -691,7 +824,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
         for (int k = 0; k < 8; ++k) topy = fmaxf(topy, fmaxf(fabsf(y[k].x), fabsf(y[k].y)));
         tops[w * 32 + lane] = w == 0 ? fmaxf(top, topy) : topy;
         sync_threads(10, 64);
-        const Scale s0 = scale_of(fmaxf(tops[lane], tops[32 + lane])), s1 = scale_of(top);  // column lane; 32 + lane
+        const float top0 = fmaxf(tops[lane], tops[32 + lane]);
+        const Scale s0 = scale_of(top0), s1 = scale_of(top);  // column lane; 32 + lane
+        if (__any_sync(0xffffffffu, !(fmaxf(top0, top) < kGrown)) && lane == 0) again[ch & 3] = ch + 1;
         const uint32_t t = base + (uint32_t)(L::kT + (ch & 1) * L::kTBytes);
         const auto put = [&](int j, int q, const float2* v, float to) {
           uint32_t hi[4], lo[4];
