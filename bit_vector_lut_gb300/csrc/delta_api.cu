@@ -125,6 +125,13 @@ int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* s
   return report_ok();
 }
 
+int vq3_delta_status(int* status_host, void* stream) {
+  if (!status_host) return report_error(VQ3_EINVAL, "delta_status: null pointer");
+  const cudaError_t e = delta_status(status_host, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(VQ3_ECUDA, "delta_status: %s", cudaGetErrorString(e));
+  return report_ok();
+}
+
 int vq3_short_conv(const vq3_batch* batch, const vq3_conv* conv, void* stream) {
   const char* who = "short_conv";
   if (!batch || !conv) return report_error(VQ3_EINVAL, "%s: null descriptor", who);

@@ -25,7 +25,7 @@
 // 0.75 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.34 ms for 16 of 1 to 1,100 tokens.
 // (Without the copying warp, with code of 165 KB: 1,622 and 611 us. The output by the state's warps while U is made:
 // the same for one prompt, 336 us for 16. The output's copies by the copying warp: 728 us.)
-// All waits are bounded: one that runs out ends the CTA's work and sets the status word.
+// All waits are bounded: one that runs out ends the CTA's work and sets the caller's status word, or the device's.
 #include "vq3_internal.h"
 
 namespace vq3 {
@@ -101,6 +101,8 @@ enum {
   kbPair,         // [4] the two warps of 32 columns, while they step
   kBars = kbPair + 4
 };
+
+__device__ int g_delta_status;  // of the calls without a status word of their own; vq3_delta_status reads it
 
 struct DeltaMaps {
   CUtensorMap k, q, v, out;
@@ -999,7 +1001,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
   }
   tc_before();
   __syncthreads();
-  if (tid == 0 && *abort && a.status) *a.status = 3;
+  if (tid == 0 && *abort) *(a.status ? a.status : &g_delta_status) = 3;
   if (warp == kIssueWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
@@ -1025,6 +1027,17 @@ cudaError_t launch(const DeltaArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t delta_status(int* host, cudaStream_t st) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(host, g_delta_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && *host) {
+    static const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_delta_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
+  return e;
+}
 
 cudaError_t launch_delta_wide(const DeltaArgs& a, bool bf16, cudaStream_t st) {
   if (a.d_k == 64) return bf16 ? launch<64, true>(a, st) : launch<64, false>(a, st);

@@ -339,7 +339,7 @@ struct DeltaArgs {
   const int* slot_in;
   const int* slot_out;
   long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head, alpha_token, beta_token, state_slot;
-  int* status;  // or null
+  int* status;  // or null: the device's word
   int tokens, requests, slots, v_heads, group, d_k, d_v, max_new;
   float scale;
 };
@@ -350,6 +350,7 @@ struct DeltaArgs {
 constexpr int kDeltaStepTokens = 3, kDeltaBlockTokens = 32, kDeltaBlockTokens256 = 24;
 cudaError_t launch_delta_batch(const DeltaArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_delta_wide(const DeltaArgs& a, bool bf16, cudaStream_t st);  // d_k 64 or 128
+cudaError_t delta_status(int* host, cudaStream_t st);
 struct ConvArgs {
   const uint16_t* x;
   const uint16_t* weight;

@@ -164,6 +164,7 @@ def _load() -> ctypes.CDLL:
         # vq3_rotary, vq3_batch, vq3_delta and vq3_conv come as their bytes or by reference
         "vq3_kv_append_rotary": (c_int, [c_void_p, POINTER(vq3_kv_rows), c_void_p, POINTER(vq3_kv_cache), c_void_p]),
         "vq3_delta_rule_batch": (c_int, [c_void_p, c_void_p, c_void_p]),
+        "vq3_delta_status": (c_int, [POINTER(c_int), c_void_p]),
         "vq3_short_conv": (c_int, [c_void_p, c_void_p, c_void_p]),
         "vq3_last_error": (ctypes.c_char_p, []),
         "vq3_version": (ctypes.c_char_p, []),
@@ -819,7 +820,8 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
     [slots, v_heads, d_k, d_v] FP32. Request r has rows q_start[r] .. q_start[r + 1] - 1, goes on from slot
     slot_in[r] (negative, or slot_in None: from zeros) and leaves its state in slot_out[r] (negative, or None: nowhere).
     max_new: most new tokens of a request, 0 if unknown. It only picks the kernel, but say it where it is known.
-    status: an int32 tensor [1] that becomes 3 if a wait inside the call gave up (its results are invalid then)."""
+    status: an int32 tensor [1] that becomes 3 if a wait inside the call gave up (its results are invalid then);
+    without one delta_status tells."""
     index, dtype = v.get_device(), v.dtype
     qs, vs = q.shape, v.shape
     if dtype not in TYPES or len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or q.dtype is not dtype or \
@@ -855,6 +857,16 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
                     beta.stride(0), alpha.stride(0), st[0], 0 if status is None else status.data_ptr())
     _launch(index, stream, lib.vq3_delta_rule_batch, batch, d)
     return out
+
+
+def delta_status(device=None, stream=None) -> int:
+    """0, or 3 when a wait gave up in a delta_rule_batch call on `device` (the current one) that was given no `status`,
+    since the last answer other than 0 (vq3_delta_status). Waits for the stream; ask before results are handed on."""
+    device = torch.device("cuda" if device is None else device)
+    v = c_int(0)
+    _launch(torch.cuda.current_device() if device.index is None else device.index, stream, lib.vq3_delta_status,
+            ctypes.byref(v))
+    return int(v.value)
 
 
 def short_conv(x: torch.Tensor, weight: torch.Tensor, states: torch.Tensor, q_start: torch.Tensor,

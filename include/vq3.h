@@ -535,9 +535,16 @@ typedef struct vq3_delta {
   long long v_token, v_head, out_token, out_head;
   long long beta_token, alpha_token;
   long long state_slot;  /* a multiple of 4 */
-  int* status;           /* device word or NULL: 3 if a wait inside the call gave up, else left as it is */
+  int* status;           /* device word that becomes 3 if a wait inside the call gave up (and is left as it is
+                            otherwise), or NULL: the device's own word, read by vq3_delta_status. Then the call's
+                            rows of out and the slots it writes are undefined. */
 } vq3_delta;
 VQ3_API int vq3_delta_rule_batch(const vq3_batch* batch, const vq3_delta* delta, void* stream);
+
+/* Status of the vq3_delta_rule_batch calls on the current device that brought no word of their own, after the
+ * stream's prior work: 0, or 3 when a wait in one of them gave up since the last answer other than 0. Copies it to
+ * *status_host and waits for the stream. Errors: VQ3_EINVAL (null pointer), VQ3_ECUDA. */
+VQ3_API int vq3_delta_status(int* status_host, void* stream);
 
 /*
  * The short convolution in front of the delta rule: per channel c and token t
