@@ -835,7 +835,7 @@ def delta_rule_batch(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: to
             raise Vq3Error(-1, "beta and alpha must be float32 [tokens, v_heads], the heads side by side")
     ss, st = states.shape, states.stride()
     if states.dtype is not _FLOAT or len(ss) != 4 or ss[1] != heads or ss[2] != d_k or ss[3] != d_v or \
-            states.get_device() != index or st[1] != d_k * d_v or st[2] != d_v or st[3] != 1:
+            states.get_device() != index or (heads > 1 and st[1] != d_k * d_v) or st[2] != d_v or st[3] != 1:
         raise Vq3Error(-1, "states must be float32 [slots, v_heads, d_k, d_v], contiguous within a slot")
     if status is not None and not (_ints_ok(index, status) and status.numel() == 1):
         raise Vq3Error(-1, "status must be an int32 tensor [1] on the inputs' device")
