@@ -482,7 +482,8 @@ VQ3_API int vq3_kv_append_rotary(const vq3_rotary* rotary, const vq3_kv_rows* ro
  * ---------------------------------------------------------------------------
  * The delta-rule token mixer for packed requests, each with a state of its own in a slot of a pool: the
  * other kind of layer of the pages' hybrid decoder in serving form. They give no interface for it; the
- * two calls below are this library's, their batch that of the attention calls (q_start as there).
+ * two calls below are this library's, their batch that of the attention calls (q_start as there; starts outside the
+ * batch are brought into it, and where they do not ascend some requests may be left out, but nothing outside is touched).
  * slot_in[r] is the slot that request r goes on from: an entry outside [0, slots), or slot_in NULL, starts it
  * from zeros. slot_out[r] takes its state after the last new token: an entry outside [0, slots), or slot_out
  * NULL, keeps none. They may be the same slot. So a verify step can leave its state unwritten and the accepted
