@@ -3,8 +3,9 @@
 //     (x1 cos - x2 sin, x2 cos + x1 sin),
 // queries to their output, keys and values into the pages.
 //
-// Angles: freq / (2 pi) as a 64-bit fraction of a turn (from FP64), times the position modulo one turn in integers:
-// exact for any position, where an FP32 product is off by whole radians from some 10^7 on (by 2^-8 radians at 10^5).
+// Angles: freq / (2 pi) as a 64-bit fraction of a turn (from two FP64 parts), times the position modulo one turn in
+// integers: right for any position, where an FP32 product is off by whole radians from some 10^7 on (by 2^-8 radians at
+// 10^5), and for any frequency up to 2^40, where FP64 alone would be off by 2^-25 of a turn per radian a position.
 //
 // A CTA takes 4 tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
 // the heads' items: 2 x 16 bytes a thread, both partners of 8 pairs, so that a row may be turned in place. Bound by
@@ -53,8 +54,10 @@ __global__ void __launch_bounds__(kRotThreads, 4) kv_append_rotary_kernel(const 
   const AppendArgs& kv = a.kv;
   const long long limit = (long long)kv.n_pages << kv.page_shift;
   if (tid < a.half) {
-    const double x = (double)__ldg(a.freq + tid) * 0.15915494309189535;  // 1 / (2 pi)
-    turns[tid] = (unsigned long long)((x - floor(x)) * 18446744073709551616.0);
+    // freq / (2 pi) in two FP64 parts, their distance from a whole number as 64-bit fractions
+    constexpr double kInv = 0.15915494309189535, kRest = -9.839338337591243e-18, kOne = 18446744073709551616.0;
+    const double f = (double)__ldg(a.freq + tid), x = f * kInv, rest = fma(f, kInv, -x) + f * kRest;
+    turns[tid] = (unsigned long long)(long long)((x - rint(x)) * kOne) + (unsigned long long)(long long)(rest * kOne);
   }
   if (tid < TILE) {
     const bool in = t0 + tid < kv.tokens;

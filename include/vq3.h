@@ -457,7 +457,7 @@ VQ3_API int vq3_prompt_attention(const vq3_attn* attn, const vq3_kv_rows* rows, 
  * Queries go to q_out, keys and values to slot slots[t] of the cache as in vq3_kv_append (slots outside the
  * cache are skipped there, their queries are turned all the same). A token with a negative position is left
  * out altogether: its row of q_out and the cache stay. positions and slots are vq3_paged_plan's, for instance.
- * Angles are exact to some 2^-25 of a turn for any position; products in FP32, rounded once.
+ * Angles are exact to some 2^-25 of a turn for any position and |freq| up to 2^40; products in FP32, rounded once.
  * type is that of q, k, v and the cache. rotated: a multiple of 16 up to head_dim. heads 0: no queries, q and
  * q_out unused; otherwise q_out may be q with the same strides (in place) and overlaps nothing else.
  * The pages name no rotation: this library's, as the calls around it.
