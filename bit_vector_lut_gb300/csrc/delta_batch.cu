@@ -32,17 +32,19 @@ namespace {
 // Three producer warps take turns with the chunks: they copy K and Q, form T and M, which do not depend on
 // the state, and hand them over through a ring of three stages (named barriers, no spinning).
 //
-// Numbers: the tensor cores multiply FP16. K and Q enter exactly (BF16 rows are brought to a largest
-// entry of 2^14 by a power of two, which the factors of the token take back). Every FP32 operand (S, R, U,
+// Numbers: the tensor cores multiply FP16. K and Q enter exactly (BF16 rows are brought to a largest entry of 2^14
+// by a power of two, which the factors of the token take back: exact down to 2^-31 of the largest entry, smaller ones
+// lose bits to FP16's subnormals, 2^-39 of the largest at most). Every FP32 operand (S, R, U,
 // T, M) enters as two FP16 parts, hi and what hi leaves, scaled by a power of two per row of the product
 // so that neither part leaves FP16's range: some 22 bits, for either type: a BF16 output made from hi
 // alone (11 bits) may be rounded the other way (one prompt of 8,192 tokens: 670 us instead of 720).
 //
 // mma.sync: a state of 256 x 128 with its two parts, the chunk's products and [K; Q] K^T would take 768 of the 512
-// columns of tensor memory. (d_k = 128, which the wide kernel takes: 16 ragged prompts 415 us here, 321 us there; one
-// prompt of 8,192 tokens 648 us at 96 CTAs here, 695 us at 48 there.) Three producers, as many as stages: one prompt of
-// 1,024 tokens, 48 heads of 256 x 128, 139 us, with two 148 us: a chunk's T and M take a warp as long as two chunks of
-// the consumers.
+// columns of tensor memory. (d_k = 128, before BF16 outputs took both parts: 16 ragged prompts 415 us here, 321 by the
+// wide kernel; one prompt of 8,192 tokens 648 us here, whose 96 CTAs fill more SMs, 668 there: not worth a
+// second kernel for one case that is as fast.) One prompt of 1,024 tokens, 48 heads of 256 x 128, BF16: 155 us (139 with
+// outputs from hi alone and no look at the values' range; then 148 with two producers: a chunk's T and M take a warp as
+// long as two chunks of the consumers). A chunk gone through token by token: some 36 us.
 constexpr int kConsumers = 4, kProducers = 3, kStages = 3;
 constexpr int kChunkThreads = 32 * (kConsumers + kProducers);
 constexpr int kWarpCols = 16, kCtaCols = kWarpCols * kConsumers;
@@ -679,10 +681,10 @@ cudaError_t launch_chunk(const DeltaArgs& a, cudaStream_t st) {
 // transposed by movmatrix, K's part of the state's product. The order of d_k within a product is free: a lane loads 16
 // bytes of a row, two pairs of entries for each of two steps, and the state's rows follow (block_row). N goes through
 // 64 floats of shared memory to lanes that each solve for a column of T. 16 requests x 8 tokens, 48 heads of 128 x 128:
-// 27.2 us (57% of a copy's rate), some 1,500 instructions a warp at three warps a scheduler; 28.8 us as chunks of 8 whose
-// T and M two warps made for four; 29.0 us with four warps a scheduler, which spill; 27.0 us, but 5.0 instead of 4.6 for
-// one request, with the next task's state on its way into shared memory; 41 us in FP32 on CUDA cores, bound by the reads
-// of k and q from shared memory.
+// 27.9 us (56% of a copy's rate), some 1,550 instructions a warp at three warps a scheduler. When it took 27.2: 28.8 us as
+// chunks of 8 whose T and M two warps made for four; 29.0 us with four warps a scheduler, which spill; 27.0 us, but 5.0
+// instead of 4.6 for one request, with the next task's state on its way into shared memory; 41 us in FP32 on CUDA cores,
+// bound by the reads of k and q from shared memory.
 constexpr int kBlockTokens = 8, kBlockThreads = 128;
 
 template <bool BF16>

@@ -19,12 +19,14 @@
 // has to be known before dS is: it is made from a bound, |g_C| max |S| + sum |u w| max |k|, which is some 2^5 above
 // what comes out and leaves 17 bits of FP16's range below it. A chunk with values that cannot share a power of two
 // (kRange, kGrown) goes on as it is, but its dS and its output are not used: the state's warps, whose S is still the
-// chunk's first, step through its tokens in FP32.
-// Bound by that chain and by the row warps, which are both busy some 10,400 cycles a chunk, a third of them waiting for
-// products of 50 to 70 cycles for 128 x 64 x 16 (32 where they have the SM to themselves): 5.3 us a chunk of 64 tokens,
+// chunk's first, step through its tokens in FP32: 74 us instead of 5.8. Looking for such values costs the others 3% (the
+// loop over R under the wait for U).
+// Bound by that chain and by the row warps, which are both busy some 11,000 cycles a chunk, a third of them waiting for
+// products of 50 to 70 cycles for 128 x 64 x 16 (32 where they have the SM to themselves): 5.8 us a chunk of 64 tokens,
 // 0.75 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.34 ms for 16 of 1 to 1,100 tokens.
-// (Without the copying warp, with code of 165 KB: 1,622 and 611 us. The output by the state's warps while U is made:
-// the same for one prompt, 336 us for 16. The output's copies by the copying warp: 728 us.)
+// (When both took 0.67 and 0.32 ms, with BF16 outputs from 11 bits: without the copying warp, with code of 165 KB, 1,622
+// and 611 us; the output by the state's warps while U is made: the same for one prompt, 336 us for 16; the output's
+// copies by the copying warp: 728 us.)
 // All waits are bounded: one that runs out ends the CTA's work and sets the caller's status word, or the device's.
 #include "vq3_internal.h"
 
@@ -40,8 +42,8 @@ namespace {
 
 constexpr int kC = 64;           // tokens of a chunk
 constexpr int kCols = 128;       // columns of a CTA
-// Tokens up to which a request is stepped through instead (16 requests of 48 heads, one request: 5 tokens 71, 10.5 us
-// against 85, 14.2; 6 tokens 80, 12.1 against 85, 14.2; 8 tokens 97, 14.7 against 86, 14.2).
+// Tokens up to which a request is stepped through instead (16 requests of 48 heads, one request: 5 tokens 71, 10.4 us
+// against 89, 15.0; 6 tokens 80, 12.0 against 90, 15.2; 8 tokens 96, 14.9 against 90, 15.2).
 constexpr int kStepMost = 6;
 constexpr int kWideThreads = 512;
 constexpr int kRowWarp = 8, kInvWarp = 12, kIssueWarp = 14;

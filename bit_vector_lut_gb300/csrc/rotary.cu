@@ -9,7 +9,7 @@
 //
 // A CTA takes 4 tokens (one where tokens are few), makes their table of (cos, sin) once for all heads, and walks
 // the heads' items: 2 x 16 bytes a thread, both partners of 8 pairs, so that a row may be turned in place. Bound by
-// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 64 us (91% of a copy's rate).
+// HBM: some 16,000 tokens of 32 + 8 heads of 128, BF16, 65 us (90% of a copy's rate).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

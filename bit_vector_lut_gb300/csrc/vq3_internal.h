@@ -343,10 +343,11 @@ struct DeltaArgs {
   int tokens, requests, slots, v_heads, group, d_k, d_v, max_new;
   float scale;
 };
-// max_new up to which the kernels of few tokens run. 48 heads of 128 x 128, 16 requests (1 request), us, single tokens |
-// blocks: 2 tokens 20.3 (3.4) | 26.6 (4.3), 3 tokens 23.2 (4.1) | 26.8 (4.3), 4 tokens 25.8 (5.0) | 27.0 (4.5); blocks |
-// prompts: 24 tokens 49 (8.2) | 87 (14.4), 32 tokens 63 (10.0) | 86 (13.8), 48 tokens 91 (13.7) | 88 (14.3). d_k = 256:
-// 24 tokens 105 (14.0) | 131 (13.0), 32 tokens 131 (17.0) | 132 (13.0).
+// max_new up to which the kernels of few tokens run. 48 heads of 128 x 128, BF16, 16 requests (1 request), us, single
+// tokens | blocks: 2 tokens 20.4 (3.5) | 27.0 (4.4), 3 tokens 23.1 (4.1) | 27.2 (4.3), 4 tokens 25.9 (5.1) | 27.2 (4.6);
+// blocks | prompts: 24 tokens 52 (8.5) | 92 (15.3), 32 tokens 65 (10.3) | 91 (14.9), 48 tokens 94 (14.1) | 93 (15.1).
+// d_k = 256: 16 tokens 88 (12.4) | 137 (13.6), 24 tokens 116 (16.2) | 139 (13.8), 32 tokens 144 (20.0) | 141 (13.9): 24 is
+// the batch's; one request alone would go over at 16. (d_k = 64 takes those of 128, not measured.)
 constexpr int kDeltaStepTokens = 3, kDeltaBlockTokens = 32, kDeltaBlockTokens256 = 24;
 cudaError_t launch_delta_batch(const DeltaArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_delta_wide(const DeltaArgs& a, bool bf16, cudaStream_t st);  // d_k 64 or 128

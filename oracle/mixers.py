@@ -39,11 +39,14 @@ def delta(q, k, v, beta, alpha, state, scale):
 
 
 def delta_bound(out, info, v, scale, dtype, q):
-    """Tolerances (out [T, dv], state per column [dv]).
+    """Tolerances (out [T, dv], state per column [dv]). They take in what a token cannot see (the largest value of all
+    tokens, the longest that a state column has been): for values of like size. delta_causal's are the narrower ones.
 
     FP32 operands enter the products with 22 bits or more (half a step 2^-22), sums of FP32: each of a token's
-    four products leaves up to 2^-21 of the column's length and value. BF16 outputs take their products from
-    11-bit operands (half a step 2^-11), one with the state and two with the chunk's own tokens."""
+    four products leaves up to 2^-21 of the column's length and value. For BF16 outputs there is room for products
+    of 11-bit operands (half a step 2^-11), one with the state and two with the last WINDOW tokens: more than kernels
+    need that take 22 bits for either type. And the sizes are those of all tokens, later ones among them, and of a
+    column at its longest: delta_causal has the bound of what a token can see."""
     T = max(1, out.shape[0])
     size = info["top"] + np.abs(v).max(axis=0, initial=0)
     tol_state = 4 * 2.0**-21 * (1 + np.sqrt(T)) * size
