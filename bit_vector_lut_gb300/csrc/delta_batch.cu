@@ -373,12 +373,12 @@ __device__ __forceinline__ void warp_steps(const DeltaArgs& a, int h, long long 
   }
 }
 // Least of a column's sizes over the lanes that share it.
-__device__ __forceinline__ unsigned seen_least(unsigned m) {
-  m = min(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return min(m, __shfl_xor_sync(0xffffffffu, m, 2));
+__device__ __forceinline__ float seen_least(float m) {
+  m = fminf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fminf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
-// The least that a token's R finds in its two columns, from `size` on and with earlier tokens' as the gates leave them:
-// for the few chunks that the least value alone would have gone through again (a small one behind large ones).
+// The least that a token finds in its two columns, from `size` on and with earlier tokens' R as the gates leave them
+// (nothing at all needs no bits): for the few chunks whose least R alone, or a zero, would have had them gone through again.
 template <int NB, class Gate>
 __device__ __forceinline__ float2 least_found(const float (&r)[NB][4], float2 size, Gate gate) {
   const int quad = threadIdx.x & 28;
@@ -391,8 +391,8 @@ __device__ __forceinline__ float2 least_found(const float (&r)[NB][4], float2 si
       const float y1 = fabsf(__shfl_sync(0xffffffffu, r[n][2 + (i & 1)], quad + i / 2));
       const float a = fabsf(gate(8 * n + i));
       size = make_float2(fmaxf(a * size.x, y0), fmaxf(a * size.y, y1));
-      if (y0 != 0.f) least.x = fminf(least.x, size.x);
-      if (y1 != 0.f) least.y = fminf(least.y, size.y);
+      if (size.x > 0.f) least.x = fminf(least.x, size.x);
+      if (size.y > 0.f) least.y = fminf(least.y, size.y);
     }
   return least;
 }
@@ -400,7 +400,7 @@ __device__ __forceinline__ float2 least_found(const float (&r)[NB][4], float2 si
 // ---- consumer: one chunk against this warp's 16 columns; acc: S^T, row g column 2g, row g + 8 column 2g + 1.
 // False, with S as it was: the chunk has to be gone through token by token.
 template <bool BF16>
-__device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int warp,
+__device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned char* st, float (&o)[NN][4], int nt, int warp,
                                         int lane) {
   using L = Stage;
   constexpr int C = L::C, RS = L::RS, TS = L::TS;
@@ -450,7 +450,7 @@ __device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned 
     }
   // R^T = V^T - X_K, times the factor of T's column
   const unsigned char* sv = st + L::kV + ((2 * t) * L::VS + warp * kWarpCols + 2 * g) * 2;
-  unsigned seen0 = ~0u, seen1 = ~0u;
+  float seen0 = INFINITY, seen1 = INFINITY;  // of the request's tokens
 #pragma unroll
   for (int n = 0; n < NN; ++n) {
     const float2 fv = *reinterpret_cast<const float2*>(f + L::kFv + 8 * n + 2 * t);
@@ -461,8 +461,14 @@ __device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned 
     xk[n][1] = vb.x * fv.y - fk.y * xk[n][1];
     xk[n][2] = va.y * fv.x - fk.x * xk[n][2];
     xk[n][3] = vb.y * fv.y - fk.y * xk[n][3];
-    seen0 = min(seen0, min(seen_of(fmaxf(fabsf(va.x * fv.x), fabsf(xk[n][0]))), seen_of(fmaxf(fabsf(vb.x * fv.y), fabsf(xk[n][1])))));
-    seen1 = min(seen1, min(seen_of(fmaxf(fabsf(va.y * fv.x), fabsf(xk[n][2]))), seen_of(fmaxf(fabsf(vb.y * fv.y), fabsf(xk[n][3])))));
+    if (8 * n + 2 * t < nt) {
+      seen0 = fminf(seen0, fmaxf(fabsf(va.x * fv.x), fabsf(xk[n][0])));
+      seen1 = fminf(seen1, fmaxf(fabsf(va.y * fv.x), fabsf(xk[n][2])));
+    }
+    if (8 * n + 2 * t + 1 < nt) {
+      seen0 = fminf(seen0, fmaxf(fabsf(vb.x * fv.y), fabsf(xk[n][1])));
+      seen1 = fminf(seen1, fmaxf(fabsf(vb.y * fv.y), fabsf(xk[n][3])));
+    }
   }
   seen0 = seen_least(seen0);
   seen1 = seen_least(seen1);
@@ -509,7 +515,7 @@ __device__ __forceinline__ bool consume(float (&acc)[2 * KS][4], const unsigned 
     // (R and what it comes from have T's factor of 2^-14)
     if (__any_sync(0xffffffffu, !(all < INFINITY)) || f[L::kFt] != 0.f) return false;
     const float need0 = fmaxf(top0, 0x1p-14f * um0) * kRange, need1 = fmaxf(top1, 0x1p-14f * um1) * kRange;
-    if (__any_sync(0xffffffffu, need0 > seen_back(seen0) || need1 > seen_back(seen1))) {
+    if (__any_sync(0xffffffffu, need0 > seen0 || need1 > seen1)) {
       const float2 least = least_found<NN>(xk, make_float2(0x1p-17f * m0, 0x1p-17f * m1), [f](int i) { return f[L::kFa + i]; });
       if (__any_sync(0xffffffffu, need0 > least.x || need1 > least.y)) return false;
     }
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     const int s = c % kStages;
     bar_sync(kFullBar + s * kConsumers + warp, kFullThreads);
     float o[NN][4];
-    const bool done = on && consume<BF16>(acc, smem + s * L::kBytes, o, warp, lane);
+    const bool done = on && consume<BF16>(acc, smem + s * L::kBytes, o, rq.n - c * C, warp, lane);
     if (c + kStages < chunks) bar_arrive(kEmptyBar + s, kEmptyThreads);
     if (on && !done) {
       warp_steps<2 * KS, BF16>(a, h, rq.first + c * C, min(rq.n - c * C, C), col, acc, [t](int n, int e) { return 8 * n + 2 * t + e; });
@@ -861,11 +867,12 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
       xk[0][3] = vb.y - g1 * kb1 * (s1.back * xk[0][3]);
     }
     uint32_t hi[4], lo[4];
-    unsigned seen0, seen1;
+    float seen0, seen1;
     {
       const float2 va = delta_unpack2<BF16>(vw[0]), vb = delta_unpack2<BF16>(vw[1]);
-      seen0 = seen_least(min(seen_of(fmaxf(fabsf(va.x), fabsf(xk[0][0]))), seen_of(fmaxf(fabsf(vb.x), fabsf(xk[0][1])))));
-      seen1 = seen_least(min(seen_of(fmaxf(fabsf(va.y), fabsf(xk[0][2]))), seen_of(fmaxf(fabsf(vb.y), fabsf(xk[0][3])))));
+      const float a0 = 2 * t < nt ? 0.f : INFINITY, b0 = 2 * t + 1 < nt ? 0.f : INFINITY;  // tokens past the last count for nothing
+      seen0 = seen_least(fminf(fmaxf(fmaxf(fabsf(va.x), fabsf(xk[0][0])), a0), fmaxf(fmaxf(fabsf(vb.x), fabsf(xk[0][1])), b0)));
+      seen1 = seen_least(fminf(fmaxf(fmaxf(fabsf(va.y), fabsf(xk[0][2])), a0), fmaxf(fmaxf(fabsf(vb.y), fabsf(xk[0][3])), b0)));
     }
     row_max<1>(xk, top0, top1);
     const Scale r0 = scale_of(top0), r1 = scale_of(top1);
@@ -884,7 +891,7 @@ __global__ void __launch_bounds__(kBlockThreads, KS <= 8 ? 3 : 2) delta_block_ke
       row_max<1>(u, um0, um1);
       const float need0 = fmaxf(top0, um0) * kRange, need1 = fmaxf(top1, um1) * kRange;
       bool lost = __any_sync(0xffffffffu, !(fabsf(u[0][0]) + fabsf(u[0][1]) + fabsf(u[0][2]) + fabsf(u[0][3]) < INFINITY));
-      if (__any_sync(0xffffffffu, need0 > seen_back(seen0) || need1 > seen_back(seen1))) {
+      if (__any_sync(0xffffffffu, need0 > seen0 || need1 > seen1)) {
         const float2 least = least_found<1>(xk, size, [al](int i) { return __shfl_sync(0xffffffffu, al, i); });
         lost |= __any_sync(0xffffffffu, need0 > least.x || need1 > least.y) != 0;
       }

@@ -65,18 +65,14 @@ __device__ __forceinline__ Scale scale_of(float m) {
 }
 // Where tokens of a chunk share a power of two, what a token adds has to be seen beside what its column holds already (of
 // the values, the state and earlier tokens, as the gates leave them), or tokens behind it, which it cannot see, cost it
-// its bits; and matrix products bring infinities and NaN of later tokens to earlier ones as 0 * inf. So a chunk is
-// gone through again token by token where a column has a value of 2^20 times that size, or one that is not
-// finite: what shares a power of two is right to 2^-19 of what the token sees. Seldom: not for values of like size, nor for
-// small ones behind large ones.
+// its bits (T's and M's entries share one, too: nothing new behind a small gate is as bad as something small);
+// and matrix products bring infinities and NaN of later tokens to earlier ones as 0 * inf. So a chunk is gone through again
+// token by token where R or U has a value of 2^20 times that size, or one that is not finite: each is right to 2^-19 of what
+// the token sees. Seldom: not for values of like size, nor for small ones behind large ones.
 constexpr float kRange = 0x1p-20f;
 // Entries of T = (I + N)^-1 are below this for keys and strengths that do not let the state grow; its columns share
 // a power of two, too.
 constexpr float kGrown = 4.f;
-// m >= 0 as a number whose least over several leaves zeros out (they need no bits), and back.
-__device__ __forceinline__ unsigned seen_of(float m) { return __float_as_uint(m) - 1u; }
-__device__ __forceinline__ float seen_back(unsigned m) { return __uint_as_float(m + 1u); }
-
 // Two FP32 operations an instruction.
 __device__ __forceinline__ unsigned long long pair_bits(float2 x) {
   unsigned long long r;

@@ -19,11 +19,11 @@
 // has to be known before dS is: it is made from a bound, |g_C| max |S| + sum |u w| max |k|, which is some 2^5 above
 // what comes out and leaves 17 bits of FP16's range below it. A chunk with values that cannot share a power of two
 // (kRange, kGrown) goes on as it is, but its dS and its output are not used: the state's warps, whose S is still the
-// chunk's first, step through its tokens in FP32: 74 us instead of 5.8. Looking for such values costs the others 3% (the
+// chunk's first, step through its tokens in FP32: 74 us instead of 5.8. Looking for such values costs the others 4 to 6% (the
 // loop over R under the wait for U).
 // Bound by that chain and by the row warps, which are both busy some 11,000 cycles a chunk, a third of them waiting for
 // products of 50 to 70 cycles for 128 x 64 x 16 (32 where they have the SM to themselves): 5.8 us a chunk of 64 tokens,
-// 0.75 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.34 ms for 16 of 1 to 1,100 tokens.
+// 0.77 ms for one prompt of 8,192 tokens (48 heads of 128 x 128, BF16, 48 CTAs), 0.34 ms for 16 of 1 to 1,100 tokens.
 // (When both took 0.67 and 0.32 ms, with BF16 outputs from 11 bits: without the copying warp, with code of 165 KB, 1,622
 // and 611 us; the output by the state's warps while U is made: the same for one prompt, 336 us for 16; the output's
 // copies by the copying warp: 728 us.)
@@ -430,15 +430,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           top = max_pair(top, y);
         }
       }
-      // with S's largest entry, rounded up to 16 bits, what the half's last tokens leave to the next one
-      const float last = fmaxf(fabsf(r[15].y), fabsf(f[L::kFa + 32 * hf + 31] * r[15].x));
-      const uint32_t mS16 = (__float_as_uint(mS) + 0xffffu) & 0xffff0000u;
-      x1[hf * 128 + c] = make_float2(top, __uint_as_float(mS16 | __float_as_uint(last) >> 16));
+      x1[hf * 128 + c] = make_float2(top, mS);
       pair_sync();
       const float2 o1 = x1[(hf ^ 1) * 128 + c];
       const float topr = fmaxf(top, o1.x);
       const Scale rs = scale_of(topr);
-      const float mS_all = __uint_as_float(max(mS16, __float_as_uint(o1.y) & 0xffff0000u));
+      const float mS_all = fmaxf(mS, o1.y);
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) split2(mul_pair(r[e], rs.to), hi[e], lo[e]);
@@ -450,23 +447,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       tmem_st16(tm + kTmR + 32u + 16u * hf, lo);
       tc_wait_st();
       arrive(kbR);
-      // (under U) the least that a token's R finds in its column, from the state on; with T's factor, as R
-      float least = INFINITY;
-      {
-        // (BF16: k's factor is 2^-14 of its largest entry); the second half also goes on from the last tokens of the first
-        float size = mS_all * fabsf(f[L::kFk + 32 * hf]) * (BF16 ? 0x1p11f : 0x1p-3f);
-        if (hf) size = fmaxf(size, __uint_as_float(__float_as_uint(o1.y) << 16));
+      // (under U) the least that a token of this half finds in its column, its own R with it: from the state on in the first
+      // half (with T's factor of 2^-14, as R, and less, for keys that are no unit vectors)
+      const float need = topr * (4.f * kRange);
+      float found = hf ? 0.f : 0x1p-17f * mS_all, least = INFINITY, worst = INFINITY;
+      const auto scan = [&](auto each) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 fa = *reinterpret_cast<const float4*>(f + L::kFa + 32 * hf + j);
           const float av[4] = {fa.x, fa.y, fa.z, fa.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float y = e & 1 ? r[(j + e) / 2].y : r[(j + e) / 2].x;
-            size = fmaxf(fabsf(av[e] * size), fabsf(y));
-            if (y != 0.f) least = fminf(least, size);
+            found = fmaxf(fabsf(av[e] * found), fabsf(e & 1 ? r[(j + e) / 2].y : r[(j + e) / 2].x));
+            each(av[e]);
           }
         }
+      };
+      scan([&](float) { least = fminf(least, found); });
+      if (hf && __any_sync(0xffffffffu, least < need)) {  // what the gates up to such a token leave of the first half's
+        float kept = 1.f;
+        found = 0.f;
+        scan([&](float a) {
+          kept *= a;
+          if (found < need) worst = fminf(worst, fabsf(kept));
+        });
       }
       // U^T, as it is for the output and times w for dS
       wait(kbU, ch);
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
           l1 = fmaf(fabsf(w.x), e ? km.z : km.x, fmaf(fabsf(w.y), e ? km.w : km.y, l1));
         }
       }
-      x2[hf * 128 + c] = make_float4(topu, top, l1, least);
+      x2[hf * 128 + c] = make_float4(topu, top, l1, found);
       pair_sync();
       const float4 o2 = x2[(hf ^ 1) * 128 + c];
       const Scale us = scale_of(fmaxf(topu, o2.x));
@@ -498,8 +502,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) delta_wide_kernel(const __gri
       if (hf == 0) reinterpret_cast<float2*>(smem + L::kXO)[(ch & 1) * 128 + c] = make_float2(ss.back, us.back);
       ss = scale_of(fabsf(gC) * mS_all + (l1 + o2.z));
       {
-        // (l1 is not finite if a U is not)
-        const bool lost = !(l1 + o2.z < INFINITY) || fmaxf(topr, 0x1p-14f * fmaxf(topu, o2.x)) * kRange > fminf(least, o2.w);
+        // (l1 is not finite if a U is not; U is up to twice R, whose factor of T is 2^-14 or 2^-13)
+        const bool lost = !(l1 + o2.z < INFINITY) || 0x1p-14f * fmaxf(topu, o2.x) > 4.f * topr ||
+                          (hf ? worst < INFINITY && o2.w * worst < need : least < need);
         if (__any_sync(0xffffffffu, lost) && lane == 0) again[ch & 3] = ch + 1;
       }
 #pragma unroll

@@ -505,15 +505,15 @@ typedef struct vq3_batch {
  * The gated delta rule, as vq3_delta_rule_forward: per value head h and token t, with the query/key head
  * h / (v_heads / qk_heads),
  *   S <- alpha[t][h] S + beta[t][h] k_t (v_t - alpha[t][h] S^T k_t)^T,   out_t = scale S^T q_t.
- * States, sums and gates are FP32, out is rounded once. Products take FP32 values with 22 bits; a token's values
- * may be off by 2^-19 of the largest that it finds in its column of the state, from that token and those before it, as
- * the gates leave them. No token depends on a later one: a chunk (of 8 to 64 tokens) is gone through token by token, some
- * ten times as slowly, if a column's values in it lie further apart than 2^20, if one is not finite, or if keys are
- * longer than their strengths allow (entries of (I + N)^-1 of 4 and more). alpha may be 0 (the state starts over). Rows outside the requests count for nothing and are left as they are. All lengths
- * live in device memory. max_new picks the kernel (up to 3: one that streams the states token by token; up to 32, or 24
- * of d_k = 256: blocks of 8 tokens; above or 0: prompts by chunks, where d_k 64 and 128 take requests of up to 6 tokens
- * token by token, and d_k 256 any as chunks of 32); a wrong value costs time, not correctness. Deterministic, no
- * workspace, one launch.
+ * States, sums and gates are FP32, out is rounded once. Products take FP32 values with 22 bits; a token's values may be
+ * off by 2^-18 of the largest that it finds in its column of the state, from that token and those before it, as the
+ * gates leave them. No token depends on a later one: a chunk (of 8 to 64 tokens) is gone through token by token, some
+ * ten times as slowly, if a token finds less than 2^-18 of a column's largest value in it, if one is not finite, or if
+ * keys are longer than their strengths allow (entries of (I + N)^-1 of 4 and more). alpha may be 0 (the state starts
+ * over). Rows outside the requests count for nothing and are left as they are. All lengths live in device memory.
+ * max_new picks the kernel (up to 3: one that streams the states token by token; up to 32, or 24 of d_k = 256: blocks
+ * of 8 tokens; above or 0: prompts by chunks, where d_k 64 and 128 take requests of up to 6 tokens token by token, and
+ * d_k 256 any as chunks of 32); a wrong value costs time, not correctness. Deterministic, no workspace, one launch.
  * d_k 64, 128 or 256; d_v a multiple of 16 up to 4096. Strides as in the attention calls; alpha and beta have
  * their heads side by side. out and states overlap no other buffer.
  * Errors: VQ3_EINVAL, VQ3_EALIGN, VQ3_EUNSUPPORTED, VQ3_ECUDA.
